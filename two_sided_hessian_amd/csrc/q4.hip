@@ -1,0 +1,300 @@
+// q4.hip -- 4-bit layers: packing, the linear layer and its input gradient.
+#include <algorithm>
+
+#include "../../include/bakron_q4.h"
+#include "q4.hpp"
+
+namespace bk {
+
+// ------------------------------------------------------------------ packing
+//
+// One thread per 16-byte unit (32 codes of one row).  Reads half of what it
+// writes twice over; bound by HBM, run once per layer.
+__global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ codes, int64_t m, int64_t n, int RT,
+                                                 int KB, int64_t layer_bytes, int64_t unit_at,
+                                                 char* __restrict__ packed)
+{
+    if (blockIdx.x == 0 && threadIdx.x == 0)   // k_q4_pack_grid raises it
+        *reinterpret_cast<float*>(packed + blockIdx.y * layer_bytes + unit_at) = 0.f;
+    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (unit >= (int64_t)RT * KB * 64) return;
+    const int64_t layer = blockIdx.y;
+    const int r = (int)(unit & 15), q = (int)(unit >> 4) & 3;
+    const int64_t block = unit >> 6;
+    const int64_t row = block / KB * kQ4Rows + r;
+    const int64_t col0 = block % KB * kQ4Cols + 16 * q;
+    u32x4 out = {0u, 0u, 0u, 0u};
+    if (row < m) {
+        const uint8_t* src = codes + (layer * m + row) * n;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int64_t c0 = col0 + 64 * (d >> 1) + 8 * (d & 1);
+            uint32_t v = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c0 + e < n) v |= (uint32_t)(src[c0 + e] & 15u) << (4 * (e >> 1) + 16 * (e & 1));
+            out[d] = __builtin_rotateleft32(v, 3);
+        }
+    }
+    reinterpret_cast<u32x4*>(packed + layer * layer_bytes)[unit] = out;
+}
+
+__global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ scale, const float* __restrict__ zero,
+                                                      int64_t m, int RT, int G, int64_t layer_bytes, int64_t grid_at,
+                                                      int64_t unit_at, char* __restrict__ packed)
+{
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t layer = blockIdx.y;
+    const int r = (int)(e & 15);
+    const int64_t row = (e >> 4) / G * kQ4Rows + r, g = (e >> 4) % G;
+    f32x2 v = {0.f, 0.f};
+    if (e < (int64_t)RT * G * kQ4Rows) {
+        if (row < m) {
+            v.x = scale[(layer * m + row) * G + g];
+            v.y = zero[(layer * m + row) * G + g];
+        }
+        reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at)[e] = v;
+    }
+    // the unit: its largest weight's exponent, rounded up (the maximum of
+    // integers does not depend on the order it is taken in)
+    float top = fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y));
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if ((threadIdx.x & 63) == 0 && top > 0.f && top < INFINITY) {
+        const uint32_t exponent = min((__float_as_uint(top) >> 23) + 1u, 254u);
+        atomicMax(reinterpret_cast<unsigned*>(packed + layer * layer_bytes + unit_at), max(exponent, 1u) << 23);
+    }
+}
+
+// ------------------------------------------- the linear layer, a few tokens
+//
+// y (T x m) for one tile of 16 rows of W and 16 NT tokens per workgroup: the
+// waves take the 128-column blocks in turn, tokens are the MFMA's rows and
+// rows of W its columns, so a lane's four accumulators share one (s, z).  A
+// product with ones gives the sums of x beside them.  Joined through LDS in
+// wave order (the result does not depend on timing).
+template <class X, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_q4_few(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
+                                                       uint16_t* __restrict__ y, int64_t ldy)
+{
+    typedef typename X::vec vec;
+    __shared__ float red[WAVES][NT * 4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int q = lane >> 4, r = lane & 15;
+    const int rt = blockIdx.x, t0 = blockIdx.y * 16 * NT;
+    const bool wide = ((reinterpret_cast<uintptr_t>(x) & 15) | (ldx & 7)) == 0;
+    const uint16_t* xr[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) xr[i] = x + (int64_t)min(t0 + 16 * i + r, T - 1) * ldx;
+    const vec ones = q4_ones<X>();
+    f32x4 acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int kb = wave; kb < w.KB; kb += WAVES) {
+        const u32x4 c = w.codes[((int64_t)rt * w.KB + kb) * 64 + lane];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int g = min((2 * kb + h) / w.gb, w.G - 1);
+            const f32x2 sz = w.grid[((int64_t)rt * w.G + g) * 16 + r];
+            const vec w0 = X::codes(c[2 * h]), w1 = X::codes(c[2 * h + 1]);
+            const int k = kb * 128 + 64 * h + 16 * q;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                u32x4 xv[2];
+                q4_load16(xr[i] + k, w.n - k, wide, xv);
+                const vec a0 = __builtin_bit_cast(vec, xv[0]), a1 = __builtin_bit_cast(vec, xv[1]);
+                f32x4 t = {0.f, 0.f, 0.f, 0.f}, s = {0.f, 0.f, 0.f, 0.f};
+                t = X::mfma16(a0, w0, t);
+                s = X::mfma16(a0, ones, s);
+                t = X::mfma16(a1, w1, t);
+                s = X::mfma16(a1, ones, s);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][e] = fmaf(sz.x, fmaf(-(sz.y + kQ4Offset), s[e], t[e]), acc[i][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[wave][4 * i + e][lane] = acc[i][e];
+    __syncthreads();
+    for (int o = threadIdx.x; o < NT * 4 * 64; o += 64 * WAVES) {
+        const int e = o >> 6, l = o & 63;
+        float v = 0.f;
+#pragma unroll
+        for (int u = 0; u < WAVES; ++u) v += red[u][e][l];
+        const int t = t0 + 16 * (e >> 2) + 4 * (l >> 4) + (e & 3), row = rt * 16 + (l & 15);
+        if (t < T && row < w.m) y[(int64_t)t * ldy + row] = X::down(v);
+    }
+}
+
+// ---------------------------------------------------------- input gradient
+//
+// dx[t, j] = sum_i dy[t, i] s_ig (c_ij - z_ig), g the group of column j: one
+// thread per entry, float32.
+template <class X>
+__global__ __launch_bounds__(256) void k_q4_grad(const uint16_t* __restrict__ dy, int64_t lddy, int T, Q4Layer w,
+                                                 uint16_t* __restrict__ dx, int64_t lddx)
+{
+    const int j = blockIdx.x * 64 + (threadIdx.x & 63);
+    const int64_t t = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6);
+    if (j >= w.n || t >= T) return;
+    const int kb = j >> 7, d = (j >> 6 & 1) * 2 + (j >> 3 & 1), q = j >> 4 & 3, e = j & 7;
+    const int shift = 4 * (e >> 1) + 16 * (e & 1);
+    const int g = min((j >> 6) / w.gb, w.G - 1);
+    float acc = 0.f;
+    for (int i = 0; i < w.m; ++i) {
+        const uint32_t c = w.codes[(((int64_t)(i >> 4) * w.KB + kb) * 4 + q) * 16 + (i & 15)][d];
+        const f32x2 sz = w.grid[((int64_t)(i >> 4) * w.G + g) * 16 + (i & 15)];
+        const float v = sz.x * ((float)(__builtin_rotateright32(c, 3 + shift) & 15u) - sz.y);
+        acc = fmaf(X::up(dy[t * lddy + i]), v, acc);
+    }
+    dx[t * lddx + j] = X::down(acc);
+}
+
+// rows x cols zeros of a 2-byte type
+__global__ __launch_bounds__(256) void k_q4_zero(uint16_t* __restrict__ y, int64_t ld, int64_t rows, int64_t cols)
+{
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e < rows * cols) y[e / cols * ld + e % cols] = 0;
+}
+
+int q4_zero_enqueue(void* y, int64_t ld, int64_t rows, int64_t cols, hipStream_t s)
+{
+    launch(nullptr, KK_Q4_ZERO, 0.0, 2.0 * rows * cols, k_q4_zero, dim3((unsigned)ceil_div(rows * cols, 256)), dim3(256),
+           s, static_cast<uint16_t*>(y), ld, rows, cols);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <class X>
+static void few_enqueue(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, void* y, int64_t ldy, hipStream_t s)
+{
+    const uint16_t* xp = static_cast<const uint16_t*>(x);
+    uint16_t* yp = static_cast<uint16_t*>(y);
+    // grid.y holds at most 65535 token blocks
+    for (int64_t t0 = 0; t0 < T; t0 += 65535 * 16) {
+        const int64_t tn = std::min<int64_t>(T - t0, 65535 * 16);
+        launch(nullptr, KK_Q4_FEW, 2.0 * tn * w.m * w.n, 0.0, k_q4_few<X, 1, 8>,
+               dim3((unsigned)w.RT, (unsigned)ceil_div(tn, 16)), dim3(512), s, xp + t0 * ldx, ldx, (int)tn, w,
+               yp + t0 * ldy, ldy);
+    }
+}
+
+template <class X>
+static void grad_enqueue(const void* dy, int64_t lddy, int64_t T, const Q4Layer& w, void* dx, int64_t lddx,
+                         hipStream_t s)
+{
+    const uint16_t* yp = static_cast<const uint16_t*>(dy);
+    uint16_t* xp = static_cast<uint16_t*>(dx);
+    for (int64_t t0 = 0; t0 < T; t0 += 65535 * 4) {
+        const int64_t tn = std::min<int64_t>(T - t0, 65535 * 4);
+        launch(nullptr, KK_Q4_GRAD, 2.0 * tn * w.m * w.n, 0.0, k_q4_grad<X>,
+               dim3((unsigned)ceil_div(w.n, 64), (unsigned)ceil_div(tn, 4)), dim3(256), s, yp + t0 * lddy, lddy, (int)tn,
+               w, xp + t0 * lddx, lddx);
+    }
+}
+
+}  // namespace bk
+
+// ------------------------------------------------------------------- C ABI
+
+static bool q4_shape_ok(int64_t m, int64_t n)
+{
+    return m >= 0 && n >= 0 && m <= BAKRON_MAX_DIM && n <= BAKRON_MAX_DIM;
+}
+
+static bool q4_group_ok(int64_t g) { return g >= 0 && g % 64 == 0; }
+
+extern "C" {
+
+size_t bakron_q4_packed_bytes(int64_t count, int64_t m, int64_t n, int64_t group_size)
+{
+    if (!q4_shape_ok(m, n) || !q4_group_ok(group_size) || count < 0 || count > BAKRON_Q4_MAX_LAYERS) return 0;
+    if (m == 0 || n == 0) return 0;
+    return (size_t)count * bk::q4_dims(m, n, group_size).bytes;
+}
+
+int bakron_q4_pack(const uint8_t* codes, const float* scale, const float* zero, int64_t count, int64_t m, int64_t n,
+                   int64_t group_size, void* packed, hipStream_t stream)
+{
+    if (!q4_shape_ok(m, n) || count < 0 || count > BAKRON_Q4_MAX_LAYERS) return BAKRON_ERR_BAD_SIZE;
+    if (!q4_group_ok(group_size)) return BAKRON_ERR_BAD_ARG;
+    if (m == 0 || n == 0 || count == 0) return BAKRON_SUCCESS;
+    if (!codes || !scale || !zero || !packed) return BAKRON_ERR_NULL_POINTER;
+    if (reinterpret_cast<uintptr_t>(packed) % bk::kAlign) return BAKRON_ERR_BAD_ARG;
+    const bk::Q4Dims d = bk::q4_dims(m, n, group_size);
+    char* out = static_cast<char*>(packed);
+    const double mn = (double)count * m * n;
+    bk::launch(nullptr, bk::KK_Q4_PACK, 0.0, 1.5 * mn, bk::k_q4_pack,
+               dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.KB * 64, 256), (unsigned)count), dim3(256), stream, codes,
+               m, n, d.RT, d.KB, (int64_t)d.bytes, (int64_t)d.unit_at, out);
+    bk::launch(nullptr, bk::KK_Q4_PACK_GRID, 0.0, 16.0 * count * m * d.G, bk::k_q4_pack_grid,
+               dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.G * 16, 256), (unsigned)count), dim3(256), stream, scale,
+               zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
+    return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
+}
+
+// The argument checks that the layer and its gradient share: `in` rows of
+// `in_cols` values, `out` rows of `out_cols`.  1: nothing to do, 2: zeros.
+static int check_q4(const void* in, int64_t ldin, int64_t in_cols, int64_t tokens, int32_t type, const void* packed,
+                    int64_t m, int64_t n, int64_t group_size, const void* out, int64_t ldout, int64_t out_cols,
+                    const void* ws, size_t ws_bytes, size_t need)
+{
+    if (!q4_shape_ok(m, n) || tokens < 0 || tokens > BAKRON_Q4_MAX_TOKENS) return BAKRON_ERR_BAD_SIZE;
+    if (!q4_group_ok(group_size) || (type != BAKRON_Q4_BF16 && type != BAKRON_Q4_FP16)) return BAKRON_ERR_BAD_ARG;
+    if (ldin < in_cols || ldout < out_cols || ldin >= ((int64_t)1 << 32) || ldout >= ((int64_t)1 << 32))
+        return BAKRON_ERR_BAD_ARG;
+    if (out_cols == 0 || tokens == 0) return 1;
+    if (!out) return BAKRON_ERR_NULL_POINTER;
+    if (reinterpret_cast<uintptr_t>(out) & 1) return BAKRON_ERR_BAD_ARG;
+    if (in_cols == 0) return 2;
+    if (!in || !packed) return BAKRON_ERR_NULL_POINTER;
+    if ((reinterpret_cast<uintptr_t>(in) & 1) || reinterpret_cast<uintptr_t>(packed) % bk::kAlign)
+        return BAKRON_ERR_BAD_ARG;
+    if (need && (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % bk::kAlign)) return BAKRON_ERR_WORKSPACE;
+    return BAKRON_SUCCESS;
+}
+
+size_t bakron_q4_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int64_t group_size)
+{
+    (void)tokens, (void)m, (void)n, (void)group_size;
+    return 0;
+}
+
+int bakron_q4_linear(const void* x, int64_t ldx, int64_t tokens, int32_t type, const void* packed, int64_t m, int64_t n,
+                     int64_t group_size, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream)
+{
+    const int c = check_q4(x, ldx, n, tokens, type, packed, m, n, group_size, y, ldy, m, workspace, workspace_bytes,
+                           bakron_q4_linear_workspace_bytes(tokens, m, n, group_size));
+    if (c < 0) return c;
+    if (c == 1) return BAKRON_SUCCESS;
+    if (c == 2) return bk::q4_zero_enqueue(y, ldy, tokens, m, stream) ? BAKRON_ERR_HIP : BAKRON_SUCCESS;
+    const bk::Q4Layer w = bk::q4_layer(packed, bk::q4_dims(m, n, group_size));
+    if (type == BAKRON_Q4_BF16) bk::few_enqueue<bk::Bf16>(x, ldx, tokens, w, y, ldy, stream);
+    else bk::few_enqueue<bk::Fp16>(x, ldx, tokens, w, y, ldy, stream);
+    return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
+}
+
+size_t bakron_q4_linear_grad_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int64_t group_size)
+{
+    (void)tokens, (void)m, (void)n, (void)group_size;
+    return 0;
+}
+
+int bakron_q4_linear_grad(const void* dy, int64_t lddy, int64_t tokens, int32_t type, const void* packed, int64_t m,
+                          int64_t n, int64_t group_size, void* dx, int64_t lddx, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream)
+{
+    const int c = check_q4(dy, lddy, m, tokens, type, packed, m, n, group_size, dx, lddx, n, workspace, workspace_bytes,
+                           bakron_q4_linear_grad_workspace_bytes(tokens, m, n, group_size));
+    if (c < 0) return c;
+    if (c == 1) return BAKRON_SUCCESS;
+    if (c == 2) return bk::q4_zero_enqueue(dx, lddx, tokens, n, stream) ? BAKRON_ERR_HIP : BAKRON_SUCCESS;
+    const bk::Q4Layer w = bk::q4_layer(packed, bk::q4_dims(m, n, group_size));
+    if (type == BAKRON_Q4_BF16) bk::grad_enqueue<bk::Bf16>(dy, lddy, tokens, w, dx, lddx, stream);
+    else bk::grad_enqueue<bk::Fp16>(dy, lddy, tokens, w, dx, lddx, stream);
+    return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,173 @@
+// q4.hpp -- packed 4-bit layers: the layout and the device pieces that the
+// q4 kernels share (gfx950).
+//
+// Layout of one packed layer (m x n, RT = ceil(m / 16) row tiles, KB =
+// ceil(n / 128) column blocks, G grids per row):
+//   codes: RT x KB blocks of 1 KB, each 16 rows x 128 columns, as 64 units of
+//          16 bytes; unit u = 16 q + r belongs to row r of the tile and holds
+//          four dwords d of 8 columns each,
+//              column = 64 (d >> 1) + 16 q + 8 (d & 1) + e,  e = 0 .. 7,
+//          so lane u of a wave loads a unit, a wave instruction one block, and
+//          dword pair d = 0, 1 (2, 3) of all units is the block's first (last)
+//          64 columns: a group of 64 columns never shares an MFMA with the
+//          next.  A 16 x 16 x 32 MFMA takes dword d of lane (q, r) as its
+//          fragment; a 32 x 32 x 16 one takes two tiles and units q, q + 2.
+//   dword: column pair p (e = 2p, 2p + 1) has its codes in bits 4p .. 4p + 3
+//          and 16 + 4p .. 16 + 4p + 3, and the whole is rotated left by 3,
+//          which puts pair 0 where a bfloat16's mantissa wants it.
+//   grids: RT x G x 16 pairs (scale, zero), at the next 256 bytes after the
+//          codes; rows beyond m have scale = zero = 0.
+//   unit:  one float, the power of two at or above the layer's largest
+//          weight |s (c - z)|, at the next 256 bytes after the grids: kernels
+//          that round weights to 16 bits divide by it first, so that no
+//          layer's weights leave float16's normal range as a whole.
+// Codes of rows beyond m and columns beyond n are 0; their products are kept
+// out by zeros of the activations.
+//
+// A code becomes the exact number u = 16 + c in one operation per pair: in
+// bfloat16, 16 has the bits 0x4180 and four mantissa bits of weight 1 at bits
+// 3 .. 6; in float16, 0x4C00 and bits 6 .. 9.  The products of u with
+// activations are exact in the MFMA's float32, and
+//     sum_j s (c_j - z) x_j = s ( sum_j u_j x_j - (16 + z) sum_j x_j )
+// over a group applies step and zero point once, in float32.  The offset of
+// 16 costs about 16 / 5 of the sum's float32 rounding, 2 bits of 24.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm.hpp"
+#include "internal.hpp"
+
+namespace bk {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kQ4Rows = 16;       // rows of a code block
+constexpr int kQ4Cols = 128;      // columns of a code block
+constexpr float kQ4Offset = 16.f; // u = c + 16
+
+struct Q4Dims {
+    int64_t m, n;
+    int RT, KB, G;
+    int gb;                       // 64-column halves per grid (>= 2 KB when one grid per row)
+    size_t grid_at, unit_at;      // byte offsets of the grids and the unit
+    size_t bytes;                 // bytes of one layer
+};
+
+inline Q4Dims q4_dims(int64_t m, int64_t n, int64_t group_size)
+{
+    Q4Dims d;
+    d.m = m;
+    d.n = n;
+    d.RT = (int)ceil_div(m, kQ4Rows);
+    d.KB = (int)ceil_div(n, kQ4Cols);
+    d.G = group_size ? (int)ceil_div(n, group_size) : 1;
+    if (d.G < 1) d.G = 1;
+    d.gb = group_size ? (int)(group_size / 64 < (1 << 20) ? group_size / 64 : (1 << 20)) : (1 << 20);
+    d.grid_at = align_up((size_t)d.RT * d.KB * 1024);
+    d.unit_at = align_up(d.grid_at + (size_t)d.RT * d.G * kQ4Rows * 8);
+    d.bytes = d.unit_at + kAlign;
+    return d;
+}
+
+// One packed layer as the kernels take it.
+struct Q4Layer {
+    const u32x4* codes;
+    const f32x2* grid;
+    const float* unit;
+    int m, n, RT, KB, G, gb;
+};
+
+inline Q4Layer q4_layer(const void* packed, const Q4Dims& d)
+{
+    const char* p = static_cast<const char*>(packed);
+    return Q4Layer{reinterpret_cast<const u32x4*>(p), reinterpret_cast<const f32x2*>(p + d.grid_at),
+                   reinterpret_cast<const float*>(p + d.unit_at), (int)d.m, (int)d.n, d.RT, d.KB, d.G, d.gb};
+}
+
+// The activation types: raw 16-bit storage, MFMA forms and roundings.
+struct Bf16 {
+    typedef bf16x8 vec;
+    static __device__ __forceinline__ float up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+    static __device__ __forceinline__ uint16_t down(float v)
+    {
+        return __builtin_bit_cast(uint16_t, (__bf16)v);   // to nearest, ties to even
+    }
+    static __device__ __forceinline__ f32x4 mfma16(vec a, vec b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(vec a, vec b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // u of the 8 codes of a dword
+    static __device__ __forceinline__ vec codes(uint32_t w)
+    {
+        u32x4 v;
+        v.x = (w & 0x00780078u) | 0x41804180u;
+        v.y = (__builtin_rotateright32(w, 4) & 0x00780078u) | 0x41804180u;
+        v.z = (__builtin_rotateright32(w, 8) & 0x00780078u) | 0x41804180u;
+        v.w = (__builtin_rotateright32(w, 12) & 0x00780078u) | 0x41804180u;
+        return __builtin_bit_cast(vec, v);
+    }
+    static constexpr uint16_t kOne = 0x3F80;
+};
+
+struct Fp16 {
+    typedef f16x8 vec;
+    static __device__ __forceinline__ float up(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+    static __device__ __forceinline__ uint16_t down(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+    static __device__ __forceinline__ f32x4 mfma16(vec a, vec b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(vec a, vec b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ vec codes(uint32_t w)
+    {
+        u32x4 v;
+        v.x = (__builtin_rotateright32(w, 29) & 0x03C003C0u) | 0x4C004C00u;
+        v.y = (__builtin_rotateright32(w, 1) & 0x03C003C0u) | 0x4C004C00u;
+        v.z = (__builtin_rotateright32(w, 5) & 0x03C003C0u) | 0x4C004C00u;
+        v.w = (__builtin_rotateright32(w, 9) & 0x03C003C0u) | 0x4C004C00u;
+        return __builtin_bit_cast(vec, v);
+    }
+    static constexpr uint16_t kOne = 0x3C00;
+};
+
+// 16 consecutive activations p[0 .. 15] of a row that has `left` of them from
+// p on (zeros beyond); `wide`: p is 16-byte aligned.
+__device__ __forceinline__ void q4_load16(const uint16_t* __restrict__ p, int left, bool wide, u32x4 (&v)[2])
+{
+    if (wide && left >= 16) {
+        v[0] = *reinterpret_cast<const u32x4*>(p);
+        v[1] = *reinterpret_cast<const u32x4*>(p + 8);
+        return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 8 * h + 2 * i;
+            const uint32_t lo = e < left ? p[e] : 0u;
+            const uint32_t hi = e + 1 < left ? p[e + 1] : 0u;
+            v[h][i] = lo | (hi << 16);
+        }
+}
+
+template <class X>
+__device__ __forceinline__ typename X::vec q4_ones()
+{
+    const uint32_t o = (uint32_t)X::kOne * 0x10001u;
+    const u32x4 v = {o, o, o, o};
+    return __builtin_bit_cast(typename X::vec, v);
+}
+
+}  // namespace bk

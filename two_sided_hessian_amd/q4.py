@@ -1,0 +1,242 @@
+"""Layers on 4-bit codes (include/bakron_q4.h): packing, the linear layer, its
+input gradient and a mixture-of-experts layer.
+
+As in the rest of the binding, arguments are checked here, every arithmetic
+step runs in the library's HIP kernels, and there is no fallback.  The
+calls are made once per layer and token, so the checks are kept to
+attribute reads (no tensor is looked into: no copy, no synchronisation).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _binding as _b
+
+BAKRON_Q4_BF16 = 0
+BAKRON_Q4_FP16 = 1
+BAKRON_Q4_MAX_TOKENS = 16777216
+BAKRON_Q4_MAX_LAYERS = 256
+BAKRON_Q4_MOE_MAX_TOKENS = 64
+BAKRON_Q4_MOE_MAX_TOP_K = 16
+
+_VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_LINEAR = [_VP, _I64, _I64, _I32, _VP, _I64, _I64, _I64, _VP, _I64, _VP, _SZ, _VP]
+_b.SIGNATURES.update({
+    "bakron_q4_packed_bytes": (_SZ, [_I64] * 4),
+    "bakron_q4_pack": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I64, _I64, _I64, _VP, _VP]),
+    "bakron_q4_linear_workspace_bytes": (_SZ, [_I64] * 4),
+    "bakron_q4_linear": (ctypes.c_int, _LINEAR),
+    "bakron_q4_linear_grad_workspace_bytes": (_SZ, [_I64] * 4),
+    "bakron_q4_linear_grad": (ctypes.c_int, _LINEAR),
+    "bakron_q4_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I32, _I64]),
+    "bakron_q4_moe": (ctypes.c_int, [_VP, _I64, _I64, _I32, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I32, _I64, _VP, _I64,
+                                     _VP, _VP, _VP, _SZ, _VP]),
+})
+
+_TYPES = {torch.bfloat16: BAKRON_Q4_BF16, torch.float16: BAKRON_Q4_FP16}
+
+
+class Q4Weight:
+    """One layer (count 1) or a stack of ``count`` layers of m x n in the
+    packed layout, with group_size columns per grid (None: one grid per row).
+    ``data`` is the device buffer (uint8) that holds it."""
+
+    __slots__ = ("data", "count", "m", "n", "group_size", "device", "_ptr", "_group")
+
+    def __init__(self, data, count, m, n, group_size):
+        self.data, self.count, self.m, self.n, self.group_size = data, count, m, n, group_size
+        self.device = data.device
+        self._ptr, self._group = data.data_ptr(), group_size or 0
+
+    def __repr__(self):
+        return f"Q4Weight(count={self.count}, m={self.m}, n={self.n}, group_size={self.group_size})"
+
+
+def _group(group_size):
+    if group_size is None:
+        return 0
+    if group_size <= 0 or group_size % 64:
+        raise ValueError("group_size must be a positive multiple of 64")
+    return int(group_size)
+
+
+def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
+    """bakron_q4_pack: the packed form of a rounded layer (codes m x n, grids m
+    or m x ceil(n / group_size)) or of a stack of layers (one more dimension
+    in front): codes uint8 in [0, 15], scale and zero float32, as solve() and
+    gptq() take and return them.  ``check``: raise GridError if a code is
+    above 15 or a grid is not finite (reads them back to the host, which
+    waits for the work that makes them)."""
+    g = _group(group_size)
+    if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
+        raise ValueError("codes must be an m x n or count x m x n tensor")
+    lead, (m, n) = tuple(codes.shape[:-2]), codes.shape[-2:]
+    count = lead[0] if lead else 1
+    _b._check_dev("codes", codes, torch.uint8, lead + (m, n))
+    gshape = lead + ((m, -(-n // g)) if g else (m,))
+    if not g and isinstance(scale, torch.Tensor) and scale.dim() == len(lead) + 2:
+        gshape = lead + (m, 1)
+    _b._check_dev("scale", scale, torch.float32, gshape)
+    _b._check_dev("zero", zero, torch.float32, gshape)
+    if check and codes.numel():
+        if int(codes.max()) > 15:
+            raise _b.GridError("codes must lie in [0, 15]")
+        if not bool(torch.isfinite(scale).all()) or not bool(torch.isfinite(zero).all()):
+            raise _b.GridError("scale and zero must be finite")
+    L = _b.lib()
+    data = _b.workspace(L.bakron_q4_packed_bytes(count, m, n, g), codes.device)
+    if stream is not None:
+        _keep(stream, data)
+    rc = L.bakron_q4_pack(codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), count, m, n, g, data.data_ptr(),
+                          _b._stream(stream))
+    if rc != _b.BAKRON_SUCCESS:
+        raise _b.BakronError(rc, "bakron_q4_pack")
+    return Q4Weight(data, count, m, n, group_size)
+
+
+def q4_linear_workspace_bytes(tokens: int, w: Q4Weight) -> int:
+    return _b.lib().bakron_q4_linear_workspace_bytes(tokens, w.m, w.n, w._group)
+
+
+def q4_linear_grad_workspace_bytes(tokens: int, w: Q4Weight) -> int:
+    return _b.lib().bakron_q4_linear_grad_workspace_bytes(tokens, w.m, w.n, w._group)
+
+
+def q4_moe_workspace_bytes(tokens: int, w_gate: Q4Weight, top_k: int) -> int:
+    return _b.lib().bakron_q4_moe_workspace_bytes(tokens, w_gate.n, w_gate.m, w_gate.count, top_k, w_gate._group)
+
+
+def _rows(name, t, cols, like=None):
+    """Leading dimension of a tokens x cols matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in _TYPES or (like is not None and t.dtype != like):
+        raise TypeError(f"{name} must be {like or 'torch.bfloat16 or torch.float16'}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} must have shape (tokens, {cols}), got {tuple(t.shape)}")
+    rows, ld = t.shape[0], t.stride(0)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1 or cols == 0:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return ld
+
+
+def _one(name, w, device, count=1):
+    if not isinstance(w, Q4Weight):
+        raise TypeError(f"{name} must be a Q4Weight (q4_pack)")
+    if w.count != count:
+        raise ValueError(f"{name} must hold {count} layer(s), got {w.count}")
+    if w.device != device:
+        raise ValueError(f"{name} is on {w.device}, not on {device}")
+
+
+def _ws(ws, need, device):
+    """The workspace as (tensor, pointer, bytes)."""
+    if ws is None:
+        size = need()
+        if not size:
+            return None, None, 0
+        ws = _b.workspace(size, device)
+    elif ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, not on {device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _keep(stream, *tensors):
+    """Tensors made here, on the current stream, and used on the caller's
+    other one: torch's allocator has to wait for it before it hands them out
+    again."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def _linear(call, size, name, x, w, out, ws, stream):
+    if not isinstance(w, Q4Weight):
+        raise TypeError("w must be a Q4Weight (q4_pack)")
+    in_cols, out_cols = (w.n, w.m) if name == "x" else (w.m, w.n)
+    ldx = _rows(name, x, in_cols)
+    device, T = x.device, x.shape[0]
+    _one("w", w, device)
+    if out is None:
+        out = torch.empty((T, out_cols), dtype=x.dtype, device=device)
+        ldo = out_cols
+    else:
+        ldo = _rows("out", out, out_cols, x.dtype)
+        if out.shape[0] != T or out.device != device:
+            raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {device}")
+    L = _b.lib()
+    given, (ws, wp, wn) = ws, _ws(ws, lambda: size(T, w), device)
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+    else:
+        s = stream
+        _keep(s, out, None if given is not None else ws)
+    rc = getattr(L, call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w._ptr, w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn,
+                          s.cuda_stream)
+    if rc != _b.BAKRON_SUCCESS:
+        raise _b.BakronError(rc, call)
+    return out
+
+
+def q4_linear(x, w, *, out=None, ws=None, stream=None):
+    """bakron_q4_linear: y = x W^T (tokens x m) of one packed layer, x tokens x n
+    in bfloat16 or float16 (rows contiguous, any row stride).  ``out``: where
+    to write y; ``ws``: a workspace of q4_linear_workspace_bytes."""
+    return _linear("bakron_q4_linear", q4_linear_workspace_bytes, "x", x, w, out, ws, stream)
+
+
+def q4_linear_grad(dy, w, *, out=None, ws=None, stream=None):
+    """bakron_q4_linear_grad: dx = dy W (tokens x n), the gradient of q4_linear
+    with respect to x.  ``out``, ``ws`` (q4_linear_grad_workspace_bytes): as
+    there."""
+    return _linear("bakron_q4_linear_grad", q4_linear_grad_workspace_bytes, "dy", dy, w, out, ws, stream)
+
+
+def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=None):
+    """bakron_q4_moe: a mixture-of-experts layer for up to 64 tokens.  x tokens x
+    hidden; router experts x hidden; w_gate and w_up stacks of ffn x hidden,
+    w_down a stack of hidden x ffn layers.  Returns dict(y, ids, weights): the
+    layer's output, the chosen experts (int32 tokens x top_k, largest logit
+    first) and their shares (float32).  ``out``: a dict of the three to write
+    to; ``ws``: a workspace of q4_moe_workspace_bytes."""
+    if not isinstance(w_gate, Q4Weight):
+        raise TypeError("w_gate must be a Q4Weight (q4_pack)")
+    f, h, E = w_gate.m, w_gate.n, w_gate.count
+    ldx = _rows("x", x, h)
+    device, T = x.device, x.shape[0]
+    for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        _one(name, w, device, E)
+        if (w.m, w.n) != ((h, f) if name == "w_down" else (f, h)):
+            raise ValueError(f"{name} must be {(h, f) if name == 'w_down' else (f, h)}, got {(w.m, w.n)}")
+        if w._group != w_gate._group:
+            raise ValueError("the three stacks must have one group_size")
+    _b._check_dev("router", router, x.dtype, (E, h))
+    if out is None:
+        out = {"y": torch.empty((T, h), dtype=x.dtype, device=device),
+               "ids": torch.empty((T, top_k), dtype=torch.int32, device=device),
+               "weights": torch.empty((T, top_k), dtype=torch.float32, device=device)}
+        ldy = h
+    else:
+        ldy = _rows("out['y']", out["y"], h, x.dtype)
+        if out["y"].shape[0] != T:
+            raise ValueError(f"out['y'] must have shape ({T}, {h}), got {tuple(out['y'].shape)}")
+        _b._check_dev("out['ids']", out["ids"], torch.int32, (T, top_k))
+        _b._check_dev("out['weights']", out["weights"], torch.float32, (T, top_k))
+    given, (ws, wp, wn) = ws, _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), device)
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+    else:
+        s = stream
+        _keep(s, *out.values(), None if given is not None else ws)
+    rc = _b.lib().bakron_q4_moe(x.data_ptr(), ldx, T, _TYPES[x.dtype], router.data_ptr(), w_gate._ptr, w_up._ptr,
+                                w_down._ptr, h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy,
+                                out["ids"].data_ptr(), out["weights"].data_ptr(), wp, wn, s.cuda_stream)
+    if rc != _b.BAKRON_SUCCESS:
+        raise _b.BakronError(rc, "bakron_q4_moe")
+    return out
