@@ -10,9 +10,9 @@ namespace bk {
 //
 // One thread per 16-byte unit (32 codes of one row).  Reads half of what it
 // writes twice over; bound by HBM, run once per layer.
-__global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ codes, int64_t m, int64_t n, int RT,
-                                                 int KB, int64_t layer_bytes, int64_t unit_at,
-                                                 char* __restrict__ packed)
+__global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ codes, const float* __restrict__ scale,
+                                                 int64_t m, int64_t n, int RT, int KB, int G, int gb,
+                                                 int64_t layer_bytes, int64_t unit_at, char* __restrict__ packed)
 {
     if (blockIdx.x == 0 && threadIdx.x == 0)   // k_q4_pack_grid raises it
         *reinterpret_cast<float*>(packed + blockIdx.y * layer_bytes + unit_at) = 0.f;
@@ -30,6 +30,8 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
         for (int d = 0; d < 4; ++d) {
             const int64_t c0 = col0 + 64 * (d >> 1) + 8 * (d & 1);
             uint32_t v = 0;
+            const int64_t g = min((int)(c0 >> 6) / gb, G - 1);
+            if (scale[(layer * m + row) * G + g] == 0.f) continue;   // weights of 0: see k_q4_pack_grid
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (c0 + e < n) v |= (uint32_t)(src[c0 + e] & 15u) << (4 * (e >> 1) + 16 * (e & 1));
@@ -52,6 +54,9 @@ __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ 
         if (row < m) {
             v.x = scale[(layer * m + row) * G + g];
             v.y = zero[(layer * m + row) * G + g];
+            // a step of 0 (every weight 0, whatever the codes) becomes step 1,
+            // zero point 0 on codes of 0: kernels divide by steps
+            if (v.x == 0.f) v = f32x2{1.f, 0.f};
         }
         reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at)[e] = v;
     }
@@ -227,7 +232,7 @@ int bakron_q4_pack(const uint8_t* codes, const float* scale, const float* zero, 
     const double mn = (double)count * m * n;
     bk::launch(nullptr, bk::KK_Q4_PACK, 0.0, 1.5 * mn, bk::k_q4_pack,
                dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.KB * 64, 256), (unsigned)count), dim3(256), stream, codes,
-               m, n, d.RT, d.KB, (int64_t)d.bytes, (int64_t)d.unit_at, out);
+               scale, m, n, d.RT, d.KB, d.G, d.gb, (int64_t)d.bytes, (int64_t)d.unit_at, out);
     bk::launch(nullptr, bk::KK_Q4_PACK_GRID, 0.0, 16.0 * count * m * d.G, bk::k_q4_pack_grid,
                dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.G * 16, 256), (unsigned)count), dim3(256), stream, scale,
                zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
@@ -257,8 +262,10 @@ static int check_q4(const void* in, int64_t ldin, int64_t in_cols, int64_t token
 
 size_t bakron_q4_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int64_t group_size)
 {
-    (void)tokens, (void)m, (void)n, (void)group_size;
-    return 0;
+    if (!q4_shape_ok(m, n) || !q4_group_ok(group_size) || tokens <= bk::kQ4Few || tokens > BAKRON_Q4_MAX_TOKENS ||
+        m == 0 || n == 0)
+        return 0;
+    return bk::q4_prompt_workspace_bytes(tokens, n, bk::q4_dims(m, n, group_size).G);
 }
 
 int bakron_q4_linear(const void* x, int64_t ldx, int64_t tokens, int32_t type, const void* packed, int64_t m, int64_t n,
@@ -271,6 +278,10 @@ int bakron_q4_linear(const void* x, int64_t ldx, int64_t tokens, int32_t type, c
     if (c == 1) return BAKRON_SUCCESS;
     if (c == 2) return bk::q4_zero_enqueue(y, ldy, tokens, m, stream) ? BAKRON_ERR_HIP : BAKRON_SUCCESS;
     const bk::Q4Layer w = bk::q4_layer(packed, bk::q4_dims(m, n, group_size));
+    if (tokens > bk::kQ4Few)
+        return bk::q4_prompt_enqueue(x, ldx, tokens, type == BAKRON_Q4_BF16, w, y, ldy, workspace, stream)
+                   ? BAKRON_ERR_HIP
+                   : BAKRON_SUCCESS;
     if (type == BAKRON_Q4_BF16) bk::few_enqueue<bk::Bf16>(x, ldx, tokens, w, y, ldy, stream);
     else bk::few_enqueue<bk::Fp16>(x, ldx, tokens, w, y, ldy, stream);
     return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;

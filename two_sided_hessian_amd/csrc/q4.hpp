@@ -170,4 +170,10 @@ __device__ __forceinline__ typename X::vec q4_ones()
     return __builtin_bit_cast(typename X::vec, v);
 }
 
+// Many tokens (q4_prompt.hip)
+constexpr int64_t kQ4Few = 64;   // up to so many tokens the few-token kernel runs
+size_t q4_prompt_workspace_bytes(int64_t T, int64_t n, int64_t G);
+int q4_prompt_enqueue(const void* x, int64_t ldx, int64_t T, bool bf16, const Q4Layer& w, void* y, int64_t ldy, void* ws,
+                      hipStream_t s);
+
 }  // namespace bk
