@@ -89,6 +89,17 @@ inline Q4Layer q4_layer(const void* packed, const Q4Dims& d)
                    reinterpret_cast<const float*>(p + d.unit_at), (int)d.m, (int)d.n, d.RT, d.KB, d.G, d.gb};
 }
 
+// (w & mask) | base.  The constants pass through empty asm statements so that
+// the compiler keeps them in registers, the mask in a vector one, and takes
+// its one instruction for both (which reads no literal and at most one scalar
+// register) instead of two with literals.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t base)
+{
+    asm("" : "+v"(mask));
+    asm("" : "+s"(base));
+    return (w & mask) | base;
+}
+
 // The activation types: raw 16-bit storage, MFMA forms and roundings.
 struct Bf16 {
     typedef bf16x8 vec;
@@ -109,10 +120,10 @@ struct Bf16 {
     static __device__ __forceinline__ vec codes(uint32_t w)
     {
         u32x4 v;
-        v.x = (w & 0x00780078u) | 0x41804180u;
-        v.y = (__builtin_rotateright32(w, 4) & 0x00780078u) | 0x41804180u;
-        v.z = (__builtin_rotateright32(w, 8) & 0x00780078u) | 0x41804180u;
-        v.w = (__builtin_rotateright32(w, 12) & 0x00780078u) | 0x41804180u;
+        v.x = and_or(w, 0x00780078u, 0x41804180u);
+        v.y = and_or(__builtin_rotateright32(w, 4), 0x00780078u, 0x41804180u);
+        v.z = and_or(__builtin_rotateright32(w, 8), 0x00780078u, 0x41804180u);
+        v.w = and_or(__builtin_rotateright32(w, 12), 0x00780078u, 0x41804180u);
         return __builtin_bit_cast(vec, v);
     }
     static constexpr uint16_t kOne = 0x3F80;
@@ -133,10 +144,10 @@ struct Fp16 {
     static __device__ __forceinline__ vec codes(uint32_t w)
     {
         u32x4 v;
-        v.x = (__builtin_rotateright32(w, 29) & 0x03C003C0u) | 0x4C004C00u;
-        v.y = (__builtin_rotateright32(w, 1) & 0x03C003C0u) | 0x4C004C00u;
-        v.z = (__builtin_rotateright32(w, 5) & 0x03C003C0u) | 0x4C004C00u;
-        v.w = (__builtin_rotateright32(w, 9) & 0x03C003C0u) | 0x4C004C00u;
+        v.x = and_or(__builtin_rotateright32(w, 29), 0x03C003C0u, 0x4C004C00u);
+        v.y = and_or(__builtin_rotateright32(w, 1), 0x03C003C0u, 0x4C004C00u);
+        v.z = and_or(__builtin_rotateright32(w, 5), 0x03C003C0u, 0x4C004C00u);
+        v.w = and_or(__builtin_rotateright32(w, 9), 0x03C003C0u, 0x4C004C00u);
         return __builtin_bit_cast(vec, v);
     }
     static constexpr uint16_t kOne = 0x3C00;
@@ -168,6 +179,23 @@ __device__ __forceinline__ typename X::vec q4_ones()
     const uint32_t o = (uint32_t)X::kOne * 0x10001u;
     const u32x4 v = {o, o, o, o};
     return __builtin_bit_cast(typename X::vec, v);
+}
+
+// Direct loads to LDS through a buffer descriptor: per-lane byte offsets
+// `lane_at` that never change, a scalar one that does, no vector arithmetic
+// per load.  Lane l's 16 (4) bytes land at s + 16 l (4 l).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+__device__ __forceinline__ void load_lds16(Rsrc r, uint32_t lane_at, uint32_t at, char* s)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)s, 16, lane_at, at, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(Rsrc r, uint32_t lane_at, uint32_t at, char* s)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)s, 4, lane_at, at, 0, 0);
 }
 
 // Many tokens (q4_prompt.hip)

@@ -17,10 +17,11 @@
 // k_q4_prompt: a workgroup of 2 x WR waves computes 64 TA tokens x 64 WR rows
 // of W; a wave owns 32 TA tokens x 64 rows as TA x 2 MFMA tiles of 32 x 32
 // (v_mfma_f32_32x32x16, tokens are its rows).  x goes through LDS in chunks
-// of 64 columns by direct loads, two buffers, 16-byte slots permuted so that
-// fragment reads spread over the banks.  W never touches LDS: a lane loads
-// its fragments' codes from the packed layout (32 bytes per 128 columns and
-// tile) and expands them in registers, 7 operations per 8 codes.
+// of 64 columns by direct loads, 16-byte slots permuted so that
+// fragment reads spread over the banks.  Codes come through LDS as they are
+// (a quarter of the bytes of 16-bit weights); each wave expands its fragments
+// in registers, 7 operations per 8 codes.  Two or three chunks are in flight
+// at any time: a chunk's products take less than a load's latency.
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
@@ -83,31 +84,78 @@ __global__ __launch_bounds__(256) void k_q4_sums(const uint16_t* __restrict__ x,
 
 template <int TA, int WR>
 struct Prompt {
-    static constexpr int BT = 64 * TA;           // tokens of a workgroup
-    static constexpr int BR = 64 * WR;           // rows of W of a workgroup
-    static constexpr int THREADS = 128 * WR;
-    static constexpr int BUF = BT * 128;         // bytes of a 64-column chunk of x
-    static constexpr int LOADS = BT / 8 / (2 * WR);   // direct loads of a wave per chunk (8 tokens each)
-    static_assert(LOADS >= 1, "a wave stages at least eight tokens");
+    static constexpr int BT = 64 * TA;                // tokens of a workgroup
+    static constexpr int BR = 64 * WR;                // rows of W of a workgroup
+    static constexpr int XBUF = BT * 128;             // bytes of a 64-column chunk of x
+    static constexpr int WBUF = BR * 64;              // bytes of a 128-column block of codes
+    static constexpr int AHEAD = TA == 4 ? 2 : 3;     // chunks in flight (LDS allows no more)
+    static constexpr int NX = AHEAD + 1, NW = AHEAD + 1;
+    static constexpr int XLOADS = BT / 8 / (2 * WR);  // direct loads of a wave per chunk of x (8 tokens each)
+    static constexpr int LOADS = XLOADS + 2;          // one of the grid and one of codes
+    static constexpr int GBUF = BR * 8;               // bytes of the grid entries of a chunk
+    static constexpr int CODES = NX * XBUF, GRID = CODES + NW * WBUF, LDS = GRID + NX * GBUF;
+    static_assert(XLOADS >= 1, "a wave stages at least eight tokens");
 };
 
-// Tokens [t0, t0 + BT) x columns [64 c, 64 c + 64) of x into LDS: token r's
-// 16-byte slot v holds columns 8 (v ^ ((r >> 1) & 7)).  Tokens beyond T read
-// the last one (their results are not stored).
-template <int TA, int WR>
-__device__ __forceinline__ void prompt_stage(const uint16_t* __restrict__ x, int64_t ldx, int t0, int T, int c, char* s)
+// Waits until at most `left` loads of this wave are in flight (they complete
+// in order), then for the other waves.
+template <int LEFT>
+__device__ __forceinline__ void prompt_wait()
 {
-    typedef Prompt<TA, WR> P;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-#pragma unroll
-    for (int i = 0; i < P::LOADS; ++i) {
-        const int q = wave * P::LOADS + i;
-        const int r = 8 * q + (lane >> 3);
-        const uint16_t* src = x + (int64_t)min(t0 + r, T - 1) * ldx + 64 * c + 8 * ((lane & 7) ^ ((r >> 1) & 7));
-        __builtin_amdgcn_global_load_lds((global_cptr)src, (lds_ptr)(s + 1024 * q), 16, 0, 0);
-    }
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
+
+// The direct loads of a workgroup, chunk by chunk: tokens [t0, t0 + BT) x
+// columns [64 c, 64 c + 64) of x (token r's 16-byte slot v holds columns
+// 8 (v ^ ((r >> 1) & 7))), the grid entries of the rows for that chunk, and
+// half of the codes of column block c / 2 + 1, which is needed two chunks on.
+// Tokens beyond T and row tiles beyond RT read the last ones (their results
+// are not stored); past the last chunk the last one is loaded again, into a
+// buffer that no one reads, so that every chunk counts the same loads.
+template <int TA, int WR>
+struct PromptStage {
+    typedef Prompt<TA, WR> P;
+    Rsrc x, codes, grid;
+    uint32_t x_at[P::XLOADS], code_at[2], grid_at;
+    int nchunk, KB, G, gb, wave;
+    char* lds;
+
+    __device__ __forceinline__ PromptStage(const uint16_t* xp, int64_t ldx, int t0, int T, const Q4Layer& w, int rt0,
+                                           char* lds_)
+        : x(buffer_of(xp + t0 * ldx, 0x7FFFFFFFu)),
+          codes(buffer_of(w.codes + (int64_t)rt0 * w.KB * 64, 0x7FFFFFFFu)),
+          grid(buffer_of(w.grid + (int64_t)rt0 * w.G * 16, 0x7FFFFFFFu)),
+          nchunk((w.n + 63) / 64), KB(w.KB), G(w.G), gb(w.gb),
+          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lds(lds_)
+    {
+        const int lane = threadIdx.x & 63;
+        const int rts = w.RT - 1 - rt0;
+#pragma unroll
+        for (int i = 0; i < P::XLOADS; ++i) {
+            const int r = 8 * (wave * P::XLOADS + i) + (lane >> 3);
+            x_at[i] = (uint32_t)(min(r, T - 1 - t0) * ldx * 2) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) code_at[p] = (uint32_t)min(p * 2 * WR + wave, rts) * w.KB * 1024 + 16 * lane;
+        grid_at = (uint32_t)min(2 * wave + (lane >> 5), rts) * w.G * 128 + 4 * (lane & 31);
+    }
+    // bx, bw: the buffers of chunk c and of column block c / 2 + 1; part = c & 1
+    __device__ __forceinline__ void chunk(int c, int bx, int bw, int part) const
+    {
+        const int cx = min(c, nchunk - 1);
+        char* s = lds + bx * P::XBUF + wave * P::XLOADS * 1024;
+#pragma unroll
+        for (int i = 0; i < P::XLOADS; ++i) load_lds16(x, x_at[i], 128 * cx, s + 1024 * i);
+        load_lds4(grid, grid_at, 128 * min(cx / gb, G - 1), lds + P::GRID + bx * P::GBUF + 256 * wave);
+        load_lds16(codes, code_at[part], 1024 * min((c >> 1) + 1, KB - 1),
+                     lds + P::CODES + bw * P::WBUF + 1024 * (part * 2 * WR + wave));
+    }
+    __device__ __forceinline__ void first() const
+    {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) load_lds16(codes, code_at[p], 0, lds + P::CODES + 1024 * (p * 2 * WR + wave));
+    }
+};
 
 // The three-term split of a float32 value into bfloat16, v = a + b + c.
 __device__ __forceinline__ void split3(float v, uint32_t& a, uint32_t& b, uint32_t& c)
@@ -133,31 +181,24 @@ __device__ __forceinline__ void prompt_tile(int nt, int nr, int& bt, int& br)
 }
 
 template <class X, int TA, int WR>
-__global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restrict__ x, int64_t ldx,
-                                                        int T, Q4Layer w,
+__global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
                                                         const float* __restrict__ sums, int64_t lds_,
-                                                        uint16_t* __restrict__ y, int64_t ldy, int nt,
-                                                        int nr)
+                                                        uint16_t* __restrict__ y, int64_t ldy, int nt, int nr)
 {
     typedef Prompt<TA, WR> P;
     typedef typename X::vec vec;
-    __shared__ __align__(16) char lds[2 * P::BUF];
+    __shared__ __align__(16) char lds[P::LDS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, ml = lane & 31;
     const int wt = wave / WR, wr = wave % WR;
     int bt, br;
     prompt_tile(nt, nr, bt, br);
-    const int t0 = bt * P::BT;
-    const int nchunk = (w.n + 63) / 64;
-
-    // this lane's row tile and its units (q = h and h + 2) of each 32-row tile
-    int64_t unit[2], grid[2];
+    const int t0 = bt * P::BT, rt0 = br * (P::BR / 16);
+    const PromptStage<TA, WR> stage(x, ldx, t0, T, w, rt0, lds);
+    stage.first();
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const int rt = min(br * (P::BR / 16) + wr * 4 + 2 * b + (ml >> 4), w.RT - 1);
-        unit[b] = (int64_t)rt * w.KB * 64 + 16 * h + (ml & 15);
-        grid[b] = (int64_t)rt * w.G * 16 + (ml & 15);
-    }
+    for (int c = 0; c < P::AHEAD; ++c) stage.chunk(c, c, ((c >> 1) + 1) % P::NW, c & 1);
+
     f32x16 acc[TA][2];
 #pragma unroll
     for (int a = 0; a < TA; ++a)
@@ -166,67 +207,67 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
-    u32x4 next[2][2], cur[2][2];
-    float step[2];
-    prompt_stage<TA, WR>(x, ldx, t0, T, 0, lds);
+    u32x4 codes[2][2];   // [row tile pair][unit h, h + 2]
+    float step[2] = {1.f, 1.f};
+    int group = -1;
+    int bx = 0, bw = 0;                                  // buffers of chunk c and block kb
+    int px = P::AHEAD % P::NX, pw = (P::AHEAD / 2 + 1) % P::NW;   // and of the ones staged beside them
+    // the lane's parts of the LDS addresses
+    uint32_t x_lane[4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        next[b][0] = w.codes[unit[b]];
-        next[b][1] = w.codes[unit[b] + 32];
-        step[b] = w.grid[grid[b]].x;
-    }
-    int group = 0;
+    for (int v = 0; v < 4; ++v)
+        x_lane[v] = 128 * (32 * wt * TA + ml) + 16 * ((4 * (v >> 1) + 2 * h + (v & 1)) ^ ((ml >> 1) & 7));
+    const uint32_t w_lane = P::CODES + 1024 * (4 * wr + (ml >> 4)) + 256 * h + 16 * (ml & 15);
+    const uint32_t g_lane = P::GRID + 8 * (64 * wr + ml);
     for (int kb = 0; kb < w.KB; ++kb) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int c = 2 * kb + half;
-            if (c < nchunk) {
-                wait_direct_loads();
-                __syncthreads();
-                if (c + 1 < nchunk) prompt_stage<TA, WR>(x, ldx, t0, T, c + 1, lds + ((half + 1) & 1) * P::BUF);
+            if (c < stage.nchunk) {
+                prompt_wait<(P::AHEAD - 1) * P::LOADS>();
+                stage.chunk(c + P::AHEAD, px, pw, (half + P::AHEAD) & 1);
+                px = px + 1 == P::NX ? 0 : px + 1;
+                if ((half + P::AHEAD) & 1) pw = pw + 1 == P::NW ? 0 : pw + 1;
                 if (half == 0) {
-                    const int kn = min(kb + 1, w.KB - 1);
+                    const char* s = lds + w_lane + bw * P::WBUF;
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            cur[b][u] = next[b][u];
-                            next[b][u] = w.codes[unit[b] + (int64_t)kn * 64 + 32 * u];
-                        }
+                        for (int u = 0; u < 2; ++u)
+                            codes[b][u] = *reinterpret_cast<const u32x4*>(s + 2048 * b + 512 * u);
                 }
                 const int g = min(c / w.gb, w.G - 1);
                 if (g != group) {
                     group = g;
+                    const char* s = lds + g_lane + bx * P::GBUF;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const float s = w.grid[grid[b] + (int64_t)g * 16].x;
-                        const float ratio = step[b] / s;
-                        step[b] = s;
+                        const float s1 = *reinterpret_cast<const float*>(s + 256 * b);
+                        const float ratio = step[b] * __builtin_amdgcn_rcpf(s1);
+                        step[b] = s1;
 #pragma unroll
                         for (int a = 0; a < TA; ++a)
 #pragma unroll
                             for (int r = 0; r < 16; ++r) acc[a][b][r] *= ratio;
                     }
                 }
-                const char* s = lds + half * P::BUF;
+                const char* s = lds + bx * P::XBUF;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int v = 0; v < 4; ++v) {
+                    vec wf[2];
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        vec wf[2];
+                    for (int b = 0; b < 2; ++b) wf[b] = X::codes(codes[b][v >> 1][2 * half + (v & 1)]);
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) wf[b] = X::codes(cur[b][u][2 * half + d]);
-                        const int slot = 4 * u + 2 * h + d;
+                    for (int a = 0; a < TA; ++a) {
+                        const vec xf = *reinterpret_cast<const vec*>(s + x_lane[v] + 4096 * a);
 #pragma unroll
-                        for (int a = 0; a < TA; ++a) {
-                            const int r = 32 * (wt * TA + a) + ml;
-                            const vec xf = *reinterpret_cast<const vec*>(s + 128 * r + 16 * (slot ^ ((r >> 1) & 7)));
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf, wf[b], acc[a][b]);
-                        }
+                        for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf, wf[b], acc[a][b]);
                     }
+                }
+                bx = bx + 1 == P::NX ? 0 : bx + 1;
             }
         }
+        bw = bw + 1 == P::NW ? 0 : bw + 1;
     }
 #pragma unroll
     for (int a = 0; a < TA; ++a)
@@ -234,45 +275,81 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] *= step[b];
-
-    // minus s (16 + z) X: lane half h takes group g0 + h, slots
-    // X1 Z1, X1 Z2, X2 Z1, X1 Z3, X2 Z2, X3 Z1
-    for (int g0 = 0; g0 < w.G; g0 += 2) {
-        const int g = g0 + h;
-        bf16x8 zf[2];
+    int64_t grid[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            uint32_t z1 = 0, z2 = 0, z3 = 0;
-            if (g < w.G) {
-                const f32x2 sz = w.grid[grid[b] + (int64_t)g * 16];
-                split3(-sz.x * (sz.y + kQ4Offset), z1, z2, z3);
-            }
-            const u32x4 v = {z1 | (z2 << 16), z1 | (z3 << 16), z2 | (z1 << 16), 0u};
-            zf[b] = __builtin_bit_cast(bf16x8, v);
+    for (int b = 0; b < 2; ++b)
+        grid[b] = (int64_t)min(rt0 + wr * 4 + 2 * b + (ml >> 4), w.RT - 1) * w.G * 16 + (ml & 15);
+
+    // minus s (16 + z) X: lane half h takes group g0 + 2 j + h, slots
+    // X1 Z1, X1 Z2, X2 Z1, X1 Z3, X2 Z2, X3 Z1; four pairs of groups at a time
+    // so that their loads are in flight together
+    constexpr int GP = 4;
+    for (int g0 = 0; g0 < w.G; g0 += 2 * GP) {
+        f32x2 sz[GP][2];
+        float xs[GP][TA];
+#pragma unroll
+        for (int j = 0; j < GP; ++j) {
+            const int g = min(g0 + 2 * j + h, w.G - 1);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) sz[j][b] = w.grid[grid[b] + (int64_t)g * 16];
+#pragma unroll
+            for (int a = 0; a < TA; ++a)
+                xs[j][a] = sums[(int64_t)g * lds_ + min(t0 + 32 * (wt * TA + a) + ml, T - 1)];
         }
 #pragma unroll
-        for (int a = 0; a < TA; ++a) {
-            const int t = min(t0 + 32 * (wt * TA + a) + ml, T - 1);
-            uint32_t x1 = 0, x2 = 0, x3 = 0;
-            if (g < w.G) split3(sums[(int64_t)g * lds_ + t], x1, x2, x3);
-            const u32x4 v = {x1 | (x1 << 16), x2 | (x1 << 16), x2 | (x3 << 16), 0u};
-            const bf16x8 xf = __builtin_bit_cast(bf16x8, v);
+        for (int j = 0; j < GP; ++j) {
+            const float in = g0 + 2 * j + h < w.G ? 1.f : 0.f;   // groups beyond G add nothing
+            bf16x8 zf[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) acc[a][b] = Bf16::mfma32(xf, zf[b], acc[a][b]);
+            for (int b = 0; b < 2; ++b) {
+                uint32_t z1, z2, z3;
+                split3(in * (-sz[j][b].x * (sz[j][b].y + kQ4Offset)), z1, z2, z3);
+                const u32x4 v = {z1 | (z2 << 16), z1 | (z3 << 16), z2 | (z1 << 16), 0u};
+                zf[b] = __builtin_bit_cast(bf16x8, v);
+            }
+#pragma unroll
+            for (int a = 0; a < TA; ++a) {
+                uint32_t x1, x2, x3;
+                split3(xs[j][a], x1, x2, x3);
+                const u32x4 v = {x1 | (x1 << 16), x2 | (x1 << 16), x2 | (x3 << 16), 0u};
+                const bf16x8 xf = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) acc[a][b] = Bf16::mfma32(xf, zf[b], acc[a][b]);
+            }
         }
     }
 
+    // Results through LDS, 32 tokens x 64 rows of a wave at a time, so that
+    // they leave as 16-byte stores; unaligned or cut rows leave one by one.
+    wait_direct_loads();
+    __syncthreads();
+    const bool whole = ((reinterpret_cast<uintptr_t>(y) & 15) | (ldy & 7)) == 0;
+    const int row0 = br * P::BR + wr * 64;
+    uint16_t* out = reinterpret_cast<uint16_t*>(lds) + wave * 32 * 72;   // pitch 72: 16-byte rows, spread banks
 #pragma unroll
-    for (int a = 0; a < TA; ++a)
+    for (int a = 0; a < TA; ++a) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int row = br * P::BR + wr * 64 + 32 * b + ml;
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = t0 + 32 * (wt * TA + a) + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (t < T && row < w.m) y[(int64_t)t * ldy + row] = X::down(acc[a][b][r]);
+            for (int r = 0; r < 16; ++r) out[(8 * (r >> 2) + 4 * h + (r & 3)) * 72 + 32 * b + ml] = X::down(acc[a][b][r]);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int tl = 8 * i + (lane >> 3), col = 8 * (lane & 7);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(out + tl * 72 + col);
+            const int t = t0 + 32 * (wt * TA + a) + tl, row = row0 + col;
+            if (t >= T) continue;
+            uint16_t* dst = y + (int64_t)t * ldy + row;
+            if (whole && row + 8 <= w.m) {
+                *reinterpret_cast<u32x4*>(dst) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (row + e < w.m) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
             }
         }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // --------------------------------------------------------------------- host
@@ -302,7 +379,7 @@ static void prompt_launch(const uint16_t* x, int64_t ldx, int64_t T, const Q4Lay
     typedef Prompt<TA, WR> P;
     const int nt = (int)ceil_div(T, P::BT), nr = (int)ceil_div(w.m, P::BR);
     launch(nullptr, KK_Q4_PROMPT, 2.0 * T * w.m * w.n, 0.0, k_q4_prompt<X, TA, WR>, dim3((unsigned)(nt * nr)),
-           dim3(P::THREADS), s, x, ldx, (int)T, w, sums, lds_, y, ldy, nt, nr);
+           dim3(128 * WR), s, x, ldx, (int)T, w, sums, lds_, y, ldy, nt, nr);
 }
 
 template <class X>
@@ -314,7 +391,8 @@ static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, v
     uint16_t* yp = static_cast<uint16_t*>(y);
     float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + p.sums);
     uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + p.copy);
-    const bool direct = w.n % 64 == 0 && ldx % 8 == 0 && aligned16(x);
+    // (the staging offsets of a token block are 31 bits)
+    const bool direct = w.n % 64 == 0 && ldx % 8 == 0 && ldx <= (1 << 21) && aligned16(x);
     launch(nullptr, KK_Q4_SUMS, 0.0, 2.0 * T * w.n, direct ? k_q4_sums<X, false> : k_q4_sums<X, true>,
            dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, w.G, sums, p.lds_, copy, p.ldc);
     if (!direct) xp = copy, ldx = p.ldc;
