@@ -133,30 +133,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_few(const uint16_t* __restric
     }
 }
 
-// ---------------------------------------------------------- input gradient
-//
-// dx[t, j] = sum_i dy[t, i] s_ig (c_ij - z_ig), g the group of column j: one
-// thread per entry, float32.
-template <class X>
-__global__ __launch_bounds__(256) void k_q4_grad(const uint16_t* __restrict__ dy, int64_t lddy, int T, Q4Layer w,
-                                                 uint16_t* __restrict__ dx, int64_t lddx)
-{
-    const int j = blockIdx.x * 64 + (threadIdx.x & 63);
-    const int64_t t = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6);
-    if (j >= w.n || t >= T) return;
-    const int kb = j >> 7, d = (j >> 6 & 1) * 2 + (j >> 3 & 1), q = j >> 4 & 3, e = j & 7;
-    const int shift = 4 * (e >> 1) + 16 * (e & 1);
-    const int g = min((j >> 6) / w.gb, w.G - 1);
-    float acc = 0.f;
-    for (int i = 0; i < w.m; ++i) {
-        const uint32_t c = w.codes[(((int64_t)(i >> 4) * w.KB + kb) * 4 + q) * 16 + (i & 15)][d];
-        const f32x2 sz = w.grid[((int64_t)(i >> 4) * w.G + g) * 16 + (i & 15)];
-        const float v = sz.x * ((float)(__builtin_rotateright32(c, 3 + shift) & 15u) - sz.y);
-        acc = fmaf(X::up(dy[t * lddy + i]), v, acc);
-    }
-    dx[t * lddx + j] = X::down(acc);
-}
-
 // rows x cols zeros of a 2-byte type
 __global__ __launch_bounds__(256) void k_q4_zero(uint16_t* __restrict__ y, int64_t ld, int64_t rows, int64_t cols)
 {
@@ -182,20 +158,6 @@ static void few_enqueue(const void* x, int64_t ldx, int64_t T, const Q4Layer& w,
         launch(nullptr, KK_Q4_FEW, 2.0 * tn * w.m * w.n, 0.0, k_q4_few<X, 1, 8>,
                dim3((unsigned)w.RT, (unsigned)ceil_div(tn, 16)), dim3(512), s, xp + t0 * ldx, ldx, (int)tn, w,
                yp + t0 * ldy, ldy);
-    }
-}
-
-template <class X>
-static void grad_enqueue(const void* dy, int64_t lddy, int64_t T, const Q4Layer& w, void* dx, int64_t lddx,
-                         hipStream_t s)
-{
-    const uint16_t* yp = static_cast<const uint16_t*>(dy);
-    uint16_t* xp = static_cast<uint16_t*>(dx);
-    for (int64_t t0 = 0; t0 < T; t0 += 65535 * 4) {
-        const int64_t tn = std::min<int64_t>(T - t0, 65535 * 4);
-        launch(nullptr, KK_Q4_GRAD, 2.0 * tn * w.m * w.n, 0.0, k_q4_grad<X>,
-               dim3((unsigned)ceil_div(w.n, 64), (unsigned)ceil_div(tn, 4)), dim3(256), s, yp + t0 * lddy, lddy, (int)tn,
-               w, xp + t0 * lddx, lddx);
     }
 }
 
@@ -289,8 +251,10 @@ int bakron_q4_linear(const void* x, int64_t ldx, int64_t tokens, int32_t type, c
 
 size_t bakron_q4_linear_grad_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int64_t group_size)
 {
-    (void)tokens, (void)m, (void)n, (void)group_size;
-    return 0;
+    if (!q4_shape_ok(m, n) || !q4_group_ok(group_size) || tokens <= 0 || tokens > BAKRON_Q4_MAX_TOKENS || m == 0 ||
+        n == 0)
+        return 0;
+    return bk::q4_grad_workspace_bytes(tokens, m);
 }
 
 int bakron_q4_linear_grad(const void* dy, int64_t lddy, int64_t tokens, int32_t type, const void* packed, int64_t m,
@@ -303,9 +267,9 @@ int bakron_q4_linear_grad(const void* dy, int64_t lddy, int64_t tokens, int32_t 
     if (c == 1) return BAKRON_SUCCESS;
     if (c == 2) return bk::q4_zero_enqueue(dx, lddx, tokens, n, stream) ? BAKRON_ERR_HIP : BAKRON_SUCCESS;
     const bk::Q4Layer w = bk::q4_layer(packed, bk::q4_dims(m, n, group_size));
-    if (type == BAKRON_Q4_BF16) bk::grad_enqueue<bk::Bf16>(dy, lddy, tokens, w, dx, lddx, stream);
-    else bk::grad_enqueue<bk::Fp16>(dy, lddy, tokens, w, dx, lddx, stream);
-    return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
+    return bk::q4_grad_enqueue(dy, lddy, tokens, type == BAKRON_Q4_BF16, w, dx, lddx, workspace, stream)
+               ? BAKRON_ERR_HIP
+               : BAKRON_SUCCESS;
 }
 
 }  // extern "C"

@@ -108,6 +108,13 @@ struct Bf16 {
     {
         return __builtin_bit_cast(uint16_t, (__bf16)v);   // to nearest, ties to even
     }
+    // two values, a in the low half
+    static __device__ __forceinline__ uint32_t down2(float a, float b)
+    {
+        typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+        const v2 v = {(__bf16)a, (__bf16)b};
+        return __builtin_bit_cast(uint32_t, v);
+    }
     static __device__ __forceinline__ f32x4 mfma16(vec a, vec b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -133,6 +140,12 @@ struct Fp16 {
     typedef f16x8 vec;
     static __device__ __forceinline__ float up(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
     static __device__ __forceinline__ uint16_t down(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+    static __device__ __forceinline__ uint32_t down2(float a, float b)
+    {
+        typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+        const v2 v = {(_Float16)a, (_Float16)b};
+        return __builtin_bit_cast(uint32_t, v);
+    }
     static __device__ __forceinline__ f32x4 mfma16(vec a, vec b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -203,5 +216,10 @@ constexpr int64_t kQ4Few = 64;   // up to so many tokens the few-token kernel ru
 size_t q4_prompt_workspace_bytes(int64_t T, int64_t n, int64_t G);
 int q4_prompt_enqueue(const void* x, int64_t ldx, int64_t T, bool bf16, const Q4Layer& w, void* y, int64_t ldy, void* ws,
                       hipStream_t s);
+
+// Input gradient (q4_grad.hip)
+size_t q4_grad_workspace_bytes(int64_t T, int64_t m);
+int q4_grad_enqueue(const void* dy, int64_t lddy, int64_t T, bool bf16, const Q4Layer& w, void* dx, int64_t lddx, void* ws,
+                    hipStream_t s);
 
 }  // namespace bk

@@ -25,7 +25,7 @@
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
-#include "q4.hpp"
+#include "q4_tile.hpp"
 
 namespace bk {
 
@@ -88,22 +88,14 @@ struct Prompt {
     static constexpr int BR = 64 * WR;                // rows of W of a workgroup
     static constexpr int XBUF = BT * 128;             // bytes of a 64-column chunk of x
     static constexpr int WBUF = BR * 64;              // bytes of a 128-column block of codes
-    static constexpr int AHEAD = TA == 4 ? 2 : 3;     // chunks in flight (LDS allows no more)
-    static constexpr int NX = AHEAD + 1, NW = AHEAD + 1;
+    static constexpr int AHEAD = TA == 4 ? 2 : 3;     // chunks in flight (LDS has no room for 3 of TA = 4)
+    static constexpr int NX = AHEAD + 1, NW = (AHEAD + 1) / 2 + 2;
     static constexpr int XLOADS = BT / 8 / (2 * WR);  // direct loads of a wave per chunk of x (8 tokens each)
     static constexpr int LOADS = XLOADS + 2;          // one of the grid and one of codes
     static constexpr int GBUF = BR * 8;               // bytes of the grid entries of a chunk
     static constexpr int CODES = NX * XBUF, GRID = CODES + NW * WBUF, LDS = GRID + NX * GBUF;
     static_assert(XLOADS >= 1, "a wave stages at least eight tokens");
 };
-
-// Waits until at most `left` loads of this wave are in flight (they complete
-// in order), then for the other waves.
-template <int LEFT>
-__device__ __forceinline__ void prompt_wait()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
-}
 
 // The direct loads of a workgroup, chunk by chunk: tokens [t0, t0 + BT) x
 // columns [64 c, 64 c + 64) of x (token r's 16-byte slot v holds columns
@@ -118,6 +110,7 @@ struct PromptStage {
     Rsrc x, codes, grid;
     uint32_t x_at[P::XLOADS], code_at[2], grid_at;
     int nchunk, KB, G, gb, wave;
+    int group = 0, in_group = 0;   // of the next chunk staged, and chunks of that group staged before it
     char* lds;
 
     __device__ __forceinline__ PromptStage(const uint16_t* xp, int64_t ldx, int t0, int T, const Q4Layer& w, int rt0,
@@ -139,14 +132,16 @@ struct PromptStage {
         for (int p = 0; p < 2; ++p) code_at[p] = (uint32_t)min(p * 2 * WR + wave, rts) * w.KB * 1024 + 16 * lane;
         grid_at = (uint32_t)min(2 * wave + (lane >> 5), rts) * w.G * 128 + 4 * (lane & 31);
     }
-    // bx, bw: the buffers of chunk c and of column block c / 2 + 1; part = c & 1
-    __device__ __forceinline__ void chunk(int c, int bx, int bw, int part) const
+    // called for c = 0, 1, ... in turn; bx, bw: the buffers of chunk c and of
+    // column block c / 2 + 1; part = c & 1
+    __device__ __forceinline__ void chunk(int c, int bx, int bw, int part)
     {
         const int cx = min(c, nchunk - 1);
         char* s = lds + bx * P::XBUF + wave * P::XLOADS * 1024;
 #pragma unroll
         for (int i = 0; i < P::XLOADS; ++i) load_lds16(x, x_at[i], 128 * cx, s + 1024 * i);
-        load_lds4(grid, grid_at, 128 * min(cx / gb, G - 1), lds + P::GRID + bx * P::GBUF + 256 * wave);
+        load_lds4(grid, grid_at, 128 * group, lds + P::GRID + bx * P::GBUF + 256 * wave);
+        if (++in_group == gb) in_group = 0, group = min(group + 1, G - 1);
         load_lds16(codes, code_at[part], 1024 * min((c >> 1) + 1, KB - 1),
                      lds + P::CODES + bw * P::WBUF + 1024 * (part * 2 * WR + wave));
     }
@@ -166,22 +161,8 @@ __device__ __forceinline__ void split3(float v, uint32_t& a, uint32_t& b, uint32
     c = Bf16::down(r - Bf16::up((uint16_t)b));
 }
 
-// Workgroups are dealt to the eight XCDs round-robin; each XCD gets a
-// contiguous run of the tile order below, so that its L2 sees few tokens and
-// rows at a time: runs of 4 token blocks share their rows of W.
-__device__ __forceinline__ void prompt_tile(int nt, int nr, int& bt, int& br)
-{
-    const unsigned total = (unsigned)nt * nr, b = blockIdx.x;
-    const unsigned per = total / 8, rest = total % 8, xcd = b % 8;
-    const unsigned p = xcd * per + min(xcd, rest) + b / 8;
-    const unsigned band = 4u * nr, g = p / band;
-    const unsigned h = min(4u, (unsigned)nt - 4 * g);
-    bt = (int)(4 * g + (p - g * band) % h);
-    br = (int)((p - g * band) / h);
-}
-
 template <class X, int TA, int WR>
-__global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
+__global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
                                                         const float* __restrict__ sums, int64_t lds_,
                                                         uint16_t* __restrict__ y, int64_t ldy, int nt, int nr)
 {
@@ -192,9 +173,9 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
     const int h = lane >> 5, ml = lane & 31;
     const int wt = wave / WR, wr = wave % WR;
     int bt, br;
-    prompt_tile(nt, nr, bt, br);
+    tile_of(nt, nr, bt, br);
     const int t0 = bt * P::BT, rt0 = br * (P::BR / 16);
-    const PromptStage<TA, WR> stage(x, ldx, t0, T, w, rt0, lds);
+    PromptStage<TA, WR> stage(x, ldx, t0, T, w, rt0, lds);
     stage.first();
 #pragma unroll
     for (int c = 0; c < P::AHEAD; ++c) stage.chunk(c, c, ((c >> 1) + 1) % P::NW, c & 1);
@@ -209,9 +190,9 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
 
     u32x4 codes[2][2];   // [row tile pair][unit h, h + 2]
     float step[2] = {1.f, 1.f};
-    int group = -1;
+    int left = 0;        // chunks left of the group whose steps the accumulators count in
     int bx = 0, bw = 0;                                  // buffers of chunk c and block kb
-    int px = P::AHEAD % P::NX, pw = (P::AHEAD / 2 + 1) % P::NW;   // and of the ones staged beside them
+    int px = P::AHEAD, pw = (P::AHEAD / 2 + 1) % P::NW;   // and of the ones staged beside them
     // the lane's parts of the LDS addresses
     uint32_t x_lane[4];
 #pragma unroll
@@ -224,7 +205,7 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
         for (int half = 0; half < 2; ++half) {
             const int c = 2 * kb + half;
             if (c < stage.nchunk) {
-                prompt_wait<(P::AHEAD - 1) * P::LOADS>();
+                tile_wait<(P::AHEAD - 1) * P::LOADS>();
                 stage.chunk(c + P::AHEAD, px, pw, (half + P::AHEAD) & 1);
                 px = px + 1 == P::NX ? 0 : px + 1;
                 if ((half + P::AHEAD) & 1) pw = pw + 1 == P::NW ? 0 : pw + 1;
@@ -236,9 +217,8 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
                         for (int u = 0; u < 2; ++u)
                             codes[b][u] = *reinterpret_cast<const u32x4*>(s + 2048 * b + 512 * u);
                 }
-                const int g = min(c / w.gb, w.G - 1);
-                if (g != group) {
-                    group = g;
+                if (left-- == 0) {
+                    left = w.gb - 1;
                     const char* s = lds + g_lane + bx * P::GBUF;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
@@ -251,18 +231,30 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
                             for (int r = 0; r < 16; ++r) acc[a][b][r] *= ratio;
                     }
                 }
+                // fragments of x PRE steps before their products: an LDS read
+                // takes longer than a step of a small TA
+                constexpr int PRE = TA == 4 ? 1 : 3;
                 const char* s = lds + bx * P::XBUF;
+                vec xf[PRE + 1][TA];
+#pragma unroll
+                for (int v = 0; v < PRE; ++v)
+#pragma unroll
+                    for (int a = 0; a < TA; ++a) xf[v][a] = *reinterpret_cast<const vec*>(s + x_lane[v] + 4096 * a);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
+                    if (v + PRE < 4) {
+#pragma unroll
+                        for (int a = 0; a < TA; ++a)
+                            xf[(v + PRE) % (PRE + 1)][a] =
+                                *reinterpret_cast<const vec*>(s + x_lane[(v + PRE) % 4] + 4096 * a);
+                    }
                     vec wf[2];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) wf[b] = X::codes(codes[b][v >> 1][2 * half + (v & 1)]);
 #pragma unroll
-                    for (int a = 0; a < TA; ++a) {
-                        const vec xf = *reinterpret_cast<const vec*>(s + x_lane[v] + 4096 * a);
+                    for (int a = 0; a < TA; ++a)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf, wf[b], acc[a][b]);
-                    }
+                        for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf[v % (PRE + 1)][a], wf[b], acc[a][b]);
                 }
                 bx = bx + 1 == P::NX ? 0 : bx + 1;
             }
@@ -319,37 +311,9 @@ __global__ __launch_bounds__(128 * WR) void k_q4_prompt(const uint16_t* __restri
         }
     }
 
-    // Results through LDS, 32 tokens x 64 rows of a wave at a time, so that
-    // they leave as 16-byte stores; unaligned or cut rows leave one by one.
     wait_direct_loads();
     __syncthreads();
-    const bool whole = ((reinterpret_cast<uintptr_t>(y) & 15) | (ldy & 7)) == 0;
-    const int row0 = br * P::BR + wr * 64;
-    uint16_t* out = reinterpret_cast<uint16_t*>(lds) + wave * 32 * 72;   // pitch 72: 16-byte rows, spread banks
-#pragma unroll
-    for (int a = 0; a < TA; ++a) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) out[(8 * (r >> 2) + 4 * h + (r & 3)) * 72 + 32 * b + ml] = X::down(acc[a][b][r]);
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tl = 8 * i + (lane >> 3), col = 8 * (lane & 7);
-            const u32x4 v = *reinterpret_cast<const u32x4*>(out + tl * 72 + col);
-            const int t = t0 + 32 * (wt * TA + a) + tl, row = row0 + col;
-            if (t >= T) continue;
-            uint16_t* dst = y + (int64_t)t * ldy + row;
-            if (whole && row + 8 <= w.m) {
-                *reinterpret_cast<u32x4*>(dst) = v;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (row + e < w.m) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-            }
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    tile_store<X, TA>(acc, 1.f, lds, t0 + 32 * wt * TA, T, br * P::BR + wr * 64, w.m, y, ldy);
 }
 
 // --------------------------------------------------------------------- host
@@ -371,6 +335,15 @@ static PromptWork prompt_work(int64_t T, int64_t n, int64_t G)
 }
 
 size_t q4_prompt_workspace_bytes(int64_t T, int64_t n, int64_t G) { return prompt_work(T, n, G).bytes; }
+
+template <class X>
+void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* copy, int64_t ldc, hipStream_t s)
+{
+    launch(nullptr, KK_Q4_SUMS, 0.0, 4.0 * T * n, k_q4_sums<X, true>, dim3((unsigned)ceil_div(T, 4)), dim3(256), s, x, ldx,
+           (int)T, n, 1, 0, static_cast<float*>(nullptr), (int64_t)0, copy, ldc);
+}
+template void copy_enqueue<Bf16>(const uint16_t*, int64_t, int64_t, int, uint16_t*, int64_t, hipStream_t);
+template void copy_enqueue<Fp16>(const uint16_t*, int64_t, int64_t, int, uint16_t*, int64_t, hipStream_t);
 
 template <class X, int TA, int WR>
 static void prompt_launch(const uint16_t* x, int64_t ldx, int64_t T, const Q4Layer& w, const float* sums, int64_t lds_,
