@@ -2,7 +2,7 @@
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
-#include "q4.hpp"
+#include "q4_few.hpp"
 
 namespace bk {
 
@@ -72,63 +72,42 @@ __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ 
 
 // ------------------------------------------- the linear layer, a few tokens
 //
-// y (T x m) for one tile of 16 rows of W and 16 NT tokens per workgroup: the
-// waves take the 128-column blocks in turn, tokens are the MFMA's rows and
-// rows of W its columns, so a lane's four accumulators share one (s, z).  A
-// product with ones gives the sums of x beside them.  Joined through LDS in
-// wave order (the result does not depend on timing).
-template <class X, int NT, int WAVES>
+// One workgroup per R tiles of 16 rows of W and 4 TQ tokens; its waves take the
+// column blocks in turn (FewSpan) and are joined through LDS in wave order,
+// so the result does not depend on timing.
+template <class X, int TQ, int R, int WAVES, int U, bool HALF>
 __global__ __launch_bounds__(64 * WAVES) void k_q4_few(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
                                                        uint16_t* __restrict__ y, int64_t ldy)
 {
-    typedef typename X::vec vec;
-    __shared__ float red[WAVES][NT * 4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int q = lane >> 4, r = lane & 15;
-    const int rt = blockIdx.x, t0 = blockIdx.y * 16 * NT;
-    const bool wide = ((reinterpret_cast<uintptr_t>(x) & 15) | (ldx & 7)) == 0;
-    const uint16_t* xr[NT];
+    typedef FewSpan<X, TQ, R, U, HALF> Span;
+    constexpr int NT = Span::NT, N = R * NT * 4;
+    constexpr int STAGE = WAVES * few_lds(TQ), JOIN = WAVES * N * 64 * 4;
+    __shared__ __align__(16) char lds[STAGE > JOIN ? STAGE : JOIN];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rt = blockIdx.x * R, t0 = blockIdx.y * 4 * TQ;
+    const uint16_t* xr[TQ];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xr[i] = x + (int64_t)min(t0 + 16 * i + r, T - 1) * ldx;
-    const vec ones = q4_ones<X>();
-    f32x4 acc[NT];
+    for (int t = 0; t < TQ; ++t) xr[t] = x + (int64_t)min(t0 + 4 * t + (lane >> 4), T - 1) * ldx;
+    const Q4Layer ws[1] = {w};
+    Span span(lds + wave * few_lds(TQ));
+    span.template rows<1>(ws, rt);
+    span.tokens(xr);
+    span.run(wave, WAVES, w.KB);
+    __syncthreads();   // the joining sums overwrite the staged tokens
+    float(*red)[N][64] = reinterpret_cast<float(*)[N][64]>(lds);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int kb = wave; kb < w.KB; kb += WAVES) {
-        const u32x4 c = w.codes[((int64_t)rt * w.KB + kb) * 64 + lane];
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int g = min((2 * kb + h) / w.gb, w.G - 1);
-            const f32x2 sz = w.grid[((int64_t)rt * w.G + g) * 16 + r];
-            const vec w0 = X::codes(c[2 * h]), w1 = X::codes(c[2 * h + 1]);
-            const int k = kb * 128 + 64 * h + 16 * q;
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                u32x4 xv[2];
-                q4_load16(xr[i] + k, w.n - k, wide, xv);
-                const vec a0 = __builtin_bit_cast(vec, xv[0]), a1 = __builtin_bit_cast(vec, xv[1]);
-                f32x4 t = {0.f, 0.f, 0.f, 0.f}, s = {0.f, 0.f, 0.f, 0.f};
-                t = X::mfma16(a0, w0, t);
-                s = X::mfma16(a0, ones, s);
-                t = X::mfma16(a1, w1, t);
-                s = X::mfma16(a1, ones, s);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][e] = fmaf(sz.x, fmaf(-(sz.y + kQ4Offset), s[e], t[e]), acc[i][e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave][4 * i + e][lane] = acc[i][e];
+            for (int e = 0; e < 4; ++e) red[wave][4 * (j * NT + i) + e][lane] = span.acc[j][i][e];
     __syncthreads();
-    for (int o = threadIdx.x; o < NT * 4 * 64; o += 64 * WAVES) {
+    for (int o = threadIdx.x; o < N * 64; o += 64 * WAVES) {
         const int e = o >> 6, l = o & 63;
         float v = 0.f;
 #pragma unroll
         for (int u = 0; u < WAVES; ++u) v += red[u][e][l];
-        const int t = t0 + 16 * (e >> 2) + 4 * (l >> 4) + (e & 3), row = rt * 16 + (l & 15);
+        const int t = t0 + 16 * ((e >> 2) % NT) + 4 * (l >> 4) + (e & 3), row = (rt + (e >> 2) / NT) * 16 + (l & 15);
         if (t < T && row < w.m) y[(int64_t)t * ldy + row] = X::down(v);
     }
 }
@@ -147,18 +126,42 @@ int q4_zero_enqueue(void* y, int64_t ld, int64_t rows, int64_t cols, hipStream_t
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
+#ifndef FW
+#define FW 8
+#define FU 2
+#define FR 1
+#endif
+template <class X, int TQ, int R, int WAVES, int U>
+static void few_launch(const uint16_t* x, int64_t ldx, int T, const Q4Layer& w, uint16_t* y, int64_t ldy, hipStream_t s)
+{
+    // HALF: a group ends inside a block of 128 columns
+    launch(nullptr, KK_Q4_FEW, 2.0 * T * w.m * w.n, 0.0,
+           w.gb % 2 ? k_q4_few<X, TQ, R, WAVES, U, true> : k_q4_few<X, TQ, R, WAVES, U, false>,
+           dim3((unsigned)ceil_div(w.RT, R), (unsigned)ceil_div(T, 4 * TQ)), dim3(64 * WAVES), s, x, ldx, T, w, y, ldy);
+}
+
+// Two row tiles per workgroup where that still gives every CU one: they share
+// the reads of x (16 tokens x 14336 x 4096: 12.0 us with one, 10.1 with two;
+// one token x 4096 x 14336, where two would leave half the CUs idle: 8.2 with
+// one, 10.2 with two).
+template <class X, int TQ, int U>
+static void few_rows(const uint16_t* x, int64_t ldx, int T, const Q4Layer& w, uint16_t* y, int64_t ldy, hipStream_t s)
+{
+    if (w.RT >= 512) few_launch<X, TQ, 2, 8, U>(x, ldx, T, w, y, ldy, s);
+    else few_launch<X, TQ, 1, 8, U>(x, ldx, T, w, y, ldy, s);
+}
+
 template <class X>
 static void few_enqueue(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, void* y, int64_t ldy, hipStream_t s)
 {
     const uint16_t* xp = static_cast<const uint16_t*>(x);
     uint16_t* yp = static_cast<uint16_t*>(y);
-    // grid.y holds at most 65535 token blocks
-    for (int64_t t0 = 0; t0 < T; t0 += 65535 * 16) {
-        const int64_t tn = std::min<int64_t>(T - t0, 65535 * 16);
-        launch(nullptr, KK_Q4_FEW, 2.0 * tn * w.m * w.n, 0.0, k_q4_few<X, 1, 8>,
-               dim3((unsigned)w.RT, (unsigned)ceil_div(tn, 16)), dim3(512), s, xp + t0 * ldx, ldx, (int)tn, w,
-               yp + t0 * ldy, ldy);
-    }
+    const int t = (int)T;
+    if (T <= 4) few_rows<X, 1, 2>(xp, ldx, t, w, yp, ldy, s);
+    else if (T <= 8) few_rows<X, 2, 2>(xp, ldx, t, w, yp, ldy, s);
+    else if (T <= 16) few_rows<X, 4, 2>(xp, ldx, t, w, yp, ldy, s);
+    else if (T <= 32) few_rows<X, 8, 1>(xp, ldx, t, w, yp, ldy, s);
+    else few_rows<X, 16, 1>(xp, ldx, t, w, yp, ldy, s);
 }
 
 }  // namespace bk
