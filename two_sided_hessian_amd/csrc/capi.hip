@@ -455,7 +455,7 @@ const char* kernel_name(int kind)
         "k_moment<true>", "k_prop_rows_far", "k_prop_rows_t_far", "k_prop_cols_far", "k_prop_cols_t_far",
         "k_ad_prep", "k_ad_quant", "k_ad_update", "k_f_update", "k_f_tile<4>",
         "k_q4_pack", "k_q4_pack_grid", "k_q4_zero", "k_q4_few", "k_q4_grad", "k_q4_router", "k_q4_moe_up",
-        "k_q4_moe_down", "k_q4_sums", "k_q4_prompt"};
+        "k_q4_moe_down", "k_q4_sums", "k_q4_prompt", "k_q4_join"};
     return (kind >= 0 && kind < KK_COUNT) ? names[kind] : "?";
 }
 

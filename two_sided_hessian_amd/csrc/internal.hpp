@@ -30,7 +30,7 @@ enum KernelKind {
     KK_K_SQNORM, KK_K_MOMENT, KK_K_MOMENT_W, KK_PROP_ROWS_FAR, KK_PROP_ROWS_T_FAR, KK_PROP_COLS_FAR,
     KK_PROP_COLS_T_FAR, KK_AD_PREP, KK_AD_QUANT, KK_AD_UPDATE, KK_F_UPDATE, KK_F_U_T,
     KK_Q4_PACK, KK_Q4_PACK_GRID, KK_Q4_ZERO, KK_Q4_FEW, KK_Q4_GRAD, KK_Q4_ROUTER, KK_Q4_MOE_UP, KK_Q4_MOE_DOWN,
-    KK_Q4_SUMS, KK_Q4_PROMPT, KK_COUNT
+    KK_Q4_SUMS, KK_Q4_PROMPT, KK_Q4_JOIN, KK_COUNT
 };
 static_assert(KK_COUNT <= BAKRON_MAX_KERNEL_KINDS, "kernel kinds exceed the ABI's statistics capacity");
 

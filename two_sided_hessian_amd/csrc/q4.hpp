@@ -100,6 +100,10 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     return (w & mask) | base;
 }
 
+// Rows may start at any 2-byte address: global loads and stores need no
+// alignment here.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
 // The activation types: raw 16-bit storage, MFMA forms and roundings.
 struct Bf16 {
     typedef bf16x8 vec;
@@ -166,26 +170,6 @@ struct Fp16 {
     static constexpr uint16_t kOne = 0x3C00;
 };
 
-// 16 consecutive activations p[0 .. 15] of a row that has `left` of them from
-// p on (zeros beyond); `wide`: p is 16-byte aligned.
-__device__ __forceinline__ void q4_load16(const uint16_t* __restrict__ p, int left, bool wide, u32x4 (&v)[2])
-{
-    if (wide && left >= 16) {
-        v[0] = *reinterpret_cast<const u32x4*>(p);
-        v[1] = *reinterpret_cast<const u32x4*>(p + 8);
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 8 * h + 2 * i;
-            const uint32_t lo = e < left ? p[e] : 0u;
-            const uint32_t hi = e + 1 < left ? p[e + 1] : 0u;
-            v[h][i] = lo | (hi << 16);
-        }
-}
-
 template <class X>
 __device__ __forceinline__ typename X::vec q4_ones()
 {
@@ -213,12 +197,12 @@ __device__ __forceinline__ void load_lds4(Rsrc r, uint32_t lane_at, uint32_t at,
 
 // Many tokens (q4_prompt.hip)
 constexpr int64_t kQ4Few = 64;   // up to so many tokens the few-token kernel runs
-size_t q4_prompt_workspace_bytes(int64_t T, int64_t n, int64_t G);
+size_t q4_prompt_workspace_bytes(int64_t T, int64_t m, int64_t n, int64_t G);
 int q4_prompt_enqueue(const void* x, int64_t ldx, int64_t T, bool bf16, const Q4Layer& w, void* y, int64_t ldy, void* ws,
                       hipStream_t s);
 
 // Input gradient (q4_grad.hip)
-size_t q4_grad_workspace_bytes(int64_t T, int64_t m);
+size_t q4_grad_workspace_bytes(int64_t T, int64_t m, int64_t n);
 int q4_grad_enqueue(const void* dy, int64_t lddy, int64_t T, bool bf16, const Q4Layer& w, void* dx, int64_t lddx, void* ws,
                     hipStream_t s);
 

@@ -21,9 +21,6 @@ namespace bk {
 // token's 256 bytes of a block and the four tokens of an instruction four
 // runs.  The LDS rows are a wave's own, so no barrier is involved.
 
-// Rows may start at any 2-byte address: global loads need no alignment here.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
 // Columns k .. k + 7 of a row of n, zeros beyond n; every load is made (of the
 // last column where there is none), so that all are in flight together.
 __device__ __forceinline__ u32x4 few_x_cut(const uint16_t* __restrict__ row, int k, int n)

@@ -16,9 +16,10 @@
 // a wave owns 32 TA tokens x 64 columns as TA x 2 MFMA tiles of 32 x 32.  dy
 // goes through LDS in chunks of 64 rows of W by direct loads.  Of each
 // chunk's 64 x 256 weights a thread expands 4 rows x 8 columns (four dwords of
-// codes, loaded two chunks ahead) and writes them to LDS transposed, four
-// rows of a column side by side as the MFMA takes them, one chunk ahead of
-// the products that read them, so one barrier per chunk orders everything.
+// codes) and writes them to LDS transposed, four rows of a column side by side
+// as the MFMA takes them, one chunk ahead of the products that read them, so
+// one barrier per chunk orders everything.  Few tiles share out their rows of
+// W over several workgroups, joined by k_q4_join.
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
@@ -33,10 +34,17 @@ struct Grad {
     static constexpr int XBUF = BT * 128;           // bytes of a 64-row chunk of dy
     static constexpr int PITCH = 144;               // bytes of a column's 64 rows in LDS: 9 x 16, spreads the banks
     static constexpr int WBUF = BJ * PITCH;
-    static constexpr int AHEAD = TA == 4 ? 1 : 2;   // chunks of dy in flight (a chunk of TA = 4 outlasts a load)
+    // Small tiles: a chunk is shorter than a load's latency, so codes and grids
+    // come by direct loads too, some chunks ahead.  TA = 4: a chunk outlasts a
+    // load, and LDS is what bounds it; codes and grids come to registers.
+    static constexpr bool RAW = TA < 4;
+    static constexpr int AHEAD = TA == 4 ? 1 : TA == 2 ? 2 : 3;
     static constexpr int NX = AHEAD + 1;
     static constexpr int XLOADS = BT / 64;
-    static constexpr int WEIGHTS = NX * XBUF, LDS = WEIGHTS + 2 * WBUF;
+    static constexpr int LOADS = XLOADS + (RAW ? 2 : 0);
+    static constexpr int TILE = 1040;               // bytes of a code block in LDS: 65 x 16, spreads the banks
+    static constexpr int RAWBUF = RAW ? 8 * TILE + 2048 : 0;   // codes, then grids [row tile][64 columns][16] of a chunk
+    static constexpr int WEIGHTS = NX * XBUF, RAWS = WEIGHTS + 2 * WBUF, LDS = RAWS + NX * RAWBUF;
 };
 
 // Eight bytes to LDS byte address at + OFFSET.  Written out because the
@@ -49,9 +57,19 @@ __device__ __forceinline__ void write64(uint32_t at, uint32_t lo, uint32_t hi)
     asm volatile("ds_write_b64 %0, %1 offset:%2" ::"v"(at), "v"(v), "n"(OFFSET));
 }
 
+// What a thread of a chunk expands: 4 rows x 8 columns, as loaded.
+struct GradRaw {
+    uint32_t c[4];
+    f32x4 g[2];   // (s, z) of rows 0, 1 and 2, 3
+};
+
+// blockIdx.y of gridDim.y shares the rows of W; more than one of them writes
+// float32 partial sums, in units, to part[blockIdx.y][token][column] instead
+// of dx.
 template <class X, int TA>
 __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy, int64_t lddy, int T, Q4Layer w,
-                                                 uint16_t* __restrict__ dx, int64_t lddx, int nt, int nj)
+                                                 uint16_t* __restrict__ dx, int64_t lddx, int nt, int nj,
+                                                 float* __restrict__ part)
 {
     typedef Grad<TA> P;
     typedef typename X::vec vec;
@@ -62,7 +80,8 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
     int bt, bj;
     tile_of(nt, nj, bt, bj);
     const int t0 = bt * P::BT, j0 = bj * P::BJ;
-    const int nchunk = (w.m + 63) / 64;
+    const int all = (w.m + 63) / 64;
+    const int c0 = all * blockIdx.y / gridDim.y, c1 = all * (blockIdx.y + 1) / gridDim.y;   // this workgroup's chunks
     const float unit = *w.unit > 0.f ? *w.unit : 1.f;
     const float down = 1.f / unit;
 
@@ -74,10 +93,22 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
         const int r = 8 * (wave * P::XLOADS + i) + (lane >> 3);
         x_at[i] = (uint32_t)(min(r, T - 1 - t0) * lddy * 2) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
     }
-    auto stage = [&](int c, int bx) {
-#pragma unroll
-        for (int i = 0; i < P::XLOADS; ++i)
-            load_lds16(x, x_at[i], 128 * min(c, nchunk - 1), lds + bx * P::XBUF + (wave * P::XLOADS + i) * 1024);
+    // load i of chunk c of dy, or (i = XLOADS, XLOADS + 1) of the codes and grids
+    // of chunk c + 1, which is expanded a chunk before its products; row tiles
+    // beyond RT repeat the last (dy is zero there)
+    const uint32_t g_at = 128 * min((4 * bj + 2 * (wave & 1) + (lane >> 5)) / w.gb, w.G - 1) + 4 * (lane & 31);
+    auto stage = [&](int i, int c, int buf) {
+        if (i < P::XLOADS) {
+            load_lds16(x, x_at[i], 128 * min(c, c1 - 1), lds + buf * P::XBUF + (wave * P::XLOADS + i) * 1024);
+        } else if (i == P::XLOADS) {
+            const int64_t rt = min(4 * (c + 1) + (wave & 3), w.RT - 1);
+            load_lds16(buffer_of(w.codes + (rt * w.KB + min(2 * bj + (wave >> 2), w.KB - 1)) * 64, 1024), 16 * lane, 0,
+                       lds + P::RAWS + buf * P::RAWBUF + wave * P::TILE);
+        } else {
+            const int64_t rt = min(4 * (c + 1) + (wave >> 1), w.RT - 1);
+            load_lds4(buffer_of(w.grid + rt * w.G * 16, 0x7FFFFFFFu), g_at, 0,
+                      lds + P::RAWS + buf * P::RAWBUF + 8 * P::TILE + 256 * wave);
+        }
     };
 
     // expansion: rows 4 a .. 4 a + 3 of the chunk, the eight columns of dword d
@@ -86,44 +117,43 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
     const int kb = min(2 * bj + (wave >> 2), w.KB - 1);
     const int g = min((2 * kb + (d >> 1)) / w.gb, w.G - 1);
     const int col = 128 * (wave >> 2) + 64 * (d >> 1) + 16 * q + 8 * (d & 1);
-    const uint32_t* code_at = reinterpret_cast<const uint32_t*>(w.codes + (int64_t)kb * 64 + 16 * q) + 16 * (a4 & 3) + d;
-    const f32x4* grid_at = reinterpret_cast<const f32x4*>(w.grid + (int64_t)g * 16 + 4 * (a4 & 3));
+    const char* code_base = reinterpret_cast<const char*>(w.codes + (int64_t)kb * 64 + 16 * q);
+    const char* grid_base = reinterpret_cast<const char*>(w.grid);
+    const uint32_t code_lane = 64 * (a4 & 3) + 4 * d, grid_lane = 128 * g + 32 * (a4 & 3);
     const uint32_t w_at = (uint32_t)(uintptr_t)(lds_ptr)lds + P::WEIGHTS + col * P::PITCH + 8 * a4;
-    struct Raw {
-        uint32_t c[4];
-        f32x4 g[2];
-    };
-    auto fetch = [&](int c, Raw& v) {
-        const int64_t rt = min(4 * min(c, nchunk - 1) + (a4 >> 2), w.RT - 1);
+    auto fetch = [&](int c, GradRaw& v) {
+        const int rt = min(4 * min(c, c1 - 1) + (a4 >> 2), w.RT - 1);
+        const char* codes = code_base + ((int64_t)rt * w.KB * 1024 + code_lane);
+        const char* grid = grid_base + ((int64_t)rt * w.G * 128 + grid_lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v.c[i] = code_at[rt * w.KB * 256 + 4 * i];
-        v.g[0] = grid_at[rt * w.G * 8];
-        v.g[1] = grid_at[rt * w.G * 8 + 1];
+        for (int i = 0; i < 4; ++i) v.c[i] = *reinterpret_cast<const uint32_t*>(codes + 16 * i);
+        v.g[0] = *reinterpret_cast<const f32x4*>(grid);
+        v.g[1] = *reinterpret_cast<const f32x4*>(grid + 16);
     };
-    auto expand = [&](const Raw& v, int buf) {
-        float f[4][8];
+    const uint32_t raw_code = P::RAWS + (4 * (wave >> 2) + (a4 >> 2)) * P::TILE + 256 * q + 64 * (a4 & 3) + 4 * d;
+    const uint32_t raw_grid = P::RAWS + 8 * P::TILE + 512 * (a4 >> 2) + 128 * (2 * (wave >> 2) + (d >> 1)) + 32 * (a4 & 3);
+    auto take = [&](int buf, GradRaw& v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v.c[i] = *reinterpret_cast<const uint32_t*>(lds + raw_code + buf * P::RAWBUF + 16 * i);
+        v.g[0] = *reinterpret_cast<const f32x4*>(lds + raw_grid + buf * P::RAWBUF);
+        v.g[1] = *reinterpret_cast<const f32x4*>(lds + raw_grid + buf * P::RAWBUF + 16);
+    };
+    // column pair p of the four rows
+    auto expand = [&](const GradRaw& v, int p, uint32_t s) {
+        float f[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float s = v.g[i >> 1][2 * (i & 1)] * down, b = -s * v.g[i >> 1][2 * (i & 1) + 1];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                // two codes in bytes 0 and 2, which convert in one instruction
-                // each (the empty statement hides that they are nibbles)
-                uint32_t two = __builtin_rotateright32(v.c[i], 3 + 4 * p) & 0x000F000Fu;
-                asm("" : "+v"(two));
-                f[i][2 * p] = fmaf(s, (float)(two & 0xFFu), b);
-                f[i][2 * p + 1] = fmaf(s, (float)(two >> 16 & 0xFFu), b);
-            }
+            const float step = v.g[i >> 1][2 * (i & 1)] * down, b = -step * v.g[i >> 1][2 * (i & 1) + 1];
+            // two codes in bytes 0 and 2, which convert in one instruction each
+            // (the empty statement hides that they are nibbles)
+            uint32_t two = __builtin_rotateright32(v.c[i], 3 + 4 * p) & 0x000F000Fu;
+            asm("" : "+v"(two));
+            f[i][0] = fmaf(step, (float)(two & 0xFFu), b);
+            f[i][1] = fmaf(step, (float)(two >> 16 & 0xFFu), b);
         }
-        const uint32_t s = w_at + buf * P::WBUF;
-        write64<0 * P::PITCH>(s, X::down2(f[0][0], f[1][0]), X::down2(f[2][0], f[3][0]));
-        write64<1 * P::PITCH>(s, X::down2(f[0][1], f[1][1]), X::down2(f[2][1], f[3][1]));
-        write64<2 * P::PITCH>(s, X::down2(f[0][2], f[1][2]), X::down2(f[2][2], f[3][2]));
-        write64<3 * P::PITCH>(s, X::down2(f[0][3], f[1][3]), X::down2(f[2][3], f[3][3]));
-        write64<4 * P::PITCH>(s, X::down2(f[0][4], f[1][4]), X::down2(f[2][4], f[3][4]));
-        write64<5 * P::PITCH>(s, X::down2(f[0][5], f[1][5]), X::down2(f[2][5], f[3][5]));
-        write64<6 * P::PITCH>(s, X::down2(f[0][6], f[1][6]), X::down2(f[2][6], f[3][6]));
-        write64<7 * P::PITCH>(s, X::down2(f[0][7], f[1][7]), X::down2(f[2][7], f[3][7]));
+        write64<0>(s + 2 * p * P::PITCH, X::down2(f[0][0], f[1][0]), X::down2(f[2][0], f[3][0]));
+        write64<P::PITCH>(s + 2 * p * P::PITCH, X::down2(f[0][1], f[1][1]), X::down2(f[2][1], f[3][1]));
     };
 
     f32x16 acc[TA][2];
@@ -134,77 +164,135 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
-    Raw raw;
-    fetch(0, raw);
-#pragma unroll
-    for (int c = 0; c < P::AHEAD; ++c) stage(c, c);
-    expand(raw, 0);
-    fetch(1, raw);
     uint32_t x_lane[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) x_lane[v] = 128 * (32 * wt * TA + ml) + 16 * ((2 * v + h) ^ ((ml >> 1) & 7));
     const uint32_t b_lane = P::WEIGHTS + (64 * wj + ml) * P::PITCH + 16 * h;
     int bx = 0, px = P::AHEAD % P::NX;
-    for (int c = 0; c < nchunk; ++c) {
+    // Chunk c: its products, and the expansion of chunk c + 1 (from raw) between
+    // them, while chunk c + 2 is fetched or further ones staged.
+    auto chunk = [&](int c, int buf, GradRaw& raw, GradRaw& next) {
         // chunk c of dy and the weights of chunk c are in LDS for every wave,
         // and every wave is done with chunk c - 1
-        tile_wait<(P::AHEAD - 1) * P::XLOADS>();
-        Raw now = raw;
-        fetch(c + 2, raw);
-        stage(c + P::AHEAD, px);
-        px = px + 1 == P::NX ? 0 : px + 1;
+        tile_wait<(P::AHEAD - 1) * P::LOADS>();
+        if (P::RAW) take(bx, raw);
+        else fetch(c + 2, next);
         const char* xs = lds + bx * P::XBUF;
-        const char* ws = lds + b_lane + (c & 1) * P::WBUF;
-        expand(now, (c + 1) & 1);
+        const char* ws = lds + b_lane + buf * P::WBUF;
+        const uint32_t to = w_at + (buf ^ 1) * P::WBUF;
+        vec wf[2][2], xf[2][TA];
+        auto read = [&](int v) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) wf[v & 1][b] = *reinterpret_cast<const vec*>(ws + 32 * v + 32 * b * P::PITCH);
+#pragma unroll
+            for (int a = 0; a < TA; ++a) xf[v & 1][a] = *reinterpret_cast<const vec*>(xs + x_lane[v] + 4096 * a);
+        };
+        read(0);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            vec wf[2];
+            if (v < 3) read(v + 1);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) wf[b] = *reinterpret_cast<const vec*>(ws + 32 * v + 32 * b * P::PITCH);
+            for (int i = v; i < P::LOADS; i += 4) stage(i, c + P::AHEAD, px);
+            expand(raw, v, to);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int a = 0; a < TA; ++a) {
-                const vec xf = *reinterpret_cast<const vec*>(xs + x_lane[v] + 4096 * a);
+            for (int a = 0; a < TA; ++a)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf, wf[b], acc[a][b]);
-            }
+                for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf[v & 1][a], wf[v & 1][b], acc[a][b]);
         }
+        px = px + 1 == P::NX ? 0 : px + 1;
         bx = bx + 1 == P::NX ? 0 : bx + 1;
+    };
+
+    GradRaw raw[2];
+    fetch(c0, raw[0]);
+    if (!P::RAW) fetch(c0 + 1, raw[1]);
+#pragma unroll
+    for (int c = 0; c < P::AHEAD; ++c)
+#pragma unroll
+        for (int i = 0; i < P::LOADS; ++i) stage(i, c0 + c, c);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) expand(raw[0], p, w_at);
+    for (int c = c0; c < c1; c += 2) {
+        chunk(c, 0, raw[1], raw[0]);
+        if (c + 1 < c1) chunk(c + 1, 1, raw[0], raw[1]);
     }
     wait_direct_loads();
+    const int tw = t0 + 32 * wt * TA, jw = j0 + wj * 64;
+    if (gridDim.y > 1) {
+        float* p = part + (int64_t)blockIdx.y * T * w.n;
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int t = tw + 32 * a + 8 * (r >> 2) + 4 * h + (r & 3), j = jw + 32 * b + ml;
+                    if (t < T && j < w.n) p[(int64_t)t * w.n + j] = acc[a][b][r];
+                }
+        return;
+    }
     __syncthreads();
-    tile_store<X, TA>(acc, unit, lds, t0 + 32 * wt * TA, T, j0 + wj * 64, w.n, dx, lddx);
+    tile_store<X, TA>(acc, unit, lds + wave * kStoreBytes, tw, T, jw, w.n, dx, lddx);
 }
 
 // --------------------------------------------------------------------- host
 
-size_t q4_grad_workspace_bytes(int64_t T, int64_t m) { return align_up((size_t)T * ceil_div(m, 64) * 64 * 2); }
+struct GradPlan {
+    int TA, splits;
+    int64_t ldc;
+    size_t part, bytes;
+};
+
+static GradPlan grad_plan(int64_t T, int64_t m, int64_t n)
+{
+    GradPlan p;
+    const int64_t nj = ceil_div(n, 256);
+    // the largest tiles that still give every CU about one, as in the layer
+    p.TA = ceil_div(T, 256) * nj >= 224 ? 4 : ceil_div(T, 128) * nj >= 192 ? 2 : 1;
+    // small problems: a workgroup per CU, down to two chunks of 64 rows each
+    p.splits = 1;
+    if (p.TA == 1) {
+        const int64_t tiles = ceil_div(T, 64) * nj;
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({16, 256 / tiles, ceil_div(m, 64) / 2}));
+    }
+    p.ldc = ceil_div(m, 64) * 64;
+    p.part = align_up((size_t)T * p.ldc * 2);
+    p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * T * n * 4) : 0);
+    return p;
+}
+
+size_t q4_grad_workspace_bytes(int64_t T, int64_t m, int64_t n) { return grad_plan(T, m, n).bytes; }
 
 template <class X, int TA>
 static void grad_launch(const uint16_t* dy, int64_t lddy, int64_t T, const Q4Layer& w, uint16_t* dx, int64_t lddx,
-                        hipStream_t s)
+                        int splits, float* part, hipStream_t s)
 {
     typedef Grad<TA> P;
     const int nt = (int)ceil_div(T, P::BT), nj = (int)ceil_div(w.n, P::BJ);
-    launch(nullptr, KK_Q4_GRAD, 2.0 * T * w.m * w.n, 0.0, k_q4_grad<X, TA>, dim3((unsigned)(nt * nj)), dim3(512), s, dy,
-           lddy, (int)T, w, dx, lddx, nt, nj);
+    launch(nullptr, KK_Q4_GRAD, 2.0 * T * w.m * w.n, 0.0, k_q4_grad<X, TA>, dim3((unsigned)(nt * nj), (unsigned)splits),
+           dim3(512), s, dy, lddy, (int)T, w, dx, lddx, nt, nj, part);
 }
 
 template <class X>
 static int grad_run(const void* dy, int64_t lddy, int64_t T, const Q4Layer& w, void* dx, int64_t lddx, void* ws,
                     hipStream_t s)
 {
+    const GradPlan p = grad_plan(T, w.m, w.n);
     const uint16_t* yp = static_cast<const uint16_t*>(dy);
     uint16_t* xp = static_cast<uint16_t*>(dx);
+    uint16_t* copy = static_cast<uint16_t*>(ws);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+    // (the staging offsets of a token block are 31 bits)
     if (w.m % 64 || lddy % 8 || lddy > (1 << 21) || !aligned16(dy)) {
-        const int64_t ldc = ceil_div(w.m, 64) * 64;
-        copy_enqueue<X>(yp, lddy, T, w.m, static_cast<uint16_t*>(ws), ldc, s);
-        yp = static_cast<const uint16_t*>(ws);
-        lddy = ldc;
+        copy_enqueue<X>(yp, lddy, T, w.m, copy, p.ldc, s);
+        yp = copy;
+        lddy = p.ldc;
     }
-    const int64_t nj = ceil_div(w.n, 256);
-    if (ceil_div(T, 256) * nj >= 256) grad_launch<X, 4>(yp, lddy, T, w, xp, lddx, s);
-    else if (ceil_div(T, 128) * nj >= 128) grad_launch<X, 2>(yp, lddy, T, w, xp, lddx, s);
-    else grad_launch<X, 1>(yp, lddy, T, w, xp, lddx, s);
+    if (p.TA == 4) grad_launch<X, 4>(yp, lddy, T, w, xp, lddx, 1, part, s);
+    else if (p.TA == 2) grad_launch<X, 2>(yp, lddy, T, w, xp, lddx, 1, part, s);
+    else grad_launch<X, 1>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
+    if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.n, w.unit, xp, lddx, s);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -5,34 +5,45 @@
 // The first sum runs on 16-bit MFMAs with exact operands.  Its accumulators
 // are kept in units of the current group's step: on entering group g they are
 // multiplied by s_{g-1} / s_g, one float32 multiplication each, so a group
-// needs no second set of accumulators.  The second sum is a product over the
-// groups alone (n / 128 terms): X and s (16 + z) are split into three
-// bfloat16 terms each and the six leading products of every group are six K
-// slots of the same MFMAs, run once at the end (error 2^-24 of a term).
-//
-// k_q4_sums makes X (float32, group-major) in a pass over x of its own, and
-// with it, where x's rows are not 16-byte aligned or n is not a multiple of
-// 64, a padded copy that the product can stage directly.
+// needs no second set of accumulators.  The zero points enter in one of two
+// ways:
+//   * large tiles: the second sum is a product over the groups alone (n / 128
+//     terms).  X and s (16 + z) are split into three bfloat16 terms each and the
+//     six leading products of every group are six K slots of the same MFMAs,
+//     run once at the end (error 2^-24 of a term).  k_q4_sums makes X in a pass
+//     over x of its own.
+//   * small tiles, which do not fill the matrix cores: X comes from a product
+//     with ones beside the others, and is taken off when its group ends.
+// Where x's rows are not 16-byte aligned or n is not a multiple of 64, that
+// pass also makes a padded copy that the product can stage directly.
 //
 // k_q4_prompt: a workgroup of 2 x WR waves computes 64 TA tokens x 64 WR rows
 // of W; a wave owns 32 TA tokens x 64 rows as TA x 2 MFMA tiles of 32 x 32
 // (v_mfma_f32_32x32x16, tokens are its rows).  x goes through LDS in chunks
-// of 64 columns by direct loads, 16-byte slots permuted so that
-// fragment reads spread over the banks.  Codes come through LDS as they are
-// (a quarter of the bytes of 16-bit weights); each wave expands its fragments
-// in registers, 7 operations per 8 codes.  Two or three chunks are in flight
-// at any time: a chunk's products take less than a load's latency.
+// of 64 columns by direct loads, 16-byte slots permuted so that fragment
+// reads spread over the banks.  Codes come through LDS as they are (a quarter
+// of the bytes of 16-bit weights); each wave expands its fragments in
+// registers, 7 operations per 8 codes.  Two or three chunks are in flight at
+// any time: a chunk's products take less than a load's latency.  Few tiles
+// share out their columns over several workgroups, joined by k_q4_join.
+//
+// Measured (8192 tokens, 8192 x 8192, one grid per row): 2840 cycles a chunk
+// against 2048 of MFMAs, at the 1.9 GHz that the power limit leaves; with TA =
+// 2, 1690 against 1024: LDS reads, expansion and staging add about 180, 150
+// and 220.
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
+#include "q4_few.hpp"
 #include "q4_tile.hpp"
 
 namespace bk {
 
 // ---------------------------------------------------------------- group sums
 //
-// One wave per token: lanes sum 8 columns, 8 lanes a 64-column half, and the
-// halves of a group are added in order.  Columns n .. np - 1 of the copy are
+// One wave per token: lanes sum 8 columns, 8 lanes a 64-column half (the loads
+// of four spans of 512 columns together), and the halves of a group are added
+// in order.  COPY: the row goes to `copy` too, columns n .. 64 ceil(n / 64) - 1
 // zero.
 constexpr int kSumsHalves = BAKRON_MAX_DIM / 64;
 
@@ -45,33 +56,32 @@ __global__ __launch_bounds__(256) void k_q4_sums(const uint16_t* __restrict__ x,
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * 4 + wave;
     const int halves = (n + 63) / 64;
-    if (t < T) {
-        const uint16_t* row = x + t * ldx;
-        for (int c0 = 0; c0 < 64 * halves; c0 += 512) {
-            const int c = c0 + 8 * lane;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (!COPY) {
-                if (c < n) v = *reinterpret_cast<const u32x4*>(row + c);
-            } else {
+    if (t >= T) return;
+    const uint16_t* row = x + t * ldx;
+    constexpr int U = 4;
+    for (int c0 = 8 * lane; c0 < 64 * halves; c0 += 512 * U) {
+        u32x4 v[U];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = c + 2 * i < n ? row[c + 2 * i] : 0u;
-                    const uint32_t b = c + 2 * i + 1 < n ? row[c + 2 * i + 1] : 0u;
-                    v[i] = a | (b << 16);
-                }
-                if (c < 64 * halves) *reinterpret_cast<u32x4*>(copy + t * ldc + c) = v;
-            }
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + 512 * u;
+            v[u] = u32x4{0u, 0u, 0u, 0u};
+            if (c + 8 <= n) v[u] = *reinterpret_cast<const u32x4_any*>(row + c);
+            else if (COPY && c < n) v[u] = few_x_cut(row, c, n);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + 512 * u;
+            if (COPY && c < 64 * halves) *reinterpret_cast<u32x4*>(copy + t * ldc + c) = v[u];
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s += X::up((uint16_t)v[i]) + X::up((uint16_t)(v[i] >> 16));
+            for (int i = 0; i < 4; ++i) s += X::up((uint16_t)v[u][i]) + X::up((uint16_t)(v[u][i] >> 16));
             s += __shfl_xor(s, 1);
             s += __shfl_xor(s, 2);
             s += __shfl_xor(s, 4);
             if ((lane & 7) == 0 && c < 64 * halves) half[wave][c >> 6] = s;
         }
     }
-    __syncthreads();
-    if (t >= T) return;
+    __builtin_amdgcn_wave_barrier();   // (a wave's own LDS row)
     for (int g = lane; g < G; g += 64) {
         const int h0 = g * gb, h1 = g == G - 1 ? halves : h0 + gb;   // gb may exceed the halves when G is 1
         float s = 0.f;
@@ -109,17 +119,18 @@ struct PromptStage {
     typedef Prompt<TA, WR> P;
     Rsrc x, codes, grid;
     uint32_t x_at[P::XLOADS], code_at[2], grid_at;
-    int nchunk, KB, G, gb, wave;
-    int group = 0, in_group = 0;   // of the next chunk staged, and chunks of that group staged before it
+    int chunks, blocks, G, gb, wave;   // the first chunk and block past this workgroup's
+    int group, in_group;               // of the next chunk staged, and chunks of that group before it
     char* lds;
 
     __device__ __forceinline__ PromptStage(const uint16_t* xp, int64_t ldx, int t0, int T, const Q4Layer& w, int rt0,
-                                           char* lds_)
+                                           int kb0, int kb1, char* lds_)
         : x(buffer_of(xp + t0 * ldx, 0x7FFFFFFFu)),
           codes(buffer_of(w.codes + (int64_t)rt0 * w.KB * 64, 0x7FFFFFFFu)),
           grid(buffer_of(w.grid + (int64_t)rt0 * w.G * 16, 0x7FFFFFFFu)),
-          nchunk((w.n + 63) / 64), KB(w.KB), G(w.G), gb(w.gb),
-          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lds(lds_)
+          chunks(min((w.n + 63) / 64, 2 * kb1)), blocks(kb1), G(w.G), gb(w.gb),
+          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), group(min(2 * kb0 / w.gb, w.G - 1)),
+          in_group(2 * kb0 % w.gb), lds(lds_)
     {
         const int lane = threadIdx.x & 63;
         const int rts = w.RT - 1 - rt0;
@@ -132,23 +143,30 @@ struct PromptStage {
         for (int p = 0; p < 2; ++p) code_at[p] = (uint32_t)min(p * 2 * WR + wave, rts) * w.KB * 1024 + 16 * lane;
         grid_at = (uint32_t)min(2 * wave + (lane >> 5), rts) * w.G * 128 + 4 * (lane & 31);
     }
-    // called for c = 0, 1, ... in turn; bx, bw: the buffers of chunk c and of
-    // column block c / 2 + 1; part = c & 1
-    __device__ __forceinline__ void chunk(int c, int bx, int bw, int part)
+    // Quarter v of the loads of chunk c, called for c = 2 kb0, 2 kb0 + 1, ... in
+    // turn; bx, bw: the buffers of chunk c and of column block c / 2 + 1; part =
+    // c & 1.
+    __device__ __forceinline__ void quarter(int v, int c, int bx, int bw, int part)
     {
-        const int cx = min(c, nchunk - 1);
+        constexpr int PER = (P::XLOADS + 3) / 4;
         char* s = lds + bx * P::XBUF + wave * P::XLOADS * 1024;
 #pragma unroll
-        for (int i = 0; i < P::XLOADS; ++i) load_lds16(x, x_at[i], 128 * cx, s + 1024 * i);
-        load_lds4(grid, grid_at, 128 * group, lds + P::GRID + bx * P::GBUF + 256 * wave);
-        if (++in_group == gb) in_group = 0, group = min(group + 1, G - 1);
-        load_lds16(codes, code_at[part], 1024 * min((c >> 1) + 1, KB - 1),
-                     lds + P::CODES + bw * P::WBUF + 1024 * (part * 2 * WR + wave));
+        for (int i = v * PER; i < (v + 1) * PER; ++i)
+            if (i < P::XLOADS) load_lds16(x, x_at[i], 128 * min(c, chunks - 1), s + 1024 * i);
+        if (v == 2) {
+            load_lds4(grid, grid_at, 128 * group, lds + P::GRID + bx * P::GBUF + 256 * wave);
+            if (++in_group == gb) in_group = 0, group = min(group + 1, G - 1);
+        }
+        if (v == 3)
+            load_lds16(codes, code_at[part], 1024 * min((c >> 1) + 1, blocks - 1),
+                       lds + P::CODES + bw * P::WBUF + 1024 * (part * 2 * WR + wave));
     }
-    __device__ __forceinline__ void first() const
+    // the codes of block kb0
+    __device__ __forceinline__ void first(int kb0) const
     {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) load_lds16(codes, code_at[p], 0, lds + P::CODES + 1024 * (p * 2 * WR + wave));
+        for (int p = 0; p < 2; ++p)
+            load_lds16(codes, code_at[p], 1024 * kb0, lds + P::CODES + 1024 * (p * 2 * WR + wave));
     }
 };
 
@@ -161,10 +179,71 @@ __device__ __forceinline__ void split3(float v, uint32_t& a, uint32_t& b, uint32
     c = Bf16::down(r - Bf16::up((uint16_t)b));
 }
 
+// acc -= s (16 + z) X for the wave's tiles.  32 groups at a time, X of the
+// workgroup's tokens and the grids of its rows come to LDS together (one round
+// trip); lane half h takes group 2 j + h, slots X1 Z1, X1 Z2, X2 Z1, X1 Z3,
+// X2 Z2, X3 Z1.
 template <class X, int TA, int WR>
+__device__ __forceinline__ void zero_points(f32x16 (&acc)[TA][2], const Q4Layer& w, int rt0,
+                                            const float* __restrict__ sums, int64_t lds_, int t0, char* lds)
+{
+    typedef Prompt<TA, WR> P;
+    constexpr int NG = 32, SUMS = NG * P::BT * 4, TILES = P::BR / 16;
+    static_assert(SUMS + TILES * NG * 128 <= P::LDS, "32 groups fit the staging buffers");
+    const int lane = threadIdx.x & 63, h = lane >> 5, ml = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wt = wave / WR, wr = wave % WR;
+    const Rsrc gb = buffer_of(w.grid + (int64_t)rt0 * w.G * 16, 0x7FFFFFFFu);
+    const int rts = w.RT - 1 - rt0;
+    for (int g0 = 0; g0 < w.G; g0 += NG) {
+        __syncthreads();
+        // sums: 256 bytes (64 tokens) an instruction; grids: 1 KB, 8 groups of a
+        // row tile; groups beyond G repeat the last
+        for (int i = wave; i < NG * TA; i += 2 * WR)
+            load_lds4(buffer_of(sums + min(g0 + i / TA, w.G - 1) * lds_ + t0, 0x7FFFFFFFu), 4 * lane, 256 * (i % TA),
+                      lds + 256 * i);
+        for (int i = wave; i < TILES * NG / 8; i += 2 * WR) {
+            const int tile = i / (NG / 8), g = g0 + 8 * (i % (NG / 8)) + (lane >> 3);
+            load_lds16(gb, (uint32_t)(min(tile, rts) * w.G + min(g, w.G - 1)) * 128 + 16 * (lane & 7), 0,
+                       lds + SUMS + 1024 * i);
+        }
+        wait_direct_loads();
+        __syncthreads();
+        for (int j = 0; j < NG && g0 + j < w.G; j += 2) {
+            const int g = j + h;
+            const float in = g0 + g < w.G ? 1.f : 0.f;   // groups beyond G add nothing
+            bf16x8 zf[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const f32x2 sz = *reinterpret_cast<const f32x2*>(lds + SUMS + (4 * wr + 2 * b + (ml >> 4)) * NG * 128 +
+                                                                 128 * g + 8 * (ml & 15));
+                uint32_t z1, z2, z3;
+                split3(in * (-sz.x * (sz.y + kQ4Offset)), z1, z2, z3);
+                const u32x4 v = {z1 | (z2 << 16), z1 | (z3 << 16), z2 | (z1 << 16), 0u};
+                zf[b] = __builtin_bit_cast(bf16x8, v);
+            }
+#pragma unroll
+            for (int a = 0; a < TA; ++a) {
+                const float xs = *reinterpret_cast<const float*>(lds + 256 * TA * g + 4 * (32 * (wt * TA + a) + ml));
+                uint32_t x1, x2, x3;
+                split3(xs, x1, x2, x3);
+                const u32x4 v = {x1 | (x1 << 16), x2 | (x1 << 16), x2 | (x3 << 16), 0u};
+                const bf16x8 xf = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) acc[a][b] = Bf16::mfma32(xf, zf[b], acc[a][b]);
+            }
+        }
+    }
+}
+
+// OWN: the sums of x come from a product with ones.  blockIdx.y of gridDim.y
+// shares the columns; more than one of them writes float32 partial sums to
+// part[blockIdx.y][token][row] instead of y.
+template <class X, int TA, int WR, bool OWN>
 __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
-                                                        const float* __restrict__ sums, int64_t lds_,
-                                                        uint16_t* __restrict__ y, int64_t ldy, int nt, int nr)
+                                                           const float* __restrict__ sums, int64_t lds_,
+                                                           uint16_t* __restrict__ y, int64_t ldy, int nt, int nr,
+                                                           float* __restrict__ part)
 {
     typedef Prompt<TA, WR> P;
     typedef typename X::vec vec;
@@ -175,10 +254,13 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
     int bt, br;
     tile_of(nt, nr, bt, br);
     const int t0 = bt * P::BT, rt0 = br * (P::BR / 16);
-    PromptStage<TA, WR> stage(x, ldx, t0, T, w, rt0, lds);
-    stage.first();
+    const int kb0 = w.KB * blockIdx.y / gridDim.y, kb1 = w.KB * (blockIdx.y + 1) / gridDim.y;
+    PromptStage<TA, WR> stage(x, ldx, t0, T, w, rt0, kb0, kb1, lds);
+    stage.first(kb0);
 #pragma unroll
-    for (int c = 0; c < P::AHEAD; ++c) stage.chunk(c, c, ((c >> 1) + 1) % P::NW, c & 1);
+    for (int c = 0; c < P::AHEAD; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) stage.quarter(v, 2 * kb0 + c, c, ((c >> 1) + 1) % P::NW, c & 1);
 
     f32x16 acc[TA][2];
 #pragma unroll
@@ -187,10 +269,19 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+    f32x16 sx[OWN ? TA : 1];   // sums of x over the group so far, in every column of the tile
+    const vec ones = q4_ones<X>();
+    if (OWN) {
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sx[a][r] = 0.f;
+    }
 
     u32x4 codes[2][2];   // [row tile pair][unit h, h + 2]
-    float step[2] = {1.f, 1.f};
-    int left = 0;        // chunks left of the group whose steps the accumulators count in
+    f32x2 sz[2] = {f32x2{1.f, 0.f}, f32x2{1.f, 0.f}};   // of the group whose steps the accumulators count in
+    int left = 0;        // chunks left of that group
+    int start = 2 * kb0 % w.gb;
     int bx = 0, bw = 0;                                  // buffers of chunk c and block kb
     int px = P::AHEAD, pw = (P::AHEAD / 2 + 1) % P::NW;   // and of the ones staged beside them
     // the lane's parts of the LDS addresses
@@ -200,15 +291,12 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
         x_lane[v] = 128 * (32 * wt * TA + ml) + 16 * ((4 * (v >> 1) + 2 * h + (v & 1)) ^ ((ml >> 1) & 7));
     const uint32_t w_lane = P::CODES + 1024 * (4 * wr + (ml >> 4)) + 256 * h + 16 * (ml & 15);
     const uint32_t g_lane = P::GRID + 8 * (64 * wr + ml);
-    for (int kb = 0; kb < w.KB; ++kb) {
+    for (int kb = kb0; kb < kb1; ++kb) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int c = 2 * kb + half;
-            if (c < stage.nchunk) {
+            if (c < stage.chunks) {
                 tile_wait<(P::AHEAD - 1) * P::LOADS>();
-                stage.chunk(c + P::AHEAD, px, pw, (half + P::AHEAD) & 1);
-                px = px + 1 == P::NX ? 0 : px + 1;
-                if ((half + P::AHEAD) & 1) pw = pw + 1 == P::NW ? 0 : pw + 1;
                 if (half == 0) {
                     const char* s = lds + w_lane + bw * P::WBUF;
 #pragma unroll
@@ -216,20 +304,6 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
                             codes[b][u] = *reinterpret_cast<const u32x4*>(s + 2048 * b + 512 * u);
-                }
-                if (left-- == 0) {
-                    left = w.gb - 1;
-                    const char* s = lds + g_lane + bx * P::GBUF;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float s1 = *reinterpret_cast<const float*>(s + 256 * b);
-                        const float ratio = step[b] * __builtin_amdgcn_rcpf(s1);
-                        step[b] = s1;
-#pragma unroll
-                        for (int a = 0; a < TA; ++a)
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) acc[a][b][r] *= ratio;
-                    }
                 }
                 // fragments of x PRE steps before their products: an LDS read
                 // takes longer than a step of a small TA
@@ -240,6 +314,28 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
                 for (int v = 0; v < PRE; ++v)
 #pragma unroll
                     for (int a = 0; a < TA; ++a) xf[v][a] = *reinterpret_cast<const vec*>(s + x_lane[v] + 4096 * a);
+                if (left-- == 0) {
+                    left = w.gb - 1 - start;
+                    start = 0;
+                    const char* g = lds + g_lane + bx * P::GBUF;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const f32x2 s1 = *reinterpret_cast<const f32x2*>(g + 256 * b);
+                        const float ratio = sz[b].x * __builtin_amdgcn_rcpf(s1.x), off = -(sz[b].y + kQ4Offset);
+                        sz[b] = s1;
+#pragma unroll
+                        for (int a = 0; a < TA; ++a)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                acc[a][b][r] = (OWN ? fmaf(off, sx[a][r], acc[a][b][r]) : acc[a][b][r]) * ratio;
+                    }
+                    if (OWN) {
+#pragma unroll
+                        for (int a = 0; a < TA; ++a)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) sx[a][r] = 0.f;
+                    }
+                }
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     if (v + PRE < 4) {
@@ -251,11 +347,19 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
                     vec wf[2];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) wf[b] = X::codes(codes[b][v >> 1][2 * half + (v & 1)]);
+                    // a quarter of the next loads, and then the products as one
+                    // run: 4 % over all loads first and the compiler's order
+                    stage.quarter(v, c + P::AHEAD, px, pw, (half + P::AHEAD) & 1);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int a = 0; a < TA; ++a)
+                    for (int a = 0; a < TA; ++a) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b) acc[a][b] = X::mfma32(xf[v % (PRE + 1)][a], wf[b], acc[a][b]);
+                        if (OWN) sx[a] = X::mfma32(xf[v % (PRE + 1)][a], ones, sx[a]);
+                    }
                 }
+                px = px + 1 == P::NX ? 0 : px + 1;
+                if ((half + P::AHEAD) & 1) pw = pw + 1 == P::NW ? 0 : pw + 1;
                 bx = bx + 1 == P::NX ? 0 : bx + 1;
             }
         }
@@ -266,75 +370,86 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[a][b][r] *= step[b];
-    int64_t grid[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-        grid[b] = (int64_t)min(rt0 + wr * 4 + 2 * b + (ml >> 4), w.RT - 1) * w.G * 16 + (ml & 15);
-
-    // minus s (16 + z) X: lane half h takes group g0 + 2 j + h, slots
-    // X1 Z1, X1 Z2, X2 Z1, X1 Z3, X2 Z2, X3 Z1; four pairs of groups at a time
-    // so that their loads are in flight together
-    constexpr int GP = 4;
-    for (int g0 = 0; g0 < w.G; g0 += 2 * GP) {
-        f32x2 sz[GP][2];
-        float xs[GP][TA];
-#pragma unroll
-        for (int j = 0; j < GP; ++j) {
-            const int g = min(g0 + 2 * j + h, w.G - 1);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) sz[j][b] = w.grid[grid[b] + (int64_t)g * 16];
-#pragma unroll
-            for (int a = 0; a < TA; ++a)
-                xs[j][a] = sums[(int64_t)g * lds_ + min(t0 + 32 * (wt * TA + a) + ml, T - 1)];
-        }
-#pragma unroll
-        for (int j = 0; j < GP; ++j) {
-            const float in = g0 + 2 * j + h < w.G ? 1.f : 0.f;   // groups beyond G add nothing
-            bf16x8 zf[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t z1, z2, z3;
-                split3(in * (-sz[j][b].x * (sz[j][b].y + kQ4Offset)), z1, z2, z3);
-                const u32x4 v = {z1 | (z2 << 16), z1 | (z3 << 16), z2 | (z1 << 16), 0u};
-                zf[b] = __builtin_bit_cast(bf16x8, v);
-            }
-#pragma unroll
-            for (int a = 0; a < TA; ++a) {
-                uint32_t x1, x2, x3;
-                split3(xs[j][a], x1, x2, x3);
-                const u32x4 v = {x1 | (x1 << 16), x2 | (x1 << 16), x2 | (x3 << 16), 0u};
-                const bf16x8 xf = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) acc[a][b] = Bf16::mfma32(xf, zf[b], acc[a][b]);
-            }
-        }
-    }
-
+            for (int r = 0; r < 16; ++r)
+                acc[a][b][r] = (OWN ? fmaf(-(sz[b].y + kQ4Offset), sx[a][r], acc[a][b][r]) : acc[a][b][r]) * sz[b].x;
     wait_direct_loads();
+    if (!OWN) zero_points<X, TA, WR>(acc, w, rt0, sums, lds_, t0, lds);
+    const int tw = t0 + 32 * wt * TA, rw = br * P::BR + wr * 64;
+    if (gridDim.y > 1) {
+        float* p = part + (int64_t)blockIdx.y * T * w.m;
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int t = tw + 32 * a + 8 * (r >> 2) + 4 * h + (r & 3), row = rw + 32 * b + ml;
+                    if (t < T && row < w.m) p[(int64_t)t * w.m + row] = acc[a][b][r];
+                }
+        return;
+    }
     __syncthreads();
-    tile_store<X, TA>(acc, 1.f, lds, t0 + 32 * wt * TA, T, br * P::BR + wr * 64, w.m, y, ldy);
+    tile_store<X, TA>(acc, 1.f, lds + wave * kStoreBytes, tw, T, rw, w.m, y, ldy);
 }
+
+// y = f times the sum of `splits` partial results, in order.
+template <class X>
+__global__ __launch_bounds__(256) void k_q4_join(const float* __restrict__ part, int splits, int T, int m,
+                                                 const float* __restrict__ f, uint16_t* __restrict__ y, int64_t ldy)
+{
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)T * m;
+    if (e >= all) return;
+    float v = 0.f;
+    for (int u = 0; u < splits; ++u) v += part[u * all + e];
+    y[e / m * ldy + e % m] = X::down(v * (f && *f > 0.f ? *f : 1.f));
+}
+
+template <class X>
+void join_enqueue(const float* part, int splits, int64_t T, int m, const float* f, uint16_t* y, int64_t ldy, hipStream_t s)
+{
+    launch(nullptr, KK_Q4_JOIN, 0.0, 4.0 * splits * T * m, k_q4_join<X>, dim3((unsigned)ceil_div(T * m, 256)), dim3(256), s,
+           part, splits, (int)T, m, f, y, ldy);
+}
+template void join_enqueue<Bf16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
+template void join_enqueue<Fp16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
 
 // --------------------------------------------------------------------- host
 
-struct PromptWork {
+// How a problem is cut: TA, WR and the workgroups that share a tile's columns.
+struct PromptPlan {
+    int TA, WR, splits;
     int64_t lds_, ldc;
-    size_t sums, copy, bytes;
+    size_t sums, copy, part, bytes;
 };
 
-static PromptWork prompt_work(int64_t T, int64_t n, int64_t G)
+static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
 {
-    PromptWork p;
-    p.lds_ = ceil_div(T, 64) * 64;
+    PromptPlan p;
+    // The largest tiles that still give every CU about one: a large tile
+    // expands a code for more tokens (2048 tokens x 4096 x 4096: 76 us with TA =
+    // 2, 95 with 1), a missing workgroup costs in proportion (1024 tokens, 128
+    // tiles of TA = 2: 68 us, 512 of TA = 1: 54).
+    p.WR = 4;
+    if (ceil_div(T, 256) * ceil_div(m, 256) >= 224) p.TA = 4;
+    else if (ceil_div(T, 128) * ceil_div(m, 256) >= 192) p.TA = 2;
+    else p.TA = 1, p.WR = 2;
+    // Small problems: a workgroup per CU, down to four column blocks each (65
+    // tokens x 4096 x 4096: 16 us with 4 splits, 33 without).
+    p.splits = 1;
+    if (p.TA == 1) {
+        const int64_t tiles = ceil_div(T, 64) * ceil_div(m, 128);
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, 256 / tiles, ceil_div(n, kQ4Cols) / 4}));
+    }
+    p.lds_ = ceil_div(T, 256) * 256;
     p.ldc = ceil_div(n, 64) * 64;
     p.sums = 0;
-    p.copy = align_up((size_t)p.lds_ * G * 4);
-    p.bytes = p.copy + align_up((size_t)T * p.ldc * 2);
+    p.copy = p.TA == 1 ? 0 : align_up((size_t)p.lds_ * G * 4);
+    p.part = p.copy + align_up((size_t)T * p.ldc * 2);
+    p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * T * m * 4) : 0);
     return p;
 }
 
-size_t q4_prompt_workspace_bytes(int64_t T, int64_t n, int64_t G) { return prompt_work(T, n, G).bytes; }
+size_t q4_prompt_workspace_bytes(int64_t T, int64_t m, int64_t n, int64_t G) { return prompt_plan(T, m, n, G).bytes; }
 
 template <class X>
 void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* copy, int64_t ldc, hipStream_t s)
@@ -345,34 +460,37 @@ void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* co
 template void copy_enqueue<Bf16>(const uint16_t*, int64_t, int64_t, int, uint16_t*, int64_t, hipStream_t);
 template void copy_enqueue<Fp16>(const uint16_t*, int64_t, int64_t, int, uint16_t*, int64_t, hipStream_t);
 
-template <class X, int TA, int WR>
+template <class X, int TA, int WR, bool OWN>
 static void prompt_launch(const uint16_t* x, int64_t ldx, int64_t T, const Q4Layer& w, const float* sums, int64_t lds_,
-                          uint16_t* y, int64_t ldy, hipStream_t s)
+                          uint16_t* y, int64_t ldy, int splits, float* part, hipStream_t s)
 {
     typedef Prompt<TA, WR> P;
     const int nt = (int)ceil_div(T, P::BT), nr = (int)ceil_div(w.m, P::BR);
-    launch(nullptr, KK_Q4_PROMPT, 2.0 * T * w.m * w.n, 0.0, k_q4_prompt<X, TA, WR>, dim3((unsigned)(nt * nr)),
-           dim3(128 * WR), s, x, ldx, (int)T, w, sums, lds_, y, ldy, nt, nr);
+    launch(nullptr, KK_Q4_PROMPT, 2.0 * T * w.m * w.n, 0.0, k_q4_prompt<X, TA, WR, OWN>,
+           dim3((unsigned)(nt * nr), (unsigned)splits), dim3(128 * WR), s, x, ldx, (int)T, w, sums, lds_, y, ldy, nt, nr, part);
 }
 
 template <class X>
 static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, void* y, int64_t ldy, void* ws,
                       hipStream_t s)
 {
-    const PromptWork p = prompt_work(T, w.n, w.G);
+    const PromptPlan p = prompt_plan(T, w.m, w.n, w.G);
     const uint16_t* xp = static_cast<const uint16_t*>(x);
     uint16_t* yp = static_cast<uint16_t*>(y);
     float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + p.sums);
     uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + p.copy);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
     // (the staging offsets of a token block are 31 bits)
     const bool direct = w.n % 64 == 0 && ldx % 8 == 0 && ldx <= (1 << 21) && aligned16(x);
-    launch(nullptr, KK_Q4_SUMS, 0.0, 2.0 * T * w.n, direct ? k_q4_sums<X, false> : k_q4_sums<X, true>,
-           dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, w.G, sums, p.lds_, copy, p.ldc);
+    if (p.TA > 1)
+        launch(nullptr, KK_Q4_SUMS, 0.0, 2.0 * T * w.n, direct ? k_q4_sums<X, false> : k_q4_sums<X, true>,
+               dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, w.G, sums, p.lds_, copy, p.ldc);
+    else if (!direct) copy_enqueue<X>(xp, ldx, T, w.n, copy, p.ldc, s);
     if (!direct) xp = copy, ldx = p.ldc;
-    const int64_t big = ceil_div(T, 256) * ceil_div(w.m, 256), mid = ceil_div(T, 128) * ceil_div(w.m, 256);
-    if (big >= 256) prompt_launch<X, 4, 4>(xp, ldx, T, w, sums, p.lds_, yp, ldy, s);
-    else if (mid >= 128) prompt_launch<X, 2, 4>(xp, ldx, T, w, sums, p.lds_, yp, ldy, s);
-    else prompt_launch<X, 1, 2>(xp, ldx, T, w, sums, p.lds_, yp, ldy, s);
+    if (p.TA == 4) prompt_launch<X, 4, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
+    else if (p.TA == 2) prompt_launch<X, 2, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
+    else prompt_launch<X, 1, 2, true>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
+    if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.m, nullptr, yp, ldy, s);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

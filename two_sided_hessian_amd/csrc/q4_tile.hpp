@@ -7,6 +7,8 @@
 
 namespace bk {
 
+constexpr int kStoreBytes = 32 * 72 * 2;   // LDS of a wave in tile_store
+
 // Waits until at most `left` loads of this wave are in flight (they complete
 // in order), then for the other waves.
 template <int LEFT>
@@ -30,16 +32,15 @@ __device__ __forceinline__ void tile_of(int nt, int nr, int& bt, int& br)
 }
 
 // Results through LDS, 32 tokens x 64 columns of a wave at a time, so that
-// they leave as 16-byte stores; unaligned or cut rows leave one by one.  acc:
-// 32-token x 32-column MFMA tiles, times f.  Each wave uses its own 4608 bytes
-// of `lds`, which no one else may touch any more.
+// they leave as 16-byte stores (to any address); cut rows leave one by one.  acc:
+// 32-token x 32-column MFMA tiles, times f.  `lds`: 4608 bytes of the wave's
+// own, which no one else may touch any more.
 template <class X, int TA>
 __device__ __forceinline__ void tile_store(const f32x16 (&acc)[TA][2], float f, char* lds, int t0, int T, int col0,
                                            int cols, uint16_t* __restrict__ y, int64_t ldy)
 {
     const int lane = threadIdx.x & 63, h = lane >> 5, ml = lane & 31;
-    const bool whole = ((reinterpret_cast<uintptr_t>(y) & 15) | (ldy & 7)) == 0;
-    uint16_t* out = reinterpret_cast<uint16_t*>(lds) + (threadIdx.x >> 6) * 32 * 72;   // pitch 72: spread banks
+    uint16_t* out = reinterpret_cast<uint16_t*>(lds);   // pitch 72: spread banks
 #pragma unroll
     for (int a = 0; a < TA; ++a) {
 #pragma unroll
@@ -55,8 +56,8 @@ __device__ __forceinline__ void tile_store(const f32x16 (&acc)[TA][2], float f, 
             const int t = t0 + 32 * a + tl, col = col0 + c;
             if (t >= T) continue;
             uint16_t* dst = y + (int64_t)t * ldy + col;
-            if (whole && col + 8 <= cols) {
-                *reinterpret_cast<u32x4*>(dst) = v;
+            if (col + 8 <= cols) {
+                *reinterpret_cast<u32x4_any*>(dst) = v;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -70,5 +71,10 @@ __device__ __forceinline__ void tile_store(const f32x16 (&acc)[TA][2], float f, 
 // A padded copy of x (T x n, n rounded up to 64 columns, zeros beyond n).
 template <class X>
 void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* copy, int64_t ldc, hipStream_t s);
+
+// y (T x m) = f times the sum of `splits` float32 results part[split][t][m], in
+// order; f: a device scalar, or null for 1.
+template <class X>
+void join_enqueue(const float* part, int splits, int64_t T, int m, const float* f, uint16_t* y, int64_t ldy, hipStream_t s);
 
 }  // namespace bk
