@@ -8,65 +8,89 @@ namespace bk {
 
 // ------------------------------------------------------------------ packing
 //
-// One thread per 16-byte unit (32 codes of one row).  Reads half of what it
-// writes twice over; bound by HBM, run once per layer.
+// One thread per 16-byte unit: 32 codes of one row, read as two runs of 16
+// (four lanes a row's 64 bytes; a wave writes one block of 1 KB).  HBM bounds
+// it: 1.5 bytes a code.
+
+// a dword of codes from eight codes, four to a dword
+__device__ __forceinline__ uint32_t pack8(uint32_t lo, uint32_t hi)
+{
+    // even codes to the low half, odd ones to the high half, 4 bits each
+    const uint32_t e0 = lo & 0x000F000Fu, o0 = lo >> 8 & 0x000F000Fu, e1 = hi & 0x000F000Fu, o1 = hi >> 8 & 0x000F000Fu;
+    const uint32_t e = ((e0 | e0 >> 12) & 0xFFu) | ((e1 | e1 >> 12) & 0xFFu) << 8;
+    const uint32_t o = ((o0 | o0 >> 12) & 0xFFu) | ((o1 | o1 >> 12) & 0xFFu) << 8;
+    return __builtin_rotateleft32(e | o << 16, 3);
+}
+
 __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ codes, const float* __restrict__ scale,
                                                  int64_t m, int64_t n, int RT, int KB, int G, int gb,
                                                  int64_t layer_bytes, int64_t unit_at, char* __restrict__ packed)
 {
     if (blockIdx.x == 0 && threadIdx.x == 0)   // k_q4_pack_grid raises it
         *reinterpret_cast<float*>(packed + blockIdx.y * layer_bytes + unit_at) = 0.f;
-    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (unit >= (int64_t)RT * KB * 64) return;
+    const int64_t block = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (block >= (int64_t)RT * KB) return;
     const int64_t layer = blockIdx.y;
-    const int r = (int)(unit & 15), q = (int)(unit >> 4) & 3;
-    const int64_t block = unit >> 6;
+    const int q = threadIdx.x & 3, r = threadIdx.x >> 2 & 15;
     const int64_t row = block / KB * kQ4Rows + r;
     const int64_t col0 = block % KB * kQ4Cols + 16 * q;
     u32x4 out = {0u, 0u, 0u, 0u};
     if (row < m) {
         const uint8_t* src = codes + (layer * m + row) * n;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int64_t c0 = col0 + 64 * (d >> 1) + 8 * (d & 1);
-            uint32_t v = 0;
+        for (int h = 0; h < 2; ++h) {
+            const int64_t c0 = col0 + 64 * h;
+            if (c0 >= n) continue;
             const int64_t g = min((int)(c0 >> 6) / gb, G - 1);
             if (scale[(layer * m + row) * G + g] == 0.f) continue;   // weights of 0: see k_q4_pack_grid
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (c0 + 16 <= n) {
+                v = *reinterpret_cast<const u32x4_any*>(src + c0);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c0 + e < n) v |= (uint32_t)(src[c0 + e] & 15u) << (4 * (e >> 1) + 16 * (e & 1));
-            out[d] = __builtin_rotateleft32(v, 3);
+                for (int e = 0; e < 16; ++e)
+                    if (c0 + e < n) v[e >> 2] |= (uint32_t)src[c0 + e] << (8 * (e & 3));
+            }
+            out[2 * h] = pack8(v[0], v[1]);
+            out[2 * h + 1] = pack8(v[2], v[3]);
         }
     }
-    reinterpret_cast<u32x4*>(packed + layer * layer_bytes)[unit] = out;
+    reinterpret_cast<u32x4*>(packed + layer * layer_bytes)[block * 64 + 16 * q + r] = out;
 }
+
+// Grids, and the unit: the exponent, rounded up, of the largest weight (a
+// maximum of integers, which does not depend on the order it is taken in).  A
+// few workgroups per layer, so that few atomics meet at the one place.
+constexpr int kPackGridBlocks = 128;
 
 __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ scale, const float* __restrict__ zero,
                                                       int64_t m, int RT, int G, int64_t layer_bytes, int64_t grid_at,
                                                       int64_t unit_at, char* __restrict__ packed)
 {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t layer = blockIdx.y;
-    const int r = (int)(e & 15);
-    const int64_t row = (e >> 4) / G * kQ4Rows + r, g = (e >> 4) % G;
-    f32x2 v = {0.f, 0.f};
-    if (e < (int64_t)RT * G * kQ4Rows) {
+    __shared__ float tops[4];
+    const int64_t layer = blockIdx.y, all = (int64_t)RT * G * kQ4Rows;
+    float top = 0.f;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < all; e += 256 * gridDim.x) {
+        const int64_t row = (e >> 4) / G * kQ4Rows + (e & 15), g = (e >> 4) % G;
+        f32x2 v = {0.f, 0.f};
         if (row < m) {
             v.x = scale[(layer * m + row) * G + g];
             v.y = zero[(layer * m + row) * G + g];
             // a step of 0 (every weight 0, whatever the codes) becomes step 1,
             // zero point 0 on codes of 0: kernels divide by steps
             if (v.x == 0.f) v = f32x2{1.f, 0.f};
+            else top = fmaxf(top, fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y)));
         }
         reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at)[e] = v;
     }
-    // the unit: its largest weight's exponent, rounded up (the maximum of
-    // integers does not depend on the order it is taken in)
-    float top = fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y));
     for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    if ((threadIdx.x & 63) == 0 && top > 0.f && top < INFINITY) {
-        const uint32_t exponent = min((__float_as_uint(top) >> 23) + 1u, 254u);
-        atomicMax(reinterpret_cast<unsigned*>(packed + layer * layer_bytes + unit_at), max(exponent, 1u) << 23);
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        if (top > 0.f && top < INFINITY)
+            atomicMax(reinterpret_cast<unsigned*>(packed + layer * layer_bytes + unit_at),
+                      max(min((__float_as_uint(top) >> 23) + 1u, 254u), 1u) << 23);
     }
 }
 
@@ -196,11 +220,12 @@ int bakron_q4_pack(const uint8_t* codes, const float* scale, const float* zero, 
     char* out = static_cast<char*>(packed);
     const double mn = (double)count * m * n;
     bk::launch(nullptr, bk::KK_Q4_PACK, 0.0, 1.5 * mn, bk::k_q4_pack,
-               dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.KB * 64, 256), (unsigned)count), dim3(256), stream, codes,
-               scale, m, n, d.RT, d.KB, d.G, d.gb, (int64_t)d.bytes, (int64_t)d.unit_at, out);
+               dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.KB, 4), (unsigned)count), dim3(256), stream, codes, scale,
+               m, n, d.RT, d.KB, d.G, d.gb, (int64_t)d.bytes, (int64_t)d.unit_at, out);
     bk::launch(nullptr, bk::KK_Q4_PACK_GRID, 0.0, 16.0 * count * m * d.G, bk::k_q4_pack_grid,
-               dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.G * 16, 256), (unsigned)count), dim3(256), stream, scale,
-               zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
+               dim3((unsigned)std::min<int64_t>(bk::kPackGridBlocks, bk::ceil_div((int64_t)d.RT * d.G * 16, 256)),
+                    (unsigned)count),
+               dim3(256), stream, scale, zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
     return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
 }
 

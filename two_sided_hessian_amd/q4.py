@@ -43,12 +43,12 @@ class Q4Weight:
     packed layout, with group_size columns per grid (None: one grid per row).
     ``data`` is the device buffer (uint8) that holds it."""
 
-    __slots__ = ("data", "count", "m", "n", "group_size", "device", "_ptr", "_group")
+    __slots__ = ("data", "count", "m", "n", "group_size", "device", "_ptr", "_group", "_index")
 
     def __init__(self, data, count, m, n, group_size):
         self.data, self.count, self.m, self.n, self.group_size = data, count, m, n, group_size
         self.device = data.device
-        self._ptr, self._group = data.data_ptr(), group_size or 0
+        self._ptr, self._group, self._index = data.data_ptr(), group_size or 0, data.get_device()
 
     def __repr__(self):
         return f"Q4Weight(count={self.count}, m={self.m}, n={self.n}, group_size={self.group_size})"
@@ -81,9 +81,10 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
     _b._check_dev("scale", scale, torch.float32, gshape)
     _b._check_dev("zero", zero, torch.float32, gshape)
     if check and codes.numel():
-        if int(codes.max()) > 15:
+        high, finite = torch.stack((codes.max() > 15, torch.isfinite(scale).all() & torch.isfinite(zero).all())).tolist()
+        if high:
             raise _b.GridError("codes must lie in [0, 15]")
-        if not bool(torch.isfinite(scale).all()) or not bool(torch.isfinite(zero).all()):
+        if not finite:
             raise _b.GridError("scale and zero must be finite")
     L = _b.lib()
     data = _b.workspace(L.bakron_q4_packed_bytes(count, m, n, g), codes.device)
@@ -114,37 +115,43 @@ def _rows(name, t, cols, like=None):
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in _TYPES or (like is not None and t.dtype != like):
         raise TypeError(f"{name} must be {like or 'torch.bfloat16 or torch.float16'}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError(f"{name} must have shape (tokens, {cols}), got {tuple(t.shape)}")
-    rows, ld = t.shape[0], t.stride(0)
-    if cols > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{name} must have shape (tokens, {cols}), got {tuple(shape)}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows <= 1 or cols == 0:
+    if shape[0] <= 1 or cols == 0:
         return cols
     if ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
     return ld
 
 
-def _one(name, w, device, count=1):
+def _one(name, w, index, count=1):
     if not isinstance(w, Q4Weight):
         raise TypeError(f"{name} must be a Q4Weight (q4_pack)")
     if w.count != count:
         raise ValueError(f"{name} must hold {count} layer(s), got {w.count}")
-    if w.device != device:
-        raise ValueError(f"{name} is on {w.device}, not on {device}")
+    if w._index != index:
+        raise ValueError(f"{name} is on {w.device}, not on cuda:{index}")
 
 
-def _ws(ws, need, device):
-    """The workspace as (tensor, pointer, bytes)."""
+def _ws(ws, size, device, index):
+    """The workspace as (tensor, pointer, bytes); size() bytes if none is given."""
     if ws is None:
-        size = need()
-        if not size:
+        need = size()
+        if not need:
             return None, None, 0
-        ws = _b.workspace(size, device)
-    elif ws.device != device:
+        ws = _b.workspace(need, device)
+    elif ws.get_device() != index:
         raise ValueError(f"ws is on {ws.device}, not on {device}")
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.nbytes
+
+
+# The current stream's handle without a Stream object around it (a call of
+# one token's layer takes less time than making that).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _keep(stream, *tensors):
@@ -156,29 +163,38 @@ def _keep(stream, *tensors):
             t.record_stream(stream)
 
 
+_calls = {}
+
+
+def _call(name):
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = getattr(_b.lib(), name)
+    return f
+
+
 def _linear(call, size, name, x, w, out, ws, stream):
     if not isinstance(w, Q4Weight):
         raise TypeError("w must be a Q4Weight (q4_pack)")
     in_cols, out_cols = (w.n, w.m) if name == "x" else (w.m, w.n)
     ldx = _rows(name, x, in_cols)
-    device, T = x.device, x.shape[0]
-    _one("w", w, device)
+    index, T = x.get_device(), x.shape[0]
+    _one("w", w, index)
+    given = ws
     if out is None:
-        out = torch.empty((T, out_cols), dtype=x.dtype, device=device)
+        out = x.new_empty((T, out_cols))
         ldo = out_cols
     else:
         ldo = _rows("out", out, out_cols, x.dtype)
-        if out.shape[0] != T or out.device != device:
-            raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {device}")
-    L = _b.lib()
-    given, (ws, wp, wn) = ws, _ws(ws, lambda: size(T, w), device)
+        if out.shape[0] != T or out.get_device() != index:
+            raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {x.device}")
+    ws, wp, wn = _ws(ws, lambda: size(T, w), w.device, index)
     if stream is None:
-        s = torch.cuda.current_stream(device)
+        s = _raw_stream(index)
     else:
-        s = stream
-        _keep(s, out, None if given is not None else ws)
-    rc = getattr(L, call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w._ptr, w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn,
-                          s.cuda_stream)
+        s = stream.cuda_stream
+        _keep(stream, out, None if given is not None else ws)
+    rc = _call(call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w._ptr, w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn, s)
     if rc != _b.BAKRON_SUCCESS:
         raise _b.BakronError(rc, call)
     return out
@@ -209,34 +225,35 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
         raise TypeError("w_gate must be a Q4Weight (q4_pack)")
     f, h, E = w_gate.m, w_gate.n, w_gate.count
     ldx = _rows("x", x, h)
-    device, T = x.device, x.shape[0]
-    for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
-        _one(name, w, device, E)
-        if (w.m, w.n) != ((h, f) if name == "w_down" else (f, h)):
-            raise ValueError(f"{name} must be {(h, f) if name == 'w_down' else (f, h)}, got {(w.m, w.n)}")
+    index, T, dtype = x.get_device(), x.shape[0], x.dtype
+    _one("w_gate", w_gate, index, E)
+    for name, w, shape in (("w_up", w_up, (f, h)), ("w_down", w_down, (h, f))):
+        _one(name, w, index, E)
+        if (w.m, w.n) != shape:
+            raise ValueError(f"{name} must be {shape}, got {(w.m, w.n)}")
         if w._group != w_gate._group:
             raise ValueError("the three stacks must have one group_size")
-    _b._check_dev("router", router, x.dtype, (E, h))
+    _b._check_dev("router", router, dtype, (E, h))
+    given = ws
     if out is None:
-        out = {"y": torch.empty((T, h), dtype=x.dtype, device=device),
-               "ids": torch.empty((T, top_k), dtype=torch.int32, device=device),
-               "weights": torch.empty((T, top_k), dtype=torch.float32, device=device)}
+        out = {"y": x.new_empty((T, h)), "ids": x.new_empty((T, top_k), dtype=torch.int32),
+               "weights": x.new_empty((T, top_k), dtype=torch.float32)}
         ldy = h
     else:
-        ldy = _rows("out['y']", out["y"], h, x.dtype)
+        ldy = _rows("out['y']", out["y"], h, dtype)
         if out["y"].shape[0] != T:
             raise ValueError(f"out['y'] must have shape ({T}, {h}), got {tuple(out['y'].shape)}")
         _b._check_dev("out['ids']", out["ids"], torch.int32, (T, top_k))
         _b._check_dev("out['weights']", out["weights"], torch.float32, (T, top_k))
-    given, (ws, wp, wn) = ws, _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), device)
+    ws, wp, wn = _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), w_gate.device, index)
     if stream is None:
-        s = torch.cuda.current_stream(device)
+        s = _raw_stream(index)
     else:
-        s = stream
-        _keep(s, *out.values(), None if given is not None else ws)
-    rc = _b.lib().bakron_q4_moe(x.data_ptr(), ldx, T, _TYPES[x.dtype], router.data_ptr(), w_gate._ptr, w_up._ptr,
-                                w_down._ptr, h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy,
-                                out["ids"].data_ptr(), out["weights"].data_ptr(), wp, wn, s.cuda_stream)
+        s = stream.cuda_stream
+        _keep(stream, *out.values(), None if given is not None else ws)
+    rc = _call("bakron_q4_moe")(x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate._ptr, w_up._ptr, w_down._ptr,
+                                h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy, out["ids"].data_ptr(),
+                                out["weights"].data_ptr(), wp, wn, s)
     if rc != _b.BAKRON_SUCCESS:
         raise _b.BakronError(rc, "bakron_q4_moe")
     return out
