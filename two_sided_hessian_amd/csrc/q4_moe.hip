@@ -6,7 +6,10 @@
 //   y_t = sum_e p_te down_e ( silu(gate_e x_t) * (up_e x_t) ).
 //
 // Three launches, since every expert's inner activations have to be complete
-// before the down products and the logits before the choice:
+// before the down products and the logits before the choice (logits made by
+// every workgroup for itself, in two launches, were slower: 61 us against 55
+// for one token and 8 experts of 4096 x 14336, 44 against 36 for 16 tokens
+// and 16 experts of 2048 x 1024):
 //   k_q4_router: the logits.
 //   k_q4_moe_up: one workgroup per (row tiles of ffn, expert).  It ranks its
 //     own expert among each token's logits (a token chooses it if fewer than
@@ -467,7 +470,11 @@ static int moe_enqueue(const void* x, int64_t ldx, int64_t T, const void* router
            dim3((unsigned)(ceil_div(du.RT, 8 / per) + 1), (unsigned)slots), dim3(512), s, xp, ldx, (int)T,
            q4_layer(gate, du), q4_layer(up, du), (int64_t)du.bytes, logits, (int)E, k, hi, lo, w.lda, ids, weights, plan);
     if (f == 0) return q4_zero_enqueue(y, ldy, T, h, s);
-    const int splits = (int)std::min<int64_t>(kMoeSplits, ceil_div(256, dd.RT));
+    // Splits of the down products: a workgroup per CU where there are fewer row
+    // tiles, but two column blocks at least for every wave (3 tokens, 5 experts
+    // of 1003 x 1501: 17.4 us with one split, 18.7 with four).
+    const int64_t blocks = slots * dd.KB / (2 * kDownWaves);
+    const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMoeSplits, ceil_div(256, dd.RT), blocks}));
     launch(nullptr, KK_Q4_MOE_DOWN, 2.0 * T * k * h * f, 0.0,
            T <= 16 ? k_q4_moe_down<X, 16, HALF> : k_q4_moe_down<X, 64, HALF>,
            dim3((unsigned)dd.RT, (unsigned)splits), dim3(64 * kDownWaves), s, hi, lo, w.lda, q4_layer(down, dd),
