@@ -108,6 +108,54 @@ def test_prompt_sizes(T, m, n, group):
         close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
 
 
+@pytest.mark.parametrize("T,wide,narrow", [(1040, 6200, 200), (2060, 7200, 136)])
+@pytest.mark.parametrize("group", [0, 64, 128])
+def test_large_tiles(T, wide, narrow, group):
+    """Enough tokens and columns of results for tiles of 128 and 256 tokens."""
+    dtype = torch.float16 if group == 128 else torch.bfloat16
+    layer = make_layer(wide, narrow, group, T)
+    w, ref = pack(*layer, group), weights64(*layer, group)
+    x = tokens(T, narrow, dtype, 1)
+    close(B.q4_linear(x, w), x.double().cpu().numpy() @ ref.T, dtype, LINEAR)
+    layer = make_layer(narrow, wide, group, T + 1)
+    w, ref = pack(*layer, group), weights64(*layer, group)
+    dy = tokens(T, narrow, dtype, 2)
+    close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_offsets_beyond_32_bits(T):
+    # rows 80 MB (2 GB at three tokens) apart, of inputs and of results
+    m, n, group = 40, 192, 64
+    layer = make_layer(m, n, group, 71)
+    w, ref = pack(*layer, group), weights64(*layer, group)
+    ld = 40_000_004 if T > 3 else 1_000_000_004
+    dtype = torch.bfloat16
+    far_in = torch.empty((T, ld), dtype=dtype, device=DEV)
+    far_out = torch.empty((T, ld), dtype=dtype, device=DEV)
+    x, dy = tokens(T, n, dtype, 1), tokens(T, m, dtype, 2)
+    far_in[:, :n] = x
+    out = B.q4_linear(far_in[:, :n], w, out=far_out[:, :m])
+    close(out, x.double().cpu().numpy() @ ref.T, dtype, LINEAR)
+    far_in[:, :m] = dy
+    out = B.q4_linear_grad(far_in[:, :m], w, out=far_out[:, :n])
+    close(out, dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
+
+
+@pytest.mark.parametrize("T", [2, 100, 300])
+def test_groups_of_step_zero(T):
+    # a step of 0 makes every weight of the group 0, whatever its codes
+    m, n, group = 70, 320, 64
+    layer = make_layer(m, n, group, 81)
+    layer[1][::3, 1] = 0.0
+    layer[1][5] = 0.0
+    w, ref = pack(*layer, group), weights64(*layer, group)
+    for dtype in (torch.bfloat16, torch.float16):
+        x, dy = tokens(T, n, dtype, 1), tokens(T, m, dtype, 2)
+        close(B.q4_linear(x, w), x.double().cpu().numpy() @ ref.T, dtype, LINEAR)
+        close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
+
+
 @pytest.mark.parametrize("T", [3, 150])
 @pytest.mark.parametrize("pad,shift", [(1, 0), (8, 0), (8, 8), (7, 3), (64, 1)])
 def test_rows_of_a_wider_buffer(T, pad, shift):

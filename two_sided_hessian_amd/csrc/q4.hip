@@ -139,14 +139,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_few(const uint16_t* __restric
 // rows x cols zeros of a 2-byte type
 __global__ __launch_bounds__(256) void k_q4_zero(uint16_t* __restrict__ y, int64_t ld, int64_t rows, int64_t cols)
 {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e < rows * cols) y[e / cols * ld + e % cols] = 0;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < rows * cols; e += (int64_t)gridDim.x * 256)
+        y[e / cols * ld + e % cols] = 0;
 }
 
 int q4_zero_enqueue(void* y, int64_t ld, int64_t rows, int64_t cols, hipStream_t s)
 {
-    launch(nullptr, KK_Q4_ZERO, 0.0, 2.0 * rows * cols, k_q4_zero, dim3((unsigned)ceil_div(rows * cols, 256)), dim3(256),
-           s, static_cast<uint16_t*>(y), ld, rows, cols);
+    launch(nullptr, KK_Q4_ZERO, 0.0, 2.0 * rows * cols, k_q4_zero,
+           dim3((unsigned)std::min<int64_t>(65536, ceil_div(rows * cols, 256))), dim3(256), s, static_cast<uint16_t*>(y), ld, rows, cols);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
