@@ -14,8 +14,8 @@
 //     over x of its own.
 //   * small tiles, which do not fill the matrix cores: X comes from a product
 //     with ones beside the others, and is taken off when its group ends.
-// Where x's rows are not 16-byte aligned or n is not a multiple of 64, that
-// pass also makes a padded copy that the product can stage directly.
+// Where x's rows are not 16-byte aligned or n is not a multiple of 64, the pass
+// over x also makes a padded copy that the product can stage directly.
 //
 // k_q4_prompt: a workgroup of 2 x WR waves computes 64 TA tokens x 64 WR rows
 // of W; a wave owns 32 TA tokens x 64 rows as TA x 2 MFMA tiles of 32 x 32
@@ -209,7 +209,10 @@ __device__ __forceinline__ void zero_points(f32x16 (&acc)[TA][2], const Q4Layer&
         }
         wait_direct_loads();
         __syncthreads();
-        for (int j = 0; j < NG && g0 + j < w.G; j += 2) {
+#pragma unroll 1
+        for (int j0 = 0; j0 < NG && g0 + j0 < w.G; j0 += 8)
+#pragma unroll
+        for (int j = j0; j < j0 + 8; j += 2) {   // (unrolled: four pairs' reads in flight)
             const int g = j + h;
             const float in = g0 + g < w.G ? 1.f : 0.f;   // groups beyond G add nothing
             bf16x8 zf[2];
@@ -373,7 +376,7 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
             for (int r = 0; r < 16; ++r)
                 acc[a][b][r] = (OWN ? fmaf(-(sz[b].y + kQ4Offset), sx[a][r], acc[a][b][r]) : acc[a][b][r]) * sz[b].x;
     wait_direct_loads();
-    if (!OWN) zero_points<X, TA, WR>(acc, w, rt0, sums, lds_, t0, lds);
+    if (!OWN && blockIdx.y == 0) zero_points<X, TA, WR>(acc, w, rt0, sums, lds_, t0, lds);
     const int tw = t0 + 32 * wt * TA, rw = br * P::BR + wr * 64;
     if (gridDim.y > 1) {
         float* p = part + (int64_t)blockIdx.y * T * w.m;
@@ -443,7 +446,7 @@ static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
     p.lds_ = ceil_div(T, 256) * 256;
     p.ldc = ceil_div(n, 64) * 64;
     p.sums = 0;
-    p.copy = p.TA == 1 ? 0 : align_up((size_t)p.lds_ * G * 4);
+    p.copy = align_up((size_t)p.lds_ * G * 4);
     p.part = p.copy + align_up((size_t)T * p.ldc * 2);
     p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * T * m * 4) : 0);
     return p;
@@ -482,14 +485,20 @@ static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, v
     float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
     // (the staging offsets of a token block are 31 bits)
     const bool direct = w.n % 64 == 0 && ldx % 8 == 0 && ldx <= (1 << 21) && aligned16(x);
-    if (p.TA > 1)
+    // Small tiles make X themselves, unless there is a pass that copies and
+    // enough of them that their arithmetic counts (900 tokens x 3500 x 3500, a
+    // copy: 53 us with products of their own, 49 without; 100 x 300 x 5000,
+    // eight splits: 16 and 20).
+    const bool own = p.TA == 1 && (direct || p.splits > 1);
+    if (!own)
         launch(nullptr, KK_Q4_SUMS, 0.0, 2.0 * T * w.n, direct ? k_q4_sums<X, false> : k_q4_sums<X, true>,
                dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, w.G, sums, p.lds_, copy, p.ldc);
     else if (!direct) copy_enqueue<X>(xp, ldx, T, w.n, copy, p.ldc, s);
     if (!direct) xp = copy, ldx = p.ldc;
     if (p.TA == 4) prompt_launch<X, 4, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
     else if (p.TA == 2) prompt_launch<X, 2, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
-    else prompt_launch<X, 1, 2, true>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
+    else if (own) prompt_launch<X, 1, 2, true>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
+    else prompt_launch<X, 1, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.m, nullptr, yp, ldy, s);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
