@@ -150,11 +150,6 @@ int q4_zero_enqueue(void* y, int64_t ld, int64_t rows, int64_t cols, hipStream_t
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
-#ifndef FW
-#define FW 8
-#define FU 2
-#define FR 1
-#endif
 template <class X, int TQ, int R, int WAVES, int U>
 static void few_launch(const uint16_t* x, int64_t ldx, int T, const Q4Layer& w, uint16_t* y, int64_t ldy, hipStream_t s)
 {
@@ -167,12 +162,14 @@ static void few_launch(const uint16_t* x, int64_t ldx, int T, const Q4Layer& w, 
 // Two row tiles per workgroup where that still gives every CU one: they share
 // the reads of x (16 tokens x 14336 x 4096: 12.0 us with one, 10.1 with two;
 // one token x 4096 x 14336, where two would leave half the CUs idle: 8.2 with
-// one, 10.2 with two).
-template <class X, int TQ, int U>
+// one, 10.2 with two).  Up to four tokens a lone row tile is spread over 16
+// waves, a block each at a time, instead of 8 with two (one token x 4096 x
+// 14336: 7.7 us and 8.1; two row tiles, 14336 x 4096: 8.9 and 8.0).
+template <class X, int TQ, int WAVES, int U>
 static void few_rows(const uint16_t* x, int64_t ldx, int T, const Q4Layer& w, uint16_t* y, int64_t ldy, hipStream_t s)
 {
-    if (w.RT >= 512) few_launch<X, TQ, 2, 8, U>(x, ldx, T, w, y, ldy, s);
-    else few_launch<X, TQ, 1, 8, U>(x, ldx, T, w, y, ldy, s);
+    if (w.RT >= 512) few_launch<X, TQ, 2, 8, WAVES * U / 8>(x, ldx, T, w, y, ldy, s);
+    else few_launch<X, TQ, 1, WAVES, U>(x, ldx, T, w, y, ldy, s);
 }
 
 template <class X>
@@ -181,11 +178,11 @@ static void few_enqueue(const void* x, int64_t ldx, int64_t T, const Q4Layer& w,
     const uint16_t* xp = static_cast<const uint16_t*>(x);
     uint16_t* yp = static_cast<uint16_t*>(y);
     const int t = (int)T;
-    if (T <= 4) few_rows<X, 1, 2>(xp, ldx, t, w, yp, ldy, s);
-    else if (T <= 8) few_rows<X, 2, 2>(xp, ldx, t, w, yp, ldy, s);
-    else if (T <= 16) few_rows<X, 4, 2>(xp, ldx, t, w, yp, ldy, s);
-    else if (T <= 32) few_rows<X, 8, 1>(xp, ldx, t, w, yp, ldy, s);
-    else few_rows<X, 16, 1>(xp, ldx, t, w, yp, ldy, s);
+    if (T <= 4) few_rows<X, 1, 16, 1>(xp, ldx, t, w, yp, ldy, s);
+    else if (T <= 8) few_rows<X, 2, 8, 2>(xp, ldx, t, w, yp, ldy, s);
+    else if (T <= 16) few_rows<X, 4, 8, 2>(xp, ldx, t, w, yp, ldy, s);
+    else if (T <= 32) few_rows<X, 8, 8, 1>(xp, ldx, t, w, yp, ldy, s);
+    else few_rows<X, 16, 8, 1>(xp, ldx, t, w, yp, ldy, s);
 }
 
 }  // namespace bk

@@ -36,6 +36,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gemm.hpp"
 #include "internal.hpp"
 
@@ -80,13 +82,22 @@ struct Q4Layer {
     const f32x2* grid;
     const float* unit;
     int m, n, RT, KB, G, gb;
+    uint32_t gm;                  // ceil(2^21 / gb), for group_of
 };
+
+// The group of 64-column half h (< 1024): h / gb as one multiplication, exact
+// since h (gm gb - 2^21) < 2^21.  An integer division, ahead of the loads that
+// wait for it, costs 0.2 us of a few-token kernel's step.
+constexpr int kQ4MaxHalves = BAKRON_MAX_DIM / 64;
+static_assert(kQ4MaxHalves <= 1024, "group_of's range");
+__device__ __forceinline__ int group_of(uint32_t h, uint32_t gm, int G) { return (int)min(h * gm >> 21, (uint32_t)G - 1); }
 
 inline Q4Layer q4_layer(const void* packed, const Q4Dims& d)
 {
     const char* p = static_cast<const char*>(packed);
     return Q4Layer{reinterpret_cast<const u32x4*>(p), reinterpret_cast<const f32x2*>(p + d.grid_at),
-                   reinterpret_cast<const float*>(p + d.unit_at), (int)d.m, (int)d.n, d.RT, d.KB, d.G, d.gb};
+                   reinterpret_cast<const float*>(p + d.unit_at), (int)d.m, (int)d.n, d.RT, d.KB, d.G, d.gb,
+                   (uint32_t)ceil_div(1 << 21, std::min(d.gb, kQ4MaxHalves))};
 }
 
 // (w & mask) | base.  The constants pass through empty asm statements so that

@@ -52,7 +52,8 @@ struct FewSpan {
     const char* codes[R];     // uniform: the row tile's first block
     const char* grid[R];
     f32x4 acc[R][NT];
-    int n, KB, G, gb;
+    int n, KB, G;
+    uint32_t gm;
     char* lds;
 
     __device__ __forceinline__ FewSpan(char* wave_lds) : lds(wave_lds) {}
@@ -61,7 +62,7 @@ struct FewSpan {
     template <int N>
     __device__ __forceinline__ void rows(const Q4Layer (&w)[N], int rt)
     {
-        n = w[0].n, KB = w[0].KB, G = w[0].G, gb = w[0].gb;
+        n = w[0].n, KB = w[0].KB, G = w[0].G, gm = w[0].gm;
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             const int64_t tile = min(rt + j % (R / N), w[0].RT - 1);
@@ -90,7 +91,7 @@ struct FewSpan {
         const uint32_t lane = threadIdx.x & 63;
         uint32_t g[NG];
 #pragma unroll
-        for (int h = 0; h < NG; ++h) g[h] = 128u * (uint32_t)min((2 * kb + h) / gb, G - 1) + 8u * (lane & 15);
+        for (int h = 0; h < NG; ++h) g[h] = 128u * (uint32_t)group_of(2 * kb + h, gm, G) + 8u * (lane & 15);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             b.c[j] = *reinterpret_cast<const u32x4*>(codes[j] + (1024u * (uint32_t)kb + 16u * lane));
@@ -101,10 +102,10 @@ struct FewSpan {
     // a block of 128 columns that all exist
     __device__ __forceinline__ void load(Block& b, int kb) const
     {
-        load_w(b, kb);
         const int k = kb * 128 + 8 * (threadIdx.x & 15);
 #pragma unroll
         for (int t = 0; t < TQ; ++t) b.x[t] = *reinterpret_cast<const u32x4_any*>(xr[t] + k);
+        load_w(b, kb);
     }
     __device__ __forceinline__ void load_cut(Block& b, int kb) const
     {
@@ -164,13 +165,20 @@ struct FewSpan {
     // blocks first, first + by, ... below end
     __device__ __forceinline__ void run(int first, int by, int end)
     {
-        const int whole = min(n / kQ4Cols, end);
-        for (int kb0 = first; kb0 < whole; kb0 += by * U) {
+        const int whole = min(n / kQ4Cols, end), count = whole > first ? (whole - first + by - 1) / by : 0;
+        for (int i = 0; i < count; i += U) {
             Block b[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) load(b[u], min(kb0 + by * u, whole - 1));
+            for (int u = 0; u < U; ++u) load(b[u], first + by * min(i + u, count - 1));
+            // every load before the first wait, and the blocks in the order of
+            // their loads: left to itself the compiler waits for single ones
+            // (32 tokens x 4096 x 4096: 8.5 us, so 7.1)
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) add(b[u], kb0 + by * u < whole ? 1.f : 0.f);
+            for (int u = 0; u < U; ++u) {
+                add(b[u], i + u < count ? 1.f : 0.f);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         if (whole < end && whole >= first && (whole - first) % by == 0) {
             Block b;

@@ -35,8 +35,13 @@ constexpr int kMoeTopK = BAKRON_Q4_MOE_MAX_TOP_K;
 constexpr int kMoeExperts = BAKRON_Q4_MAX_LAYERS;
 constexpr int kMoePairs = kMoeTokens * kMoeTopK;
 
-// The choices sorted by expert, as k_q4_moe_up leaves them for k_q4_moe_down:
-// choice t k + j is of token t.
+// A choice: p = t k + j, the j-th of token t, with its token beside it (a
+// division by k, 20 instructions, where it is made and not where it is used).
+__device__ __forceinline__ int32_t moe_choice(int t, int p) { return t << 16 | p; }
+__device__ __forceinline__ int choice_token(int32_t c) { return c >> 16; }
+__device__ __forceinline__ int choice_place(int32_t c) { return c & 0xFFFF; }
+
+// The choices sorted by expert, as k_q4_moe_up leaves them for k_q4_moe_down.
 struct MoePlan {
     int32_t active;                    // experts that some token chose, ascending:
     int32_t expert[kMoeExperts];
@@ -170,7 +175,7 @@ __device__ void moe_choose(const float* __restrict__ logits, int T, int E, int k
         for (int p0 = 0; p0 < pairs; p0 += 64) {
             const bool in = p0 + lane < pairs && chosen[min(p0 + lane, pairs - 1)] == e;
             const unsigned long long b = __ballot(in);
-            if (in) plan->pair[at + __popcll(b & ((1ull << lane) - 1))] = p0 + lane;
+            if (in) plan->pair[at + __popcll(b & ((1ull << lane) - 1))] = moe_choice((p0 + lane) / k, p0 + lane);
             at += __popcll(b);
         }
     }
@@ -191,7 +196,7 @@ __device__ __forceinline__ Q4Layer moe_layer(Q4Layer w, int e, int64_t layer_byt
 // either activation type, and no rounding that the result sees.
 template <class X, int TQ, int U, int WS, bool HALF>
 __device__ __forceinline__ void moe_up(const uint16_t* __restrict__ x, int64_t ldx, const Q4Layer (&w)[2], int rt0,
-                                       const int16_t* list, int n, int k, char* lds, uint16_t* __restrict__ hi,
+                                       const int32_t* list, int n, char* lds, uint16_t* __restrict__ hi,
                                        uint16_t* __restrict__ lo, int64_t lda)
 {
     typedef FewSpan<X, TQ, 2, U, HALF> Span;
@@ -199,7 +204,7 @@ __device__ __forceinline__ void moe_up(const uint16_t* __restrict__ x, int64_t l
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint16_t* xr[TQ];
 #pragma unroll
-    for (int t = 0; t < TQ; ++t) xr[t] = x + (int64_t)(list[min(4 * t + (lane >> 4), n - 1)] / k) * ldx;
+    for (int t = 0; t < TQ; ++t) xr[t] = x + (int64_t)choice_token(list[min(4 * t + (lane >> 4), n - 1)]) * ldx;
     Span span(lds + wave * few_lds(4));
     span.template rows<2>(w, rt0 + wave / WS);
     span.tokens(xr);
@@ -220,7 +225,7 @@ __device__ __forceinline__ void moe_up(const uint16_t* __restrict__ x, int64_t l
         if (c < n && rt0 + tile < w[0].RT) {
             const float v = a / (1.f + expf(-a)) * b;
             const uint16_t vh = Bf16::down(v);
-            const int64_t at = (int64_t)list[c] * lda + (rt0 + tile) * 16 + (lane & 15);
+            const int64_t at = (int64_t)choice_place(list[c]) * lda + (rt0 + tile) * 16 + (lane & 15);
             hi[at] = vh;
             lo[at] = Bf16::down(v - Bf16::up(vh));
         }
@@ -261,7 +266,7 @@ __global__ __launch_bounds__(512, 4) void k_q4_moe_up(const uint16_t* __restrict
                                                       float* __restrict__ weights, MoePlan* __restrict__ plan)
 {
     __shared__ __align__(16) char lds[8 * few_lds(4)];
-    __shared__ int16_t list[kMoeTokens];
+    __shared__ int32_t list[kMoeTokens];
     __shared__ int rank[kMoeTokens];
     __shared__ int expert;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -289,13 +294,13 @@ __global__ __launch_bounds__(512, 4) void k_q4_moe_up(const uint16_t* __restrict
     const unsigned long long b = __ballot(mine);
     const int n = __popcll(b);
     if (n == 0 || ((int)gridDim.y < E && __ffsll(b) - 1 < first)) return;
-    if (wave == 0 && mine) list[__popcll(b & ((1ull << lane) - 1))] = (int16_t)(lane * k + rank[lane]);
+    if (wave == 0 && mine) list[__popcll(b & ((1ull << lane) - 1))] = moe_choice(lane, lane * k + rank[lane]);
     __syncthreads();
     const Q4Layer w[2] = {moe_layer(gate, e, layer_bytes), moe_layer(up, e, layer_bytes)};
     for (int n0 = 0; n0 < n; n0 += 16) {
         const int nn = min(16, n - n0);
-        if (nn <= 4) moe_up<X, 1, 2, WS, HALF>(x, ldx, w, 8 / WS * rt, list + n0, nn, k, lds, hi, lo, lda);
-        else moe_up<X, 4, 1, WS, HALF>(x, ldx, w, 8 / WS * rt, list + n0, nn, k, lds, hi, lo, lda);
+        if (nn <= 4) moe_up<X, 1, 2, WS, HALF>(x, ldx, w, 8 / WS * rt, list + n0, nn, lds, hi, lo, lda);
+        else moe_up<X, 4, 1, WS, HALF>(x, ldx, w, 8 / WS * rt, list + n0, nn, lds, hi, lo, lda);
     }
 }
 
@@ -306,7 +311,7 @@ __global__ __launch_bounds__(512, 4) void k_q4_moe_up(const uint16_t* __restrict
 // p times the sums to the wave's ys[token][row].
 template <int TQ, bool HALF>
 __device__ __forceinline__ void moe_down(const uint16_t* __restrict__ hi, const uint16_t* __restrict__ lo, int64_t lda,
-                                         const Q4Layer& w, int rt, int kb0, int kb1, const int32_t* pair, int n, int k,
+                                         const Q4Layer& w, int rt, int kb0, int kb1, const int32_t* pair, int n,
                                          const float* weights, char* lds, float (*ys)[16])
 {
     typedef FewSpan<Bf16, TQ, 1, 2, HALF> Span;
@@ -315,7 +320,7 @@ __device__ __forceinline__ void moe_down(const uint16_t* __restrict__ hi, const 
 #pragma unroll
     for (int t = 0; t < TQ; ++t) {
         const int c = min(4 * t + q, 2 * n - 1);
-        xr[t] = (c < n ? hi : lo) + (int64_t)pair[c < n ? c : c - n] * lda;
+        xr[t] = (c < n ? hi : lo) + (int64_t)choice_place(pair[c < n ? c : c - n]) * lda;
     }
     Span span(lds);
     const Q4Layer ws[1] = {w};
@@ -330,8 +335,7 @@ __device__ __forceinline__ void moe_down(const uint16_t* __restrict__ hi, const 
         for (int e = 0; e < 4; ++e) {
             const int c = 4 * q + e - part * n;
             if (c >= 0 && c < n) {
-                const int p = pair[c];
-                ys[p / k][r] += weights[p] * span.acc[0][0][e];
+                ys[choice_token(pair[c])][r] += weights[choice_place(pair[c])] * span.acc[0][0][e];
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -377,9 +381,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_q4_moe_down(const uint16_t*
         for (int s = s0; s < s1; s += 8) {
             const int n = min(8, s1 - s);
             if (n <= 2)
-                moe_down<1, HALF>(hi, lo, lda, w, rt, kb0, kb1, pl.pair + s, n, k, share, stage[wave], ys);
+                moe_down<1, HALF>(hi, lo, lda, w, rt, kb0, kb1, pl.pair + s, n, share, stage[wave], ys);
             else
-                moe_down<4, HALF>(hi, lo, lda, w, rt, kb0, kb1, pl.pair + s, n, k, share, stage[wave], ys);
+                moe_down<4, HALF>(hi, lo, lda, w, rt, kb0, kb1, pl.pair + s, n, share, stage[wave], ys);
         }
         i += kb1 - kb0;
     }
