@@ -461,15 +461,15 @@ static int moe_enqueue(const void* x, int64_t ldx, int64_t T, const void* router
            static_cast<const uint16_t*>(router), (int)E, logits, done, dd.RT);
     const int64_t slots = std::min<int64_t>(E, T * k);
     // Waves per row tile: as many as keep the launch to two rounds of the 4096
-    // waves that fit the chip at this kernel's registers (16 tokens, 64 experts
-    // of 2048 x 1024: 42 us with 2 waves, 65 with 8; one token, 2 of 8 experts
-    // of 4096 x 14336: 30 us with 4, 37 with 8).
+    // waves that fit the chip at this kernel's registers, at least two (16
+    // tokens, 64 experts of 2048 x 1024: 42 us with 2 waves, 65 with 8; one
+    // token, 2 of 8 experts of 4096 x 14336: 30 us with 4, 37 with 8; 16 tokens,
+    // 16 experts of 4096 x 14336, whole call: 303 us with 2, 333 with 1).
     const int64_t waves = du.RT * slots;
-    auto* kup = k_q4_moe_up<X, 1, HALF>;
-    int per = 1;
+    auto* kup = k_q4_moe_up<X, 2, HALF>;
+    int per = 2;
     if (8 * waves <= 8192) kup = k_q4_moe_up<X, 8, HALF>, per = 8;
     else if (4 * waves <= 8192) kup = k_q4_moe_up<X, 4, HALF>, per = 4;
-    else if (2 * waves <= 8192) kup = k_q4_moe_up<X, 2, HALF>, per = 2;
     launch(nullptr, KK_Q4_MOE_UP, 4.0 * T * k * h * f, 0.0, kup,
            dim3((unsigned)(ceil_div(du.RT, 8 / per) + 1), (unsigned)slots), dim3(512), s, xp, ldx, (int)T,
            q4_layer(gate, du), q4_layer(up, du), (int64_t)du.bytes, logits, (int)E, k, hi, lo, w.lda, ids, weights, plan);
