@@ -395,23 +395,35 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
     tile_store<X, TA>(acc, 1.f, lds + wave * kStoreBytes, tw, T, rw, w.m, y, ldy);
 }
 
-// y = f times the sum of `splits` partial results, in order.
+// y = f times the sum of `splits` partial results, in order; a row of blocks
+// per token, eight loads in flight.
 template <class X>
 __global__ __launch_bounds__(256) void k_q4_join(const float* __restrict__ part, int splits, int T, int m,
                                                  const float* __restrict__ f, uint16_t* __restrict__ y, int64_t ldy)
 {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)T * m;
-    if (e >= all) return;
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col >= m) return;
+    const int64_t all = (int64_t)T * m;
+    const float* p = part + (int64_t)blockIdx.y * m + col;
+    constexpr int U = 8;
     float v = 0.f;
-    for (int u = 0; u < splits; ++u) v += part[u * all + e];
-    y[e / m * ldy + e % m] = X::down(v * (f && *f > 0.f ? *f : 1.f));
+    for (int u0 = 0; u0 < splits; u0 += U) {
+        float a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) a[u] = p[min(u0 + u, splits - 1) * all];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v += u0 + u < splits ? a[u] : 0.f;
+    }
+    y[blockIdx.y * ldy + col] = X::down(v * (f && *f > 0.f ? *f : 1.f));
 }
 
+// (results are shared out only where they make at most 128 tiles of 64 tokens:
+// T is a grid's y)
 template <class X>
 void join_enqueue(const float* part, int splits, int64_t T, int m, const float* f, uint16_t* y, int64_t ldy, hipStream_t s)
 {
-    launch(nullptr, KK_Q4_JOIN, 0.0, 4.0 * splits * T * m, k_q4_join<X>, dim3((unsigned)ceil_div(T * m, 256)), dim3(256), s,
-           part, splits, (int)T, m, f, y, ldy);
+    launch(nullptr, KK_Q4_JOIN, 0.0, 4.0 * splits * T * m, k_q4_join<X>, dim3((unsigned)ceil_div(m, 256), (unsigned)T),
+           dim3(256), s, part, splits, (int)T, m, f, y, ldy);
 }
 template void join_enqueue<Bf16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
 template void join_enqueue<Fp16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
@@ -436,12 +448,13 @@ static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
     if (ceil_div(T, 256) * ceil_div(m, 256) >= 224) p.TA = 4;
     else if (ceil_div(T, 128) * ceil_div(m, 256) >= 192) p.TA = 2;
     else p.TA = 1, p.WR = 2;
-    // Small problems: a workgroup per CU, down to four column blocks each (65
-    // tokens x 4096 x 4096: 16 us with 4 splits, 33 without).
+    // Small problems: a workgroup per CU, down to two column blocks each (65
+    // tokens x 4096 x 4096: 16 us with 4 splits, 33 without; 128 tokens x 1024 x
+    // 1024: 8.5 us with 4, 10.0 with 2).
     p.splits = 1;
     if (p.TA == 1) {
         const int64_t tiles = ceil_div(T, 64) * ceil_div(m, 128);
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, 256 / tiles, ceil_div(n, kQ4Cols) / 4}));
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, 256 / tiles, ceil_div(n, kQ4Cols) / 2}));
     }
     p.lds_ = ceil_div(T, 256) * 256;
     p.ldc = ceil_div(n, 64) * 64;
