@@ -248,8 +248,18 @@ static GradPlan grad_plan(int64_t T, int64_t m, int64_t n)
 {
     GradPlan p;
     const int64_t nj = ceil_div(n, 256);
-    // the largest tiles that still give every CU about one, as in the layer
-    p.TA = ceil_div(T, 256) * nj >= 224 ? 4 : ceil_div(T, 128) * nj >= 192 ? 2 : 1;
+    // The tile that leaves the busiest CU the least time, as in the layer: costs
+    // are 4096 rows of a tile in us with the chip full (4096 tokens x 4096 columns
+    // in tiles of 256 tokens: 135 us; 2048 in 128: 92; 1024 in 64: 71, and 4096:
+    // 242).  3500 tokens x 2500 columns x 3500: 139 us with 128, 111 with 256.
+    static constexpr struct {
+        int TA, cost;
+    } shapes[] = {{4, 130}, {2, 88}, {1, 64}};
+    int64_t least = 0;
+    for (const auto& c : shapes) {
+        const int64_t cost = ceil_div(ceil_div(T, 64 * c.TA) * nj, 256) * c.cost;
+        if (!least || cost < least) least = cost, p.TA = c.TA;
+    }
     // small problems: a workgroup per CU, down to two chunks of 64 rows each
     p.splits = 1;
     if (p.TA == 1) {

@@ -98,7 +98,9 @@ struct Prompt {
     static constexpr int BR = 64 * WR;                // rows of W of a workgroup
     static constexpr int XBUF = BT * 128;             // bytes of a 64-column chunk of x
     static constexpr int WBUF = BR * 64;              // bytes of a 128-column block of codes
-    static constexpr int AHEAD = TA == 4 ? 2 : 3;     // chunks in flight (LDS has no room for 3 of TA = 4)
+    // chunks in flight: LDS has no room for 3 of TA = 4, nor of two workgroups of
+    // TA = WR = 2
+    static constexpr int AHEAD = TA == 4 || (TA == 2 && WR == 2) ? 2 : 3;
     static constexpr int NX = AHEAD + 1, NW = (AHEAD + 1) / 2 + 2;
     static constexpr int XLOADS = BT / 8 / (2 * WR);  // direct loads of a wave per chunk of x (8 tokens each)
     static constexpr int LOADS = XLOADS + 2;          // one of the grid and one of codes
@@ -440,14 +442,21 @@ struct PromptPlan {
 static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
 {
     PromptPlan p;
-    // The largest tiles that still give every CU about one: a large tile
-    // expands a code for more tokens (2048 tokens x 4096 x 4096: 76 us with TA =
-    // 2, 95 with 1), a missing workgroup costs in proportion (1024 tokens, 128
-    // tiles of TA = 2: 68 us, 512 of TA = 1: 54).
-    p.WR = 4;
-    if (ceil_div(T, 256) * ceil_div(m, 256) >= 224) p.TA = 4;
-    else if (ceil_div(T, 128) * ceil_div(m, 256) >= 192) p.TA = 2;
-    else p.TA = 1, p.WR = 2;
+    // The tile that leaves the busiest CU the least time: the tiles it gets
+    // times a tile's cost, 4096 columns of it in us with the chip full (4096
+    // tokens x 4096 rows in 256 x 256: 128 us; 2048 in 128 x 256: 80; 1024 in 128
+    // x 128: 49, and 2048: 82; 1024 in 64 x 128: 57, and 512: 36).  A large tile
+    // expands a code for more tokens; a smaller one wins where the large ones
+    // are too few, or a few too many: 3500 tokens x 2500 rows x 3500, 280 of 128
+    // x 256, takes 102 us and 87 in 560 of 128 x 128.
+    static constexpr struct {
+        int TA, WR, cost;
+    } shapes[] = {{4, 4, 128}, {2, 4, 80}, {2, 2, 42}, {1, 2, 26}};
+    int64_t least = 0;
+    for (const auto& c : shapes) {
+        const int64_t cost = ceil_div(ceil_div(T, 64 * c.TA) * ceil_div(m, 64 * c.WR), 256) * c.cost;
+        if (!least || cost < least) least = cost, p.TA = c.TA, p.WR = c.WR;
+    }
     // Small problems: a workgroup per CU, down to two column blocks each (65
     // tokens x 4096 x 4096: 16 us with 4 splits, 33 without; 128 tokens x 1024 x
     // 1024: 8.5 us with 4, 10.0 with 2).
@@ -509,6 +518,7 @@ static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, v
     else if (!direct) copy_enqueue<X>(xp, ldx, T, w.n, copy, p.ldc, s);
     if (!direct) xp = copy, ldx = p.ldc;
     if (p.TA == 4) prompt_launch<X, 4, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
+    else if (p.TA == 2 && p.WR == 2) prompt_launch<X, 2, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
     else if (p.TA == 2) prompt_launch<X, 2, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
     else if (own) prompt_launch<X, 1, 2, true>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     else prompt_launch<X, 1, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
