@@ -247,25 +247,13 @@ struct GradPlan {
 static GradPlan grad_plan(int64_t T, int64_t m, int64_t n)
 {
     GradPlan p;
-    const int64_t nj = ceil_div(n, 256);
-    // The tile that leaves the busiest CU the least time, as in the layer: costs
-    // are 4096 rows of a tile in us with the chip full (4096 tokens x 4096 columns
-    // in tiles of 256 tokens: 135 us; 2048 in 128: 92; 1024 in 64: 71, and 4096:
-    // 242).  3500 tokens x 2500 columns x 3500: 139 us with 128, 111 with 256.
-    static constexpr struct {
-        int TA, cost;
-    } shapes[] = {{4, 130}, {2, 88}, {1, 64}};
-    int64_t least = 0;
-    for (const auto& c : shapes) {
-        const int64_t cost = ceil_div(ceil_div(T, 64 * c.TA) * nj, 256) * c.cost;
-        if (!least || cost < least) least = cost, p.TA = c.TA;
-    }
-    // small problems: a workgroup per CU, down to two chunks of 64 rows each
-    p.splits = 1;
-    if (p.TA == 1) {
-        const int64_t tiles = ceil_div(T, 64) * nj;
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({16, 256 / tiles, ceil_div(m, 64) / 2}));
-    }
+    // Costs: 4096 tokens x 4096 columns in tiles of 256 tokens take 135 us, 2048
+    // in 128 92, 1024 in 64 71 (and 4096 242).  3500 tokens x 2500 columns x 3500:
+    // 139 us with 128, 111 with 256.  A split has two chunks of 64 rows at least.
+    static constexpr TileShape shapes[] = {{256, 256, 130.0}, {128, 256, 88.0}, {64, 256, 64.0}};
+    const TileChoice c = tile_choose(shapes, T, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2));
+    p.TA = shapes[c.shape].tokens / 64;
+    p.splits = c.splits;
     p.ldc = ceil_div(m, 64) * 64;
     p.part = align_up((size_t)T * p.ldc * 2);
     p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * T * n * 4) : 0);
@@ -299,8 +287,8 @@ static int grad_run(const void* dy, int64_t lddy, int64_t T, const Q4Layer& w, v
         yp = copy;
         lddy = p.ldc;
     }
-    if (p.TA == 4) grad_launch<X, 4>(yp, lddy, T, w, xp, lddx, 1, part, s);
-    else if (p.TA == 2) grad_launch<X, 2>(yp, lddy, T, w, xp, lddx, 1, part, s);
+    if (p.TA == 4) grad_launch<X, 4>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
+    else if (p.TA == 2) grad_launch<X, 2>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
     else grad_launch<X, 1>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
     if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.n, w.unit, xp, lddx, s);
     return hipGetLastError() == hipSuccess ? 0 : -1;

@@ -397,16 +397,16 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
     tile_store<X, TA>(acc, 1.f, lds + wave * kStoreBytes, tw, T, rw, w.m, y, ldy);
 }
 
-// y = f times the sum of `splits` partial results, in order; a row of blocks
-// per token, eight loads in flight.
+// y = f times the sum of `splits` partial results, in order; blockIdx.x is the
+// token, eight loads are in flight.
 template <class X>
 __global__ __launch_bounds__(256) void k_q4_join(const float* __restrict__ part, int splits, int T, int m,
                                                  const float* __restrict__ f, uint16_t* __restrict__ y, int64_t ldy)
 {
-    const int col = blockIdx.x * 256 + threadIdx.x;
+    const int col = blockIdx.y * 256 + threadIdx.x;
     if (col >= m) return;
     const int64_t all = (int64_t)T * m;
-    const float* p = part + (int64_t)blockIdx.y * m + col;
+    const float* p = part + (int64_t)blockIdx.x * m + col;
     constexpr int U = 8;
     float v = 0.f;
     for (int u0 = 0; u0 < splits; u0 += U) {
@@ -416,15 +416,13 @@ __global__ __launch_bounds__(256) void k_q4_join(const float* __restrict__ part,
 #pragma unroll
         for (int u = 0; u < U; ++u) v += u0 + u < splits ? a[u] : 0.f;
     }
-    y[blockIdx.y * ldy + col] = X::down(v * (f && *f > 0.f ? *f : 1.f));
+    y[blockIdx.x * ldy + col] = X::down(v * (f && *f > 0.f ? *f : 1.f));
 }
 
-// (results are shared out only where they make at most 128 tiles of 64 tokens:
-// T is a grid's y)
 template <class X>
 void join_enqueue(const float* part, int splits, int64_t T, int m, const float* f, uint16_t* y, int64_t ldy, hipStream_t s)
 {
-    launch(nullptr, KK_Q4_JOIN, 0.0, 4.0 * splits * T * m, k_q4_join<X>, dim3((unsigned)ceil_div(m, 256), (unsigned)T),
+    launch(nullptr, KK_Q4_JOIN, 0.0, 4.0 * splits * T * m, k_q4_join<X>, dim3((unsigned)T, (unsigned)ceil_div(m, 256)),
            dim3(256), s, part, splits, (int)T, m, f, y, ldy);
 }
 template void join_enqueue<Bf16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
@@ -442,29 +440,18 @@ struct PromptPlan {
 static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
 {
     PromptPlan p;
-    // The tile that leaves the busiest CU the least time: the tiles it gets
-    // times a tile's cost, 4096 columns of it in us with the chip full (4096
-    // tokens x 4096 rows in 256 x 256: 128 us; 2048 in 128 x 256: 80; 1024 in 128
-    // x 128: 49, and 2048: 82; 1024 in 64 x 128: 57, and 512: 36).  A large tile
-    // expands a code for more tokens; a smaller one wins where the large ones
-    // are too few, or a few too many: 3500 tokens x 2500 rows x 3500, 280 of 128
-    // x 256, takes 102 us and 87 in 560 of 128 x 128.
-    static constexpr struct {
-        int TA, WR, cost;
-    } shapes[] = {{4, 4, 128}, {2, 4, 80}, {2, 2, 42}, {1, 2, 26}};
-    int64_t least = 0;
-    for (const auto& c : shapes) {
-        const int64_t cost = ceil_div(ceil_div(T, 64 * c.TA) * ceil_div(m, 64 * c.WR), 256) * c.cost;
-        if (!least || cost < least) least = cost, p.TA = c.TA, p.WR = c.WR;
-    }
-    // Small problems: a workgroup per CU, down to two column blocks each (65
-    // tokens x 4096 x 4096: 16 us with 4 splits, 33 without; 128 tokens x 1024 x
-    // 1024: 8.5 us with 4, 10.0 with 2).
-    p.splits = 1;
-    if (p.TA == 1) {
-        const int64_t tiles = ceil_div(T, 64) * ceil_div(m, 128);
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, 256 / tiles, ceil_div(n, kQ4Cols) / 2}));
-    }
+    // Costs: 4096 tokens x 4096 rows in tiles of 256 x 256 take 128 us, 2048 in
+    // 128 x 256 80, 1024 in 128 x 128 49 and 2048 82, 512 in 64 x 128 36.  A large
+    // tile expands a code for more tokens; a smaller one wins where the large
+    // ones are too few, or a few too many: 3500 tokens x 2500 rows x 3500, 280
+    // tiles of 128 x 256, takes 102 us and 87 in 560 of 128 x 128.  A split has two
+    // column blocks at least (65 tokens x 4096 x 4096: 16 us with 4 splits, 33
+    // without; 128 tokens x 1024 x 1024: 8.5 us with 4, 10.0 with 2).
+    static constexpr TileShape shapes[] = {{256, 256, 128.0}, {128, 256, 80.0}, {128, 128, 42.0}, {64, 128, 28.0}};
+    const TileChoice c = tile_choose(shapes, T, m, n, std::min<int64_t>(8, ceil_div(n, kQ4Cols) / 2));
+    p.TA = shapes[c.shape].tokens / 64;
+    p.WR = shapes[c.shape].cols / 64;
+    p.splits = c.splits;
     p.lds_ = ceil_div(T, 256) * 256;
     p.ldc = ceil_div(n, 64) * 64;
     p.sums = 0;
@@ -517,9 +504,9 @@ static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, v
                dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, w.G, sums, p.lds_, copy, p.ldc);
     else if (!direct) copy_enqueue<X>(xp, ldx, T, w.n, copy, p.ldc, s);
     if (!direct) xp = copy, ldx = p.ldc;
-    if (p.TA == 4) prompt_launch<X, 4, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
-    else if (p.TA == 2 && p.WR == 2) prompt_launch<X, 2, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
-    else if (p.TA == 2) prompt_launch<X, 2, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, 1, part, s);
+    if (p.TA == 4) prompt_launch<X, 4, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
+    else if (p.TA == 2 && p.WR == 2) prompt_launch<X, 2, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
+    else if (p.TA == 2) prompt_launch<X, 2, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     else if (own) prompt_launch<X, 1, 2, true>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     else prompt_launch<X, 1, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.m, nullptr, yp, ldy, s);

@@ -68,6 +68,34 @@ __device__ __forceinline__ void tile_store(const f32x16 (&acc)[TA][2], float f, 
     }
 }
 
+// Host: which of the tile shapes a product over `depth` terms takes, and over
+// how many workgroups each tile's terms are shared out: the choice that leaves
+// the busiest CU the least time.  That is the tiles it gets times a tile's cost,
+// and for shared tiles a launch that joins them and their partial sums' way
+// through memory (at 4 TB/s, there and back).
+struct TileShape {
+    int tokens, cols;
+    double us;   // 4096 terms of a tile, the chip full of them
+};
+struct TileChoice {
+    int shape, splits;
+};
+template <int N>
+inline TileChoice tile_choose(const TileShape (&shapes)[N], int64_t T, int64_t cols, int64_t depth, int64_t most)
+{
+    TileChoice best = {0, 1};
+    double least = 0.0;
+    for (int i = 0; i < N; ++i) {
+        const int64_t tiles = ceil_div(T, shapes[i].tokens) * ceil_div(cols, shapes[i].cols);
+        for (int s = 1; s == 1 || (s <= most && tiles * s <= 1024); ++s) {
+            const double us = ceil_div(tiles * s, 256) * shapes[i].us * depth / (4096.0 * s) +
+                              (s > 1 ? 2.0 + 8.0e-6 / 4 * s * T * cols : 0.0);
+            if (least == 0.0 || us < least) least = us, best = {i, s};
+        }
+    }
+    return best;
+}
+
 // A padded copy of x (T x n, n rounded up to 64 columns, zeros beyond n).
 template <class X>
 void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* copy, int64_t ldc, hipStream_t s);
