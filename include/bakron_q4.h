@@ -19,10 +19,18 @@
  *     (token t) starting at element t * ld, ld >= the row's length; only
  *     2-byte alignment is asked for (16-byte aligned rows, i.e. a 16-byte
  *     aligned pointer and ld a multiple of 8, are read fastest).
- *   - Sums are float32; results are rounded once to the activations' type.
+ *   - Sums are float32; results are rounded once to the activations' type
+ *     (beyond its largest value to infinity).
  *   - A non-finite value in a token's row makes that token's results
  *     non-finite (which of inf and NaN is not specified) and touches no
- *     other token.  |x| is at most 2^120.
+ *     other token.
+ *   - Range: sums are held in units of a step, so sum_j 31 |x_j|, and in a row
+ *     of several groups that sum times the ratio of any two of its steps, has
+ *     to stay below 2^127; beyond it a result may be infinite or NaN.
+ *   - A token's result does not depend on the other tokens of the call, but
+ *     for its last bits: their number, the alignment of the rows and, in
+ *     bakron_q4_moe, the experts that they chose decide on the order of its
+ *     sums.  The same call on the same inputs always gives the same bits.
  */
 #ifndef BAKRON_Q4_H
 #define BAKRON_Q4_H
@@ -59,7 +67,8 @@ size_t bakron_q4_packed_bytes(int64_t count, int64_t m, int64_t n, int64_t group
  *                  the low four bits are used).
  * scale, zero [in] count x m x G floats, G = ceil(n / group_size), or
  *                  count x m when group_size is 0: the grids the layer was
- *                  rounded with (finite).
+ *                  rounded with, finite.  A scale is 0 (its weights are 0) or
+ *                  of magnitude 2^-100 .. 2^100.  Neither is checked here.
  * count      [in]  0 <= count <= BAKRON_Q4_MAX_LAYERS.
  * m, n       [in]  0 <= m, n <= BAKRON_MAX_DIM.
  * group_size [in]  0 or a positive multiple of 64 (BAKRON_ERR_BAD_ARG
@@ -80,9 +89,7 @@ size_t bakron_q4_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, in
  *
  * x          [in]  tokens x n, row stride ldx.
  * tokens     [in]  0 <= tokens <= BAKRON_Q4_MAX_TOKENS; any number, from one
- *                  decoding token to a whole prompt.  A token's result does
- *                  not depend on the other tokens of the call, but its last
- *                  bits may depend on how many there are.
+ *                  decoding token to a whole prompt.
  * type       [in]  BAKRON_Q4_BF16 or BAKRON_Q4_FP16, of x and y.
  * packed, m, n, group_size [in] one layer as packed by bakron_q4_pack.
  * y          [out] tokens x m, row stride ldy.  n == 0 writes zeros; m == 0
@@ -97,7 +104,10 @@ size_t bakron_q4_linear_grad_workspace_bytes(int64_t tokens, int64_t m, int64_t 
 
 /*
  * bakron_q4_linear_grad -- the gradient of bakron_q4_linear with respect to
- * its input, dx = dy W: dx[t, j] = sum_i dy[t, i] w_ij.
+ * its input, dx = dy W: dx[t, j] = sum_i dy[t, i] w_ij.  Step and zero point
+ * change with the row that is summed over, so each weight is rounded once to
+ * dy's type (in units of about the layer's largest), as a layer kept in that
+ * type would be; the sums are float32.
  *
  * dy         [in]  tokens x m, row stride lddy.
  * dx         [out] tokens x n, row stride lddx.  m == 0 writes zeros; n == 0

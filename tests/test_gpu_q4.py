@@ -123,6 +123,33 @@ def test_large_tiles(T, wide, narrow, group):
     close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
 
 
+@pytest.mark.parametrize("T,m,n,group", [
+    (3498, 3458, 65, 64),       # layer: 256 x 256 tiles
+    (261, 6645, 74, 0),         # layer: 128 x 128
+    (2730, 143, 1791, 64),      # layer: 128 x 128, columns shared out; gradient: 256, rows not
+    (5100, 450, 3200, 128),     # layer: 256 x 256 or 128 x 128, columns shared out
+    (322, 64, 11732, 192),      # gradient: 128 tokens
+    (1922, 3401, 66, 64),       # gradient: 128 tokens, rows shared out
+    (3803, 6723, 68, 0),        # gradient: 256 tokens, rows shared out
+])
+def test_tiles_and_shared_sums(T, m, n, group):
+    dtype = torch.float16 if n % 2 else torch.bfloat16
+    layer = make_layer(m, n, group, T)
+    w, ref = pack(*layer, group), weights64(*layer, group)
+    x, dy = tokens(T, n, dtype, 1, pad=3), tokens(T, m, dtype, 2)
+    close(B.q4_linear(x, w), x.double().cpu().numpy() @ ref.T, dtype, LINEAR)
+    close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
+
+
+@pytest.mark.parametrize("scale", [2.0**-101, 2.0**101, float("nan"), -float("inf")])
+def test_steps_beyond_the_contract_are_refused(scale):
+    codes, step, zero = make_layer(40, 128, 64, 3)
+    B.q4_pack(dev(codes), dev(-step), dev(zero), group_size=64)
+    step[7, 1] = scale
+    with pytest.raises(B.GridError):
+        B.q4_pack(dev(codes), dev(step), dev(zero), group_size=64)
+
+
 @pytest.mark.parametrize("T", [3, 70])
 def test_offsets_beyond_32_bits(T):
     # rows 80 MB (2 GB at three tokens) apart, of inputs and of results

@@ -22,7 +22,13 @@
 //     blocks of all chosen experts evenly, keep their sums per token in LDS and
 //     are joined in wave order; splits are joined by the last one to finish, in
 //     split order.  No result depends on timing.
-// HBM bounds it: the chosen experts' codes and grids are read once.
+// HBM bounds it: the chosen experts' codes and grids are read once.  Measured,
+// router, up and down in turn: one token, 2 of 8 experts of 4096 x 14336, groups
+// of 128: 4, 28 (4.7 TB/s) and 15 - 19 us, the call 50 - 56; 16 tokens, 6 of 64
+// experts of 2048 x 1024, groups of 64: 6, 40 (3.1 TB/s) and 27, the call 74:
+// choosing, first round trips and the joins weigh more in short rows, and grids
+// are a fifth of the bytes; 16 tokens, 2 of 16 experts of 4096 x 14336: 309 us,
+// 4.5 TB/s over all.
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
@@ -462,8 +468,8 @@ static int moe_enqueue(const void* x, int64_t ldx, int64_t T, const void* router
     const int64_t slots = std::min<int64_t>(E, T * k);
     // Waves per row tile: as many as keep the launch to two rounds of the 4096
     // waves that fit the chip at this kernel's registers, at least two (16
-    // tokens, 64 experts of 2048 x 1024: 42 us with 2 waves, 65 with 8; one
-    // token, 2 of 8 experts of 4096 x 14336: 30 us with 4, 37 with 8; 16 tokens,
+    // tokens, 64 experts of 2048 x 1024: 40 us with 2 waves, 65 with 8; one
+    // token, 2 of 8 experts of 4096 x 14336: 28 us with 4, 37 with 8; 16 tokens,
     // 16 experts of 4096 x 14336, whole call: 303 us with 2, 333 with 1).
     const int64_t waves = du.RT * slots;
     auto* kup = k_q4_moe_up<X, 2, HALF>;

@@ -67,8 +67,9 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
     or m x ceil(n / group_size)) or of a stack of layers (one more dimension
     in front): codes uint8 in [0, 15], scale and zero float32, as solve() and
     gptq() take and return them.  ``check``: raise GridError if a code is
-    above 15 or a grid is not finite (reads them back to the host, which
-    waits for the work that makes them)."""
+    above 15, a scale neither 0 nor of magnitude 2^-100 .. 2^100 or a zero
+    point not finite (reads them back to the host, which waits for the work
+    that makes them)."""
     g = _group(group_size)
     if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
         raise ValueError("codes must be an m x n or count x m x n tensor")
@@ -81,11 +82,13 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
     _b._check_dev("scale", scale, torch.float32, gshape)
     _b._check_dev("zero", zero, torch.float32, gshape)
     if check and codes.numel():
-        high, finite = torch.stack((codes.max() > 15, torch.isfinite(scale).all() & torch.isfinite(zero).all())).tolist()
+        size = scale.abs()
+        steps = (((size >= 2.0**-100) & (size <= 2.0**100)) | (size == 0)).all()   # False for NaN
+        high, finite = torch.stack((codes.max() > 15, steps & torch.isfinite(zero).all())).tolist()
         if high:
             raise _b.GridError("codes must lie in [0, 15]")
         if not finite:
-            raise _b.GridError("scale and zero must be finite")
+            raise _b.GridError("scale must be 0 or of magnitude 2^-100 .. 2^100, zero finite")
     L = _b.lib()
     data = _b.workspace(L.bakron_q4_packed_bytes(count, m, n, g), codes.device)
     if stream is not None:
