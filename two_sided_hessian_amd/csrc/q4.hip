@@ -60,28 +60,53 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
 
 // Grids, and the unit: the exponent, rounded up, of the largest weight (a
 // maximum of integers, which does not depend on the order it is taken in).  A
-// few workgroups per layer, so that few atomics meet at the one place.
+// workgroup takes row tiles in turn, 16 lanes a row; a few workgroups per layer,
+// so that few atomics meet at the one place.
+//
+// A step of 0 (every weight 0, whatever the codes) is written as the row's
+// smallest step, zero point 0, on codes of 0: kernels divide by steps, and
+// k_q4_prompt counts a whole row in units of one step after the other, adding
+// 16 sum x under the present one and taking it off again.  Under a step above
+// the row's others (1, say) that difference's float32 error would bury them.
+// Rows without any step take the smallest normal number.
 constexpr int kPackGridBlocks = 128;
+constexpr float kPackNoStep = 0x1p-126f;
 
 __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ scale, const float* __restrict__ zero,
                                                       int64_t m, int RT, int G, int64_t layer_bytes, int64_t grid_at,
                                                       int64_t unit_at, char* __restrict__ packed)
 {
     __shared__ float tops[4];
-    const int64_t layer = blockIdx.y, all = (int64_t)RT * G * kQ4Rows;
+    __shared__ float least[16][kQ4Rows];
+    const int64_t layer = blockIdx.y;
+    const int r = threadIdx.x & 15, g0 = threadIdx.x >> 4;
     float top = 0.f;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < all; e += 256 * gridDim.x) {
-        const int64_t row = (e >> 4) / G * kQ4Rows + (e & 15), g = (e >> 4) % G;
-        f32x2 v = {0.f, 0.f};
-        if (row < m) {
-            v.x = scale[(layer * m + row) * G + g];
-            v.y = zero[(layer * m + row) * G + g];
-            // a step of 0 (every weight 0, whatever the codes) becomes step 1,
-            // zero point 0 on codes of 0: kernels divide by steps
-            if (v.x == 0.f) v = f32x2{1.f, 0.f};
-            else top = fmaxf(top, fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y)));
+    for (int tile = blockIdx.x; tile < RT; tile += gridDim.x) {
+        const int64_t row = (int64_t)tile * kQ4Rows + r;
+        const int64_t at = (layer * m + row) * G;
+        float low = INFINITY;
+        if (row < m)
+            for (int g = g0; g < G; g += 16) {
+                const float s = fabsf(scale[at + g]);
+                if (s > 0.f) low = fminf(low, s);
+            }
+        least[g0][r] = low;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) low = fminf(low, least[i][r]);
+        if (low == INFINITY) low = kPackNoStep;
+        f32x2* out = reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at) + (int64_t)tile * G * kQ4Rows + r;
+        for (int g = g0; g < G; g += 16) {
+            f32x2 v = {0.f, 0.f};
+            if (row < m) {
+                v.x = scale[at + g];
+                v.y = zero[at + g];
+                if (v.x == 0.f) v = f32x2{low, 0.f};
+                else top = fmaxf(top, fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y)));
+            }
+            out[g * kQ4Rows] = v;
         }
-        reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at)[e] = v;
+        __syncthreads();   // the next tile's minima overwrite these
     }
     for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
     if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
@@ -227,9 +252,8 @@ int bakron_q4_pack(const uint8_t* codes, const float* scale, const float* zero, 
                dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.KB, 4), (unsigned)count), dim3(256), stream, codes, scale,
                m, n, d.RT, d.KB, d.G, d.gb, (int64_t)d.bytes, (int64_t)d.unit_at, out);
     bk::launch(nullptr, bk::KK_Q4_PACK_GRID, 0.0, 16.0 * count * m * d.G, bk::k_q4_pack_grid,
-               dim3((unsigned)std::min<int64_t>(bk::kPackGridBlocks, bk::ceil_div((int64_t)d.RT * d.G * 16, 256)),
-                    (unsigned)count),
-               dim3(256), stream, scale, zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
+               dim3((unsigned)std::min(bk::kPackGridBlocks, d.RT), (unsigned)count), dim3(256), stream,
+               scale, zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
     return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
 }
 
