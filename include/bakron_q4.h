@@ -106,8 +106,9 @@ size_t bakron_q4_linear_grad_workspace_bytes(int64_t tokens, int64_t m, int64_t 
  * bakron_q4_linear_grad -- the gradient of bakron_q4_linear with respect to
  * its input, dx = dy W: dx[t, j] = sum_i dy[t, i] w_ij.  Step and zero point
  * change with the row that is summed over, so each weight is rounded once to
- * dy's type (in units of about the layer's largest), as a layer kept in that
- * type would be; the sums are float32.
+ * dy's type (in units of about the largest weight of its group's columns, in
+ * float16 down to 2^-29 of it without loss), as a layer kept in that type
+ * would be; the sums are float32.
  *
  * dy         [in]  tokens x m, row stride lddy.
  * dx         [out] tokens x n, row stride lddx.  m == 0 writes zeros; n == 0

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import two_sided_hessian_amd as B
-from q4_forms import few_form, prompt_form
-from test_gpu_q4 import LINEAR, close, make_layer, pack, tokens, weights64
+from q4_forms import few_form, grad_form, prompt_form
+from test_gpu_q4 import LINEAR, U, close, make_layer, pack, tokens, weights64
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,36 @@ def test_rows_of_step_zero(T, m, group):
         assert float(y[:, ::4].abs().max()) <= 2.0 ** -110
         dx = B.q4_linear_grad(tokens(T, m, dtype, 2), w)
         assert bool(torch.isfinite(dx).all())
+
+
+@pytest.mark.parametrize("T,m,form", [(1, 300, (64, 256, 2)), (130, 300, (64, 256, 1)), (300, 1500, (64, 256, 7)),
+                                      (8000, 700, (128, 256, 1))])
+def test_gradient_of_groups_of_very_different_steps(T, m, form):
+    """A group's columns of dx come from its own weights alone: they keep their
+    precision, 4 u of the rms of that group's part of a token, beside groups
+    (and under rows) whose steps are 2^16 times as large."""
+    n, group = 700, 64
+    assert grad_form(T, m, n) == form
+    codes, scale, zero = make_layer(m, n, group, 93)
+    scale *= (2.0 ** -np.arange(11.0) * 2.0 ** -6).astype(np.float32)
+    scale[:, 3] *= 2.0 ** 10
+    w, ref = pack(codes, scale, zero, group), weights64(codes, scale, zero, group)
+    for dtype in (torch.bfloat16, torch.float16):
+        dy = tokens(T, m, dtype, 2) * 2.0 ** 10
+        want, got = dy.double().cpu().numpy() @ ref, B.q4_linear_grad(dy, w)
+        for c in range(0, n, group):
+            close(got[:, c:c + group], want[:, c:c + group], dtype, 4 * U[dtype])
+
+
+def test_gradient_under_rows_that_a_token_leaves_out():
+    # the rows of large steps have gradients of zero: the others' weights count
+    m, n, group = 400, 320, 64
+    codes, scale, zero = make_layer(m, n, group, 94)
+    scale[5] *= 2.0 ** 17
+    scale[300, 2] *= 2.0 ** 19
+    w, ref = pack(codes, scale, zero, group), weights64(codes, scale, zero, group)
+    for dtype in (torch.bfloat16, torch.float16):
+        for T in (1, 130):
+            dy = tokens(T, m, dtype, 2).clone()
+            dy[:, [5, 300]] = 0
+            close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])

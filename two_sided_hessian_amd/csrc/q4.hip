@@ -26,8 +26,9 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
                                                  int64_t m, int64_t n, int RT, int KB, int G, int gb,
                                                  int64_t layer_bytes, int64_t unit_at, char* __restrict__ packed)
 {
-    if (blockIdx.x == 0 && threadIdx.x == 0)   // k_q4_pack_grid raises it
-        *reinterpret_cast<float*>(packed + blockIdx.y * layer_bytes + unit_at) = 0.f;
+    if (blockIdx.x == 0)   // k_q4_pack_grid raises them
+        for (int g = threadIdx.x; g < G; g += 256)
+            reinterpret_cast<float*>(packed + blockIdx.y * layer_bytes + unit_at)[g] = 0.f;
     const int64_t block = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (block >= (int64_t)RT * KB) return;
     const int64_t layer = blockIdx.y;
@@ -58,10 +59,10 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
     reinterpret_cast<u32x4*>(packed + layer * layer_bytes)[block * 64 + 16 * q + r] = out;
 }
 
-// Grids, and the unit: the exponent, rounded up, of the largest weight (a
-// maximum of integers, which does not depend on the order it is taken in).  A
-// workgroup takes row tiles in turn, 16 lanes a row; a few workgroups per layer,
-// so that few atomics meet at the one place.
+// Grids, and the units: the exponent, rounded up, of the largest weight of each
+// group's columns (a maximum of integers, which does not depend on the order it
+// is taken in).  A workgroup takes row tiles in turn, 16 lanes a row; a few
+// workgroups per layer, so that few atomics meet at a unit.
 //
 // A step of 0 (every weight 0, whatever the codes) is written as the row's
 // smallest step, zero point 0, on codes of 0: kernels divide by steps, and
@@ -76,11 +77,11 @@ __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ 
                                                       int64_t m, int RT, int G, int64_t layer_bytes, int64_t grid_at,
                                                       int64_t unit_at, char* __restrict__ packed)
 {
-    __shared__ float tops[4];
+    __shared__ float tops[kQ4MaxHalves];   // a group has 64 columns at least
     __shared__ float least[16][kQ4Rows];
     const int64_t layer = blockIdx.y;
     const int r = threadIdx.x & 15, g0 = threadIdx.x >> 4;
-    float top = 0.f;
+    for (int g = threadIdx.x; g < G; g += 256) tops[g] = 0.f;
     for (int tile = blockIdx.x; tile < RT; tile += gridDim.x) {
         const int64_t row = (int64_t)tile * kQ4Rows + r;
         const int64_t at = (layer * m + row) * G;
@@ -98,24 +99,23 @@ __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ 
         f32x2* out = reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at) + (int64_t)tile * G * kQ4Rows + r;
         for (int g = g0; g < G; g += 16) {
             f32x2 v = {0.f, 0.f};
+            float top = 0.f;
             if (row < m) {
                 v.x = scale[at + g];
                 v.y = zero[at + g];
                 if (v.x == 0.f) v = f32x2{low, 0.f};
-                else top = fmaxf(top, fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y)));
+                else top = fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y));
             }
             out[g * kQ4Rows] = v;
+            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+            if (r == 0) tops[g] = fmaxf(tops[g], top);   // (group g is this thread's alone)
         }
         __syncthreads();   // the next tile's minima overwrite these
     }
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        if (top > 0.f && top < INFINITY)
-            atomicMax(reinterpret_cast<unsigned*>(packed + layer * layer_bytes + unit_at),
-                      max(min((__float_as_uint(top) >> 23) + 1u, 254u), 1u) << 23);
+    unsigned* units = reinterpret_cast<unsigned*>(packed + layer * layer_bytes + unit_at);
+    for (int g = threadIdx.x; g < G; g += 256) {
+        const float top = tops[g];
+        if (top > 0.f && top < INFINITY) atomicMax(&units[g], max(min((__float_as_uint(top) >> 23) + 1u, 254u), 1u) << 23);
     }
 }
 

@@ -17,10 +17,10 @@
 //          which puts pair 0 where a bfloat16's mantissa wants it.
 //   grids: RT x G x 16 pairs (scale, zero), at the next 256 bytes after the
 //          codes; rows beyond m have scale = zero = 0.
-//   unit:  one float, the power of two at or above the layer's largest
-//          weight |s (c - z)|, at the next 256 bytes after the grids: kernels
-//          that round weights to 16 bits divide by it first, so that no
-//          layer's weights leave float16's normal range as a whole.
+//   units: one float per grid, the power of two at or above the largest weight
+//          |s (c - z)| of its columns, at the next 256 bytes after the grids:
+//          kernels that round weights to 16 bits divide by it first, so that
+//          no columns' weights leave float16's normal range as a whole.
 // Codes of rows beyond m and columns beyond n are 0; their products are kept
 // out by zeros of the activations.
 //
@@ -56,7 +56,7 @@ struct Q4Dims {
     int64_t m, n;
     int RT, KB, G;
     int gb;                       // 64-column halves per grid (>= 2 KB when one grid per row)
-    size_t grid_at, unit_at;      // byte offsets of the grids and the unit
+    size_t grid_at, unit_at;      // byte offsets of the grids and the units
     size_t bytes;                 // bytes of one layer
 };
 
@@ -72,7 +72,7 @@ inline Q4Dims q4_dims(int64_t m, int64_t n, int64_t group_size)
     d.gb = group_size ? (int)(group_size / 64 < (1 << 20) ? group_size / 64 : (1 << 20)) : (1 << 20);
     d.grid_at = align_up((size_t)d.RT * d.KB * 1024);
     d.unit_at = align_up(d.grid_at + (size_t)d.RT * d.G * kQ4Rows * 8);
-    d.bytes = d.unit_at + kAlign;
+    d.bytes = d.unit_at + align_up((size_t)d.G * 4);
     return d;
 }
 
@@ -149,6 +149,7 @@ struct Bf16 {
         return __builtin_bit_cast(vec, v);
     }
     static constexpr uint16_t kOne = 0x3F80;
+    static constexpr float kUnit = 1.f;        // of a packed layer's units, what weights are rounded in
 };
 
 struct Fp16 {
@@ -179,6 +180,7 @@ struct Fp16 {
         return __builtin_bit_cast(vec, v);
     }
     static constexpr uint16_t kOne = 0x3C00;
+    static constexpr float kUnit = 0x1p-15f;   // (2^15 is the largest power of two, 2^-14 the smallest normal)
 };
 
 template <class X>

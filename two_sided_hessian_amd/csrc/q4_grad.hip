@@ -5,12 +5,14 @@
 //
 // The sum runs over the rows of W, and step and zero point change with the
 // row: they cannot be taken out of it as in the forward product.  So a
-// weight is formed in float32, divided by the layer's unit (a power of two,
+// weight is formed in float32, divided by its columns' unit (a power of two,
 // q4.hpp) and rounded once to dy's 16-bit type, the product runs on 16-bit
-// MFMAs with float32 accumulators, and the unit comes back at the store.
-// The rounding is half a unit in the last place of each weight, as a layer
-// kept in that type would have; independent from weight to weight, it adds
-// to a result about what the result's own rounding does.
+// MFMAs with float32 accumulators, and the unit, a factor of the result's
+// column, comes back at the store.  In float16 the largest weight of a group's
+// columns is put at 2^15 at most, so that rows down to 2^-29 of it keep every
+// bit.  The rounding is half a unit in the last place of each weight, as a
+// layer kept in that type would have; independent from weight to weight, it
+// adds to a result about what the result's own rounding does.
 //
 // k_q4_grad: a workgroup of eight waves computes 64 TA tokens x 256 columns;
 // a wave owns 32 TA tokens x 64 columns as TA x 2 MFMA tiles of 32 x 32.  dy
@@ -70,8 +72,7 @@ struct GradRaw {
 };
 
 // blockIdx.y of gridDim.y shares the rows of W; more than one of them writes
-// float32 partial sums, in units, to part[blockIdx.y][token][column] instead
-// of dx.
+// float32 partial sums to part[blockIdx.y][token][column] instead of dx.
 template <class X, int TA>
 __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy, int64_t lddy, int T, Q4Layer w,
                                                  uint16_t* __restrict__ dx, int64_t lddx, int nt, int nj,
@@ -88,8 +89,13 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
     const int t0 = bt * P::BT, j0 = bj * P::BJ;
     const int all = (w.m + 63) / 64;
     const int c0 = all * blockIdx.y / gridDim.y, c1 = all * (blockIdx.y + 1) / gridDim.y;   // this workgroup's chunks
-    const float unit = *w.unit > 0.f ? *w.unit : 1.f;
-    const float down = 1.f / unit;
+    // what the weights of group g's columns are divided by; 1 where all are 0
+    auto unit_of = [&](int g) {
+        const float unit = w.unit[g];
+        return unit > 0.f ? unit * X::kUnit : 1.f;
+    };
+    const int jw = j0 + wj * 64;   // the wave's columns, of one group
+    const float unit = unit_of(min((4 * bj + wj) / w.gb, w.G - 1));
 
     // staging of dy
     const Rsrc x = buffer_of(dy + (int64_t)t0 * lddy, 0x7FFFFFFFu);
@@ -122,6 +128,7 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
     const int a4 = lane & 15, d = lane >> 4, q = wave & 3;
     const int kb = min(2 * bj + (wave >> 2), w.KB - 1);
     const int g = min((2 * kb + (d >> 1)) / w.gb, w.G - 1);
+    const float down = 1.f / unit_of(g);
     const int col = 128 * (wave >> 2) + 64 * (d >> 1) + 16 * q + 8 * (d & 1);
     const char* code_base = reinterpret_cast<const char*>(w.codes + (int64_t)kb * 64 + 16 * q);
     const char* grid_base = reinterpret_cast<const char*>(w.grid);
@@ -224,7 +231,7 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
         if (c + 1 < c1) chunk(c + 1, 1, raw[0], raw[1]);
     }
     wait_direct_loads();
-    const int tw = t0 + 32 * wt * TA, jw = j0 + wj * 64;
+    const int tw = t0 + 32 * wt * TA;
     if (gridDim.y > 1) {
         float* p = part + (int64_t)blockIdx.y * T * w.n;
 #pragma unroll
@@ -234,7 +241,7 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int t = tw + 32 * a + 8 * (r >> 2) + 4 * h + (r & 3), j = jw + 32 * b + ml;
-                    if (t < T && j < w.n) p[(int64_t)t * w.n + j] = acc[a][b][r];
+                    if (t < T && j < w.n) p[(int64_t)t * w.n + j] = unit * acc[a][b][r];
                 }
         return;
     }
@@ -296,7 +303,7 @@ static int grad_run(const void* dy, int64_t lddy, int64_t T, const Q4Layer& w, v
     if (p.TA == 4) grad_launch<X, 4>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
     else if (p.TA == 2) grad_launch<X, 2>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
     else grad_launch<X, 1>(yp, lddy, T, w, xp, lddx, p.splits, part, s);
-    if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.n, w.unit, xp, lddx, s);
+    if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.n, xp, lddx, s);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -402,11 +402,11 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
     tile_store<X, TA>(acc, 1.f, lds + wave * kStoreBytes, tw, T, rw, w.m, y, ldy);
 }
 
-// y = f times the sum of `splits` partial results, in order; blockIdx.x is the
-// token, eight loads are in flight.
+// y = the sum of `splits` partial results, in order; blockIdx.x is the token,
+// eight loads are in flight.
 template <class X>
 __global__ __launch_bounds__(256) void k_q4_join(const float* __restrict__ part, int splits, int T, int m,
-                                                 const float* __restrict__ f, uint16_t* __restrict__ y, int64_t ldy)
+                                                 uint16_t* __restrict__ y, int64_t ldy)
 {
     const int col = blockIdx.y * 256 + threadIdx.x;
     if (col >= m) return;
@@ -421,17 +421,17 @@ __global__ __launch_bounds__(256) void k_q4_join(const float* __restrict__ part,
 #pragma unroll
         for (int u = 0; u < U; ++u) v += u0 + u < splits ? a[u] : 0.f;
     }
-    y[blockIdx.x * ldy + col] = X::down(v * (f && *f > 0.f ? *f : 1.f));
+    y[blockIdx.x * ldy + col] = X::down(v);
 }
 
 template <class X>
-void join_enqueue(const float* part, int splits, int64_t T, int m, const float* f, uint16_t* y, int64_t ldy, hipStream_t s)
+void join_enqueue(const float* part, int splits, int64_t T, int m, uint16_t* y, int64_t ldy, hipStream_t s)
 {
     launch(nullptr, KK_Q4_JOIN, 0.0, 4.0 * splits * T * m, k_q4_join<X>, dim3((unsigned)T, (unsigned)ceil_div(m, 256)),
-           dim3(256), s, part, splits, (int)T, m, f, y, ldy);
+           dim3(256), s, part, splits, (int)T, m, y, ldy);
 }
-template void join_enqueue<Bf16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
-template void join_enqueue<Fp16>(const float*, int, int64_t, int, const float*, uint16_t*, int64_t, hipStream_t);
+template void join_enqueue<Bf16>(const float*, int, int64_t, int, uint16_t*, int64_t, hipStream_t);
+template void join_enqueue<Fp16>(const float*, int, int64_t, int, uint16_t*, int64_t, hipStream_t);
 
 // --------------------------------------------------------------------- host
 
@@ -514,7 +514,7 @@ static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, v
     else if (p.TA == 2) prompt_launch<X, 2, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     else if (own) prompt_launch<X, 1, 2, true>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
     else prompt_launch<X, 1, 2, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
-    if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.m, nullptr, yp, ldy, s);
+    if (p.splits > 1) join_enqueue<X>(part, p.splits, T, w.m, yp, ldy, s);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

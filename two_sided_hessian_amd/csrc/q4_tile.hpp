@@ -100,9 +100,8 @@ inline TileChoice tile_choose(const TileShape (&shapes)[N], int64_t T, int64_t c
 template <class X>
 void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* copy, int64_t ldc, hipStream_t s);
 
-// y (T x m) = f times the sum of `splits` float32 results part[split][t][m], in
-// order; f: a device scalar, or null for 1.
+// y (T x m) = the sum of `splits` float32 results part[split][t][m], in order.
 template <class X>
-void join_enqueue(const float* part, int splits, int64_t T, int m, const float* f, uint16_t* y, int64_t ldy, hipStream_t s);
+void join_enqueue(const float* part, int splits, int64_t T, int m, uint16_t* y, int64_t ldy, hipStream_t s);
 
 }  // namespace bk
