@@ -20,7 +20,10 @@
  *     2-byte alignment is asked for (16-byte aligned rows, i.e. a 16-byte
  *     aligned pointer and ld a multiple of 8, are read fastest).
  *   - Sums are float32; results are rounded once to the activations' type
- *     (beyond its largest value to infinity).
+ *     (beyond its largest value to infinity).  Each sum runs over (16 + c) x,
+ *     with (16 + z) sum x taken off after every 1024 columns at most: a result's
+ *     error is that of roundings of 2^-24 of such a partial sum, about 23 steps
+ *     times |sum x| over those columns, however long the row is.
  *   - A non-finite value in a token's row makes that token's results
  *     non-finite (which of inf and NaN is not specified) and touches no
  *     other token.

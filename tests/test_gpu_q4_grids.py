@@ -8,7 +8,7 @@ import torch
 
 import two_sided_hessian_amd as B
 from q4_forms import few_form, grad_form, prompt_form
-from test_gpu_q4 import LINEAR, U, close, make_layer, pack, tokens, weights64
+from test_gpu_q4 import DEV, LINEAR, U, close, make_layer, pack, tokens, weights64
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,44 @@ def test_gradient_under_rows_that_a_token_leaves_out():
             dy = tokens(T, m, dtype, 2).clone()
             dy[:, [5, 300]] = 0
             close(B.q4_linear_grad(dy, w), dy.double().cpu().numpy() @ ref, dtype, 4 * U[dtype])
+
+
+# x of a mean of two deviations.  Sums of (16 + c) x, about 23 times the mean of
+# x per column, grow with the columns, the result with their root.  They are
+# not kept beyond two pieces of 512 columns or two groups: a random walk of n /
+# 16 roundings of at most 0.42 * 2^-24 of a ramp up to 1024 * 23.5 * 2 steps,
+# against a result of 4.6 sqrt(5 n) steps, is 1.9e-5 of it in the rms; six times
+# that stays below 2^-13.
+@pytest.mark.parametrize("T,m,n,form", [
+    (4, 600, 16384, (1, 1)), (64, 600, 16384, (16, 1)), (200, 1000, 65536, (64, 128, 8)), (1030, 2050, 32768, (128, 128, 5)),
+    (600, 4096, 32768, (128, 256, 3)), (2048, 2048, 65536, (256, 256, 4)), (2048, 8192, 16384, (256, 256, 1))])
+@pytest.mark.parametrize("group", [0, 128])
+def test_activations_with_a_mean(T, m, n, group, form):
+    assert (few_form(T, m) if T <= 64 else prompt_form(T, m, n)) == form
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(n + group)
+    G = -(-n // group) if group else 1
+    codes = torch.randint(0, 16, (m, n), generator=gen, device=DEV, dtype=torch.uint8)
+    scale = 0.01 * torch.exp(0.3 * torch.randn((m, G), generator=gen, device=DEV))
+    zero = 7.5 + 0.3 * torch.randn((m, G), generator=gen, device=DEV)
+    dtype = torch.float16
+    x = (0.02 * (torch.randn((T, n), generator=gen, device=DEV) + 2)).to(dtype)
+    y = B.q4_linear(x, B.q4_pack(codes, scale, zero, group_size=group) if group else B.q4_pack(codes, scale, zero))
+    some = torch.linspace(0, T - 1, min(T, 12)).long()
+    col, xs, ref = torch.arange(n, device=DEV) // (group or n), x[some].double(), []
+    for r in range(0, m, 512):
+        rows = scale[r:r + 512].double()[:, col] * (codes[r:r + 512].double() - zero[r:r + 512].double()[:, col])
+        ref.append(xs @ rows.t().contiguous())
+    close(y[some], torch.cat(ref, 1).cpu().numpy(), dtype, LINEAR)
+
+
+@pytest.mark.parametrize("T,m,n,form", [(130, 300, 3000, (64, 128, 8)), (1105, 555, 1301, (64, 128, 1)), (2730, 143, 5000, (128, 128, 5)),
+                                        (2700, 1200, 900, (128, 128, 1)), (4200, 1100, 4000, (256, 256, 3))])
+@pytest.mark.parametrize("group", [0, 64, 192, 576, 1088])
+def test_groups_and_splits_that_end_in_any_column(T, m, n, group, form):
+    assert prompt_form(T, m, n) == form
+    layer = make_layer(m, n, group, 95)
+    w, ref = pack(*layer, group), weights64(*layer, group)
+    dtype = torch.float16 if group else torch.bfloat16
+    x = tokens(T, n, dtype, 1) + 2
+    close(B.q4_linear(x, w), x.double().cpu().numpy() @ ref.T, dtype, LINEAR)

@@ -283,7 +283,7 @@ size_t bakron_q4_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, in
     if (!q4_shape_ok(m, n) || !q4_group_ok(group_size) || tokens <= bk::kQ4Few || tokens > BAKRON_Q4_MAX_TOKENS ||
         m == 0 || n == 0)
         return 0;
-    return bk::q4_prompt_workspace_bytes(tokens, m, n, bk::q4_dims(m, n, group_size).G);
+    return bk::q4_prompt_workspace_bytes(tokens, m, n, bk::q4_dims(m, n, group_size).gb);
 }
 
 int bakron_q4_linear(const void* x, int64_t ldx, int64_t tokens, int32_t type, const void* packed, int64_t m, int64_t n,

@@ -29,8 +29,11 @@
 // 3 .. 6; in float16, 0x4C00 and bits 6 .. 9.  The products of u with
 // activations are exact in the MFMA's float32, and
 //     sum_j s (c_j - z) x_j = s ( sum_j u_j x_j - (16 + z) sum_j x_j )
-// over a group applies step and zero point once, in float32.  The offset of
-// 16 costs about 16 / 5 of the sum's float32 rounding, 2 bits of 24.
+// over a group (or a piece of one) applies step and zero point once, in
+// float32.  The offset of 16 costs about 16 / 5 of the sum's float32 rounding,
+// 2 bits of 24, where x has no mean.  With one, sum_j u_j x_j grows with the
+// columns and the result with their root: kernels take zero points off after
+// 128 columns (few tokens) or at most 1024 (many), not at the row's end.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -210,7 +213,7 @@ __device__ __forceinline__ void load_lds4(Rsrc r, uint32_t lane_at, uint32_t at,
 
 // Many tokens (q4_prompt.hip)
 constexpr int64_t kQ4Few = 64;   // up to so many tokens the few-token kernel runs
-size_t q4_prompt_workspace_bytes(int64_t T, int64_t m, int64_t n, int64_t G);
+size_t q4_prompt_workspace_bytes(int64_t T, int64_t m, int64_t n, int gb);
 int q4_prompt_enqueue(const void* x, int64_t ldx, int64_t T, bool bf16, const Q4Layer& w, void* y, int64_t ldy, void* ws,
                       hipStream_t s);
 

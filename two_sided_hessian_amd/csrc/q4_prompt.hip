@@ -5,15 +5,19 @@
 // The first sum runs on 16-bit MFMAs with exact operands.  Its accumulators
 // are kept in units of the current group's step: on entering group g they are
 // multiplied by s_{g-1} / s_g, one float32 multiplication each, so a group
-// needs no second set of accumulators.  The zero points enter in one of two
-// ways:
-//   * large tiles: the second sum is a product over the groups alone (n / 128
-//     terms).  X and s (16 + z) are split into three bfloat16 terms each and the
-//     six leading products of every group are six K slots of the same MFMAs,
-//     run once at the end (error 2^-24 of a term).  k_q4_sums makes X in a pass
-//     over x of its own.
+// needs no second set of accumulators.  The zero points come off piece by
+// piece, a piece being a group or 512 columns of a longer one: sums of (16 + c) x
+// grow with the mean of x where the result does not, and every float32
+// rounding, those of the steps' ratios among them, is one of the sum not yet
+// taken off (x of a mean of two deviations, 2048 x 8192 x 16384 in groups of
+// 128: an error of 5e-6 of the rms result, and 4e-4 with all zero points at
+// the end; one grid per row: 4e-6 and 5e-5).  They enter in one of two ways:
+//   * large tiles: X and 16 + z are split into three bfloat16 terms each and the
+//     six leading products of a piece are six K slots of the same MFMAs (error
+//     2^-24 of a term), two pieces at a time.  k_q4_sums makes X in a pass over
+//     x of its own.
 //   * small tiles, which do not fill the matrix cores: X comes from a product
-//     with ones beside the others, and is taken off when its group ends.
+//     with ones beside the others.
 // Where x's rows are not 16-byte aligned or n is not a multiple of 64, the pass
 // over x also makes a padded copy that the product can stage directly.
 //
@@ -47,13 +51,22 @@ namespace bk {
 // ---------------------------------------------------------------- group sums
 //
 // One wave per token: lanes sum 8 columns, 8 lanes a 64-column half (the loads
-// of four spans of 512 columns together), and the halves of a group are added
+// of four spans of 512 columns together), and the halves of a piece are added
 // in order.  COPY: the row goes to `copy` too, columns n .. 64 ceil(n / 64) - 1
 // zero.  HBM bounds it: 37 us for 8192 x 8192 (3.6 TB/s), 5 for 2048 x 4096.
 constexpr int kSumsHalves = BAKRON_MAX_DIM / 64;
 
+// Pieces of the columns, in halves of 64: a group's first, second, ... kPiece,
+// the last of them cut where the group ends.
+constexpr int kPiece = 8;
+__host__ __device__ __forceinline__ int pieces_of(int gb) { return (gb + kPiece - 1) / kPiece; }
+__host__ __device__ __forceinline__ int piece_at(int half, int gb)   // the piece of a half
+{
+    return half / gb * pieces_of(gb) + half % gb / kPiece;
+}
+
 template <class X, bool COPY>
-__global__ __launch_bounds__(256) void k_q4_sums(const uint16_t* __restrict__ x, int64_t ldx, int T, int n, int gb, int G,
+__global__ __launch_bounds__(256) void k_q4_sums(const uint16_t* __restrict__ x, int64_t ldx, int T, int n, int gb, int P,
                                                  float* __restrict__ sums, int64_t lds_, uint16_t* __restrict__ copy,
                                                  int64_t ldc)
 {
@@ -87,11 +100,13 @@ __global__ __launch_bounds__(256) void k_q4_sums(const uint16_t* __restrict__ x,
         }
     }
     __builtin_amdgcn_wave_barrier();   // (a wave's own LDS row)
-    for (int g = lane; g < G; g += 64) {
-        const int h0 = g * gb, h1 = g == G - 1 ? halves : h0 + gb;   // gb may exceed the halves when G is 1
+    const int per = pieces_of(gb);
+    for (int p = lane; p < P; p += 64) {
+        const int g = p / per, h0 = g * gb + (p - g * per) * kPiece;
+        const int h1 = min(min(h0 + kPiece, (g + 1) * gb), halves);
         float s = 0.f;
         for (int h = h0; h < h1; ++h) s += half[wave][h];
-        sums[(int64_t)g * lds_ + t] = s;
+        sums[(int64_t)p * lds_ + t] = s;
     }
 }
 
@@ -186,63 +201,28 @@ __device__ __forceinline__ void split3(float v, uint32_t& a, uint32_t& b, uint32
     c = Bf16::down(r - Bf16::up((uint16_t)b));
 }
 
-// acc -= s (16 + z) X for the wave's tiles.  32 groups at a time, X of the
-// workgroup's tokens and the grids of its rows come to LDS together (one round
-// trip); lane half h takes group 2 j + h, slots X1 Z1, X1 Z2, X2 Z1, X1 Z3,
-// X2 Z2, X3 Z1.
-template <class X, int TA, int WR>
-__device__ __forceinline__ void zero_points(f32x16 (&acc)[TA][2], const Q4Layer& w, int rt0,
-                                            const float* __restrict__ sums, int64_t lds_, int t0, char* lds)
+// acc += z X for the wave's tiles and two pieces: lane half h of the MFMAs takes
+// one of them, its lanes X of their tokens and z of their rows, slots X1 Z1,
+// X1 Z2, X2 Z1, X1 Z3, X2 Z2, X3 Z1.
+template <int TA>
+__device__ __forceinline__ void zero_points(f32x16 (&acc)[TA][2], const float (&xs)[TA], const float (&z)[2])
 {
-    typedef Prompt<TA, WR> P;
-    constexpr int NG = 32, SUMS = NG * P::BT * 4, TILES = P::BR / 16;
-    static_assert(SUMS + TILES * NG * 128 <= P::LDS, "32 groups fit the staging buffers");
-    const int lane = threadIdx.x & 63, h = lane >> 5, ml = lane & 31;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wt = wave / WR, wr = wave % WR;
-    const Rsrc gb = buffer_of(w.grid + (int64_t)rt0 * w.G * 16, 0x7FFFFFFFu);
-    const int rts = w.RT - 1 - rt0;
-    for (int g0 = 0; g0 < w.G; g0 += NG) {
-        __syncthreads();
-        // sums: 256 bytes (64 tokens) an instruction; grids: 1 KB, 8 groups of a
-        // row tile; groups beyond G repeat the last
-        for (int i = wave; i < NG * TA; i += 2 * WR)
-            load_lds4(buffer_of(sums + min(g0 + i / TA, w.G - 1) * lds_ + t0, 0x7FFFFFFFu), 4 * lane, 256 * (i % TA),
-                      lds + 256 * i);
-        for (int i = wave; i < TILES * NG / 8; i += 2 * WR) {
-            const int tile = i / (NG / 8), g = g0 + 8 * (i % (NG / 8)) + (lane >> 3);
-            load_lds16(gb, (uint32_t)(min(tile, rts) * w.G + min(g, w.G - 1)) * 128 + 16 * (lane & 7), 0,
-                       lds + SUMS + 1024 * i);
-        }
-        wait_direct_loads();
-        __syncthreads();
-#pragma unroll 1
-        for (int j0 = 0; j0 < NG && g0 + j0 < w.G; j0 += 8)
+    bf16x8 zf[2];
 #pragma unroll
-        for (int j = j0; j < j0 + 8; j += 2) {   // (unrolled: four pairs' reads in flight)
-            const int g = j + h;
-            const float in = g0 + g < w.G ? 1.f : 0.f;   // groups beyond G add nothing
-            bf16x8 zf[2];
+    for (int b = 0; b < 2; ++b) {
+        uint32_t z1, z2, z3;
+        split3(z[b], z1, z2, z3);
+        const u32x4 v = {z1 | (z2 << 16), z1 | (z3 << 16), z2 | (z1 << 16), 0u};
+        zf[b] = __builtin_bit_cast(bf16x8, v);
+    }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const f32x2 sz = *reinterpret_cast<const f32x2*>(lds + SUMS + (4 * wr + 2 * b + (ml >> 4)) * NG * 128 +
-                                                                 128 * g + 8 * (ml & 15));
-                uint32_t z1, z2, z3;
-                split3(in * (-sz.x * (sz.y + kQ4Offset)), z1, z2, z3);
-                const u32x4 v = {z1 | (z2 << 16), z1 | (z3 << 16), z2 | (z1 << 16), 0u};
-                zf[b] = __builtin_bit_cast(bf16x8, v);
-            }
+    for (int a = 0; a < TA; ++a) {
+        uint32_t x1, x2, x3;
+        split3(xs[a], x1, x2, x3);
+        const u32x4 v = {x1 | (x1 << 16), x2 | (x1 << 16), x2 | (x3 << 16), 0u};
+        const bf16x8 xf = __builtin_bit_cast(bf16x8, v);
 #pragma unroll
-            for (int a = 0; a < TA; ++a) {
-                const float xs = *reinterpret_cast<const float*>(lds + 256 * TA * g + 4 * (32 * (wt * TA + a) + ml));
-                uint32_t x1, x2, x3;
-                split3(xs, x1, x2, x3);
-                const u32x4 v = {x1 | (x1 << 16), x2 | (x1 << 16), x2 | (x3 << 16), 0u};
-                const bf16x8 xf = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) acc[a][b] = Bf16::mfma32(xf, zf[b], acc[a][b]);
-            }
-        }
+        for (int b = 0; b < 2; ++b) acc[a][b] = Bf16::mfma32(xf, zf[b], acc[a][b]);
     }
 }
 
@@ -279,7 +259,7 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
-    f32x16 sx[OWN ? TA : 1];   // sums of x over the group so far, in every column of the tile
+    f32x16 sx[OWN ? TA : 1];   // sums of x over the piece so far, in every column of the tile
     const vec ones = q4_ones<X>();
     if (OWN) {
 #pragma unroll
@@ -290,8 +270,22 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
 
     u32x4 codes[2][2];   // [row tile pair][unit h, h + 2]
     f32x2 sz[2] = {f32x2{1.f, 0.f}, f32x2{1.f, 0.f}};   // of the group whose steps the accumulators count in
-    int left = 0;        // chunks left of that group
-    int start = 2 * kb0 % w.gb;
+    int in_group = 2 * kb0 % w.gb;   // chunks of that group up to the end of the present piece
+    int left = 0;                    // and chunks left of the piece
+    // Two pieces' zero points come off together: `open` says that the first of
+    // them has ended, z_open is its -(16 + z) in units of the present step, xs
+    // the X of both (lane half h's of piece `pair` + h), loaded when the first
+    // begins.  A piece belongs to the split that it ends in.
+    bool open = false;
+    float z_open[2] = {0.f, 0.f}, xs[TA];
+    int pair = piece_at(2 * kb0, w.gb);
+    const int pieces = piece_at((w.n - 1) / 64, w.gb) + 1;
+    const float* x_sums = sums + t0 + 32 * wt * TA + ml;
+    auto load_sums = [&]() {
+#pragma unroll
+        for (int a = 0; a < TA; ++a) xs[a] = x_sums[min(pair + h, pieces - 1) * lds_ + 32 * a];
+    };
+    if (!OWN) load_sums();
     int bx = 0, bw = 0;                                  // buffers of chunk c and block kb
     int px = P::AHEAD, pw = (P::AHEAD / 2 + 1) % P::NW;   // and of the ones staged beside them
     // the lane's parts of the LDS addresses
@@ -324,28 +318,54 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
                 for (int v = 0; v < PRE; ++v)
 #pragma unroll
                     for (int a = 0; a < TA; ++a) xf[v][a] = *reinterpret_cast<const vec*>(s + x_lane[v] + 4096 * a);
-                if (left-- == 0) {
-                    left = w.gb - 1 - start;
-                    start = 0;
-                    const char* g = lds + g_lane + bx * P::GBUF;
+                if (left == 0) {
+                    const bool first = c == 2 * kb0;
+                    if (!first) {
+                        // the end of a piece: its zero points
+                        float z[2];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const f32x2 s1 = *reinterpret_cast<const f32x2*>(g + 256 * b);
-                        const float ratio = sz[b].x * __builtin_amdgcn_rcpf(s1.x), off = -(sz[b].y + kQ4Offset);
-                        sz[b] = s1;
+                        for (int b = 0; b < 2; ++b) z[b] = -(sz[b].y + kQ4Offset);
+                        if (OWN) {
 #pragma unroll
-                        for (int a = 0; a < TA; ++a)
+                            for (int a = 0; a < TA; ++a)
 #pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                acc[a][b][r] = (OWN ? fmaf(off, sx[a][r], acc[a][b][r]) : acc[a][b][r]) * ratio;
+                                for (int r = 0; r < 16; ++r) {
+#pragma unroll
+                                    for (int b = 0; b < 2; ++b) acc[a][b][r] = fmaf(z[b], sx[a][r], acc[a][b][r]);
+                                    sx[a][r] = 0.f;
+                                }
+                        } else if (open) {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) z[b] = h ? z[b] : z_open[b];
+                            zero_points<TA>(acc, xs, z);
+                            open = false;
+                            pair += 2;
+                            load_sums();
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) z_open[b] = z[b];
+                            open = true;
+                        }
                     }
-                    if (OWN) {
+                    if (first || in_group == w.gb) {
+                        if (!first) in_group = 0;
+                        const char* g = lds + g_lane + bx * P::GBUF;
 #pragma unroll
-                        for (int a = 0; a < TA; ++a)
+                        for (int b = 0; b < 2; ++b) {
+                            const f32x2 s1 = *reinterpret_cast<const f32x2*>(g + 256 * b);
+                            const float ratio = sz[b].x * __builtin_amdgcn_rcpf(s1.x);
+                            sz[b] = s1;
+                            z_open[b] *= ratio;
 #pragma unroll
-                            for (int r = 0; r < 16; ++r) sx[a][r] = 0.f;
+                            for (int a = 0; a < TA; ++a)
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) acc[a][b][r] *= ratio;
+                        }
                     }
+                    left = min(kPiece - in_group % kPiece, w.gb - in_group);
+                    in_group += left;
                 }
+                --left;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     if (v + PRE < 4) {
@@ -375,6 +395,16 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
         }
         bw = bw + 1 == P::NW ? 0 : bw + 1;
     }
+    const bool ended = left == 0 || kb1 == w.KB;   // the last piece
+    if (!OWN && (open || ended)) {
+        float z[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float last = ended ? -(sz[b].y + kQ4Offset) : 0.f;
+            z[b] = open ? (h ? last : z_open[b]) : (h ? 0.f : last);
+        }
+        zero_points<TA>(acc, xs, z);
+    }
 #pragma unroll
     for (int a = 0; a < TA; ++a)
 #pragma unroll
@@ -383,7 +413,6 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
             for (int r = 0; r < 16; ++r)
                 acc[a][b][r] = (OWN ? fmaf(-(sz[b].y + kQ4Offset), sx[a][r], acc[a][b][r]) : acc[a][b][r]) * sz[b].x;
     wait_direct_loads();
-    if (!OWN && blockIdx.y == 0) zero_points<X, TA, WR>(acc, w, rt0, sums, lds_, t0, lds);
     const int tw = t0 + 32 * wt * TA, rw = br * P::BR + wr * 64;
     if (gridDim.y > 1) {
         float* p = part + (int64_t)blockIdx.y * T * w.m;
@@ -438,11 +467,12 @@ template void join_enqueue<Fp16>(const float*, int, int64_t, int, uint16_t*, int
 // How a problem is cut: TA, WR and the workgroups that share a tile's columns.
 struct PromptPlan {
     int TA, WR, splits;
+    int pieces;
     int64_t lds_, ldc;
     size_t sums, copy, part, bytes;
 };
 
-static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
+static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int gb)
 {
     PromptPlan p;
     // Costs: 4096 tokens x 4096 rows in tiles of 256 x 256 take 128 us, 2048 in
@@ -460,13 +490,14 @@ static PromptPlan prompt_plan(int64_t T, int64_t m, int64_t n, int64_t G)
     p.lds_ = ceil_div(T, 256) * 256;
     p.ldc = ceil_div(n, 64) * 64;
     p.sums = 0;
-    p.copy = align_up((size_t)p.lds_ * G * 4);
+    p.pieces = piece_at((int)((n - 1) / 64), gb) + 1;
+    p.copy = align_up((size_t)p.lds_ * p.pieces * 4);
     p.part = p.copy + align_up((size_t)T * p.ldc * 2);
     p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * T * m * 4) : 0);
     return p;
 }
 
-size_t q4_prompt_workspace_bytes(int64_t T, int64_t m, int64_t n, int64_t G) { return prompt_plan(T, m, n, G).bytes; }
+size_t q4_prompt_workspace_bytes(int64_t T, int64_t m, int64_t n, int gb) { return prompt_plan(T, m, n, gb).bytes; }
 
 template <class X>
 void copy_enqueue(const uint16_t* x, int64_t ldx, int64_t T, int n, uint16_t* copy, int64_t ldc, hipStream_t s)
@@ -491,7 +522,7 @@ template <class X>
 static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, void* y, int64_t ldy, void* ws,
                       hipStream_t s)
 {
-    const PromptPlan p = prompt_plan(T, w.m, w.n, w.G);
+    const PromptPlan p = prompt_plan(T, w.m, w.n, w.gb);
     const uint16_t* xp = static_cast<const uint16_t*>(x);
     uint16_t* yp = static_cast<uint16_t*>(y);
     float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + p.sums);
@@ -506,7 +537,7 @@ static int prompt_run(const void* x, int64_t ldx, int64_t T, const Q4Layer& w, v
     const bool own = p.TA == 1 && (direct || p.splits > 1);
     if (!own)
         launch(nullptr, KK_Q4_SUMS, 0.0, 2.0 * T * w.n, direct ? k_q4_sums<X, false> : k_q4_sums<X, true>,
-               dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, w.G, sums, p.lds_, copy, p.ldc);
+               dim3((unsigned)ceil_div(T, 4)), dim3(256), s, xp, ldx, (int)T, w.n, w.gb, p.pieces, sums, p.lds_, copy, p.ldc);
     else if (!direct) copy_enqueue<X>(xp, ldx, T, w.n, copy, p.ldc, s);
     if (!direct) xp = copy, ldx = p.ldc;
     if (p.TA == 4) prompt_launch<X, 4, 4, false>(xp, ldx, T, w, sums, p.lds_, yp, ldy, p.splits, part, s);
