@@ -8,6 +8,7 @@ attribute reads (no tensor is looked into: no copy, no synchronisation).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -68,8 +69,8 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
     in front): codes uint8 in [0, 15], scale and zero float32, as solve() and
     gptq() take and return them.  ``check``: raise GridError if a code is
     above 15, a scale neither 0 nor of magnitude 2^-100 .. 2^100 or a zero
-    point not finite (reads them back to the host, which waits for the work
-    that makes them)."""
+    point not finite (reads them back to the host on ``stream``, which waits
+    for the work there that makes them)."""
     g = _group(group_size)
     if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
         raise ValueError("codes must be an m x n or count x m x n tensor")
@@ -82,17 +83,18 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
     _b._check_dev("scale", scale, torch.float32, gshape)
     _b._check_dev("zero", zero, torch.float32, gshape)
     if check and codes.numel():
-        size = scale.abs()
-        steps = (((size >= 2.0**-100) & (size <= 2.0**100)) | (size == 0)).all()   # False for NaN
-        high, finite = torch.stack((codes.max() > 15, steps & torch.isfinite(zero).all())).tolist()
+        with _on(stream):
+            size = scale.abs()
+            steps = (((size >= 2.0**-100) & (size <= 2.0**100)) | (size == 0)).all()   # False for NaN
+            high, finite = torch.stack((codes.max() > 15, steps & torch.isfinite(zero).all())).tolist()
         if high:
             raise _b.GridError("codes must lie in [0, 15]")
         if not finite:
             raise _b.GridError("scale must be 0 or of magnitude 2^-100 .. 2^100, zero finite")
     L = _b.lib()
-    data = _b.workspace(L.bakron_q4_packed_bytes(count, m, n, g), codes.device)
-    if stream is not None:
-        _keep(stream, data)
+    with _on(stream):
+        data = _b.workspace(L.bakron_q4_packed_bytes(count, m, n, g), codes.device)
+    _hand_over(stream, data)
     rc = L.bakron_q4_pack(codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), count, m, n, g, data.data_ptr(),
                           _b._stream(stream))
     if rc != _b.BAKRON_SUCCESS:
@@ -140,13 +142,14 @@ def _one(name, w, index, count=1):
         raise ValueError(f"{name} is on {w.device}, not on cuda:{index}")
 
 
-def _ws(ws, size, device, index):
+def _ws(ws, size, device, index, stream):
     """The workspace as (tensor, pointer, bytes); size() bytes if none is given."""
     if ws is None:
         need = size()
         if not need:
             return None, None, 0
-        ws = _b.workspace(need, device)
+        with _on(stream):
+            ws = _b.workspace(need, device)
     elif ws.get_device() != index:
         raise ValueError(f"ws is on {ws.device}, not on {device}")
     return ws, ws.data_ptr(), ws.nbytes
@@ -157,13 +160,25 @@ def _ws(ws, size, device, index):
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _keep(stream, *tensors):
-    """Tensors made here, on the current stream, and used on the caller's
-    other one: torch's allocator has to wait for it before it hands them out
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where results and workspaces of a call on ``stream`` are made: in that
+    stream's memory pool.  A block of the current stream's could still be in
+    use there, by work that is only ordered before the current stream's own
+    next use of it."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *results):
+    """Results made on ``stream`` that the caller will use on the current one:
+    torch's allocator has to wait for that too before it hands them out
     again."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+    if stream is not None:
+        here = torch.cuda.current_stream(stream.device)
+        for t in results:
+            t.record_stream(here)
 
 
 _calls = {}
@@ -183,20 +198,17 @@ def _linear(call, size, name, x, w, out, ws, stream):
     ldx = _rows(name, x, in_cols)
     index, T = x.get_device(), x.shape[0]
     _one("w", w, index)
-    given = ws
     if out is None:
-        out = x.new_empty((T, out_cols))
+        with _on(stream):
+            out = x.new_empty((T, out_cols))
+        _hand_over(stream, out)
         ldo = out_cols
     else:
         ldo = _rows("out", out, out_cols, x.dtype)
         if out.shape[0] != T or out.get_device() != index:
             raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {x.device}")
-    ws, wp, wn = _ws(ws, lambda: size(T, w), w.device, index)
-    if stream is None:
-        s = _raw_stream(index)
-    else:
-        s = stream.cuda_stream
-        _keep(stream, out, None if given is not None else ws)
+    ws, wp, wn = _ws(ws, lambda: size(T, w), w.device, index, stream)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
     rc = _call(call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w._ptr, w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn, s)
     if rc != _b.BAKRON_SUCCESS:
         raise _b.BakronError(rc, call)
@@ -237,10 +249,11 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
         if w._group != w_gate._group:
             raise ValueError("the three stacks must have one group_size")
     _b._check_dev("router", router, dtype, (E, h))
-    given = ws
     if out is None:
-        out = {"y": x.new_empty((T, h)), "ids": x.new_empty((T, top_k), dtype=torch.int32),
-               "weights": x.new_empty((T, top_k), dtype=torch.float32)}
+        with _on(stream):
+            out = {"y": x.new_empty((T, h)), "ids": x.new_empty((T, top_k), dtype=torch.int32),
+                   "weights": x.new_empty((T, top_k), dtype=torch.float32)}
+        _hand_over(stream, *out.values())
         ldy = h
     else:
         ldy = _rows("out['y']", out["y"], h, dtype)
@@ -248,12 +261,8 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
             raise ValueError(f"out['y'] must have shape ({T}, {h}), got {tuple(out['y'].shape)}")
         _b._check_dev("out['ids']", out["ids"], torch.int32, (T, top_k))
         _b._check_dev("out['weights']", out["weights"], torch.float32, (T, top_k))
-    ws, wp, wn = _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), w_gate.device, index)
-    if stream is None:
-        s = _raw_stream(index)
-    else:
-        s = stream.cuda_stream
-        _keep(stream, *out.values(), None if given is not None else ws)
+    ws, wp, wn = _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), w_gate.device, index, stream)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
     rc = _call("bakron_q4_moe")(x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate._ptr, w_up._ptr, w_down._ptr,
                                 h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy, out["ids"].data_ptr(),
                                 out["weights"].data_ptr(), wp, wn, s)
