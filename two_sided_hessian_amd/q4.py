@@ -44,12 +44,15 @@ class Q4Weight:
     packed layout, with group_size columns per grid (None: one grid per row).
     ``data`` is the device buffer (uint8) that holds it."""
 
-    __slots__ = ("data", "count", "m", "n", "group_size", "device", "_ptr", "_group", "_index")
+    __slots__ = ("data", "count", "m", "n", "group_size", "_group")
 
     def __init__(self, data, count, m, n, group_size):
         self.data, self.count, self.m, self.n, self.group_size = data, count, m, n, group_size
-        self.device = data.device
-        self._ptr, self._group, self._index = data.data_ptr(), group_size or 0, data.get_device()
+        self._group = group_size or 0
+
+    @property
+    def device(self):
+        return self.data.device
 
     def __repr__(self):
         return f"Q4Weight(count={self.count}, m={self.m}, n={self.n}, group_size={self.group_size})"
@@ -138,7 +141,7 @@ def _one(name, w, index, count=1):
         raise TypeError(f"{name} must be a Q4Weight (q4_pack)")
     if w.count != count:
         raise ValueError(f"{name} must hold {count} layer(s), got {w.count}")
-    if w._index != index:
+    if w.data.get_device() != index:
         raise ValueError(f"{name} is on {w.device}, not on cuda:{index}")
 
 
@@ -209,7 +212,8 @@ def _linear(call, size, name, x, w, out, ws, stream):
             raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {x.device}")
     ws, wp, wn = _ws(ws, lambda: size(T, w), w.device, index, stream)
     s = _raw_stream(index) if stream is None else stream.cuda_stream
-    rc = _call(call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w._ptr, w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn, s)
+    rc = _call(call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w.data.data_ptr(), w.m, w.n, w._group, out.data_ptr(), ldo,
+                     wp, wn, s)
     if rc != _b.BAKRON_SUCCESS:
         raise _b.BakronError(rc, call)
     return out
@@ -263,9 +267,9 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
         _b._check_dev("out['weights']", out["weights"], torch.float32, (T, top_k))
     ws, wp, wn = _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), w_gate.device, index, stream)
     s = _raw_stream(index) if stream is None else stream.cuda_stream
-    rc = _call("bakron_q4_moe")(x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate._ptr, w_up._ptr, w_down._ptr,
-                                h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy, out["ids"].data_ptr(),
-                                out["weights"].data_ptr(), wp, wn, s)
+    rc = _call("bakron_q4_moe")(x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate.data.data_ptr(),
+                                w_up.data.data_ptr(), w_down.data.data_ptr(), h, f, E, top_k, w_gate._group,
+                                out["y"].data_ptr(), ldy, out["ids"].data_ptr(), out["weights"].data_ptr(), wp, wn, s)
     if rc != _b.BAKRON_SUCCESS:
         raise _b.BakronError(rc, "bakron_q4_moe")
     return out
