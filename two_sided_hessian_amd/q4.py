@@ -85,6 +85,8 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
         gshape = lead + (m, 1)
     _b._check_dev("scale", scale, torch.float32, gshape)
     _b._check_dev("zero", zero, torch.float32, gshape)
+    index = codes.get_device()
+    _one_device(index, stream, scale=scale, zero=zero)
     if check and codes.numel():
         with _on(stream):
             size = scale.abs()
@@ -94,14 +96,11 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
             raise _b.GridError("codes must lie in [0, 15]")
         if not finite:
             raise _b.GridError("scale must be 0 or of magnitude 2^-100 .. 2^100, zero finite")
-    L = _b.lib()
     with _on(stream):
-        data = _b.workspace(L.bakron_q4_packed_bytes(count, m, n, g), codes.device)
+        data = _b.workspace(_b.lib().bakron_q4_packed_bytes(count, m, n, g), codes.device)
     _hand_over(stream, data)
-    rc = L.bakron_q4_pack(codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), count, m, n, g, data.data_ptr(),
-                          _b._stream(stream))
-    if rc != _b.BAKRON_SUCCESS:
-        raise _b.BakronError(rc, "bakron_q4_pack")
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    _run("bakron_q4_pack", index, codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), count, m, n, g, data.data_ptr(), s)
     return Q4Weight(data, count, m, n, group_size)
 
 
@@ -166,6 +165,31 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _HERE = contextlib.nullcontext()
 
 
+def _one_device(index, stream, **tensors):
+    """Every tensor and the stream have to be on the device of the first one."""
+    for name, t in tensors.items():
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, not on cuda:{index}")
+
+
+_device = torch._C._cuda_getDevice
+
+
+def _run(call, index, *args):
+    """The library's call with the tensors' device current: kernels go to the
+    current device, and the default stream's handle names no device."""
+    f = _call(call)
+    if _device() == index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args)
+    if rc != _b.BAKRON_SUCCESS:
+        raise _b.BakronError(rc, call)
+
+
 def _on(stream):
     """Where results and workspaces of a call on ``stream`` are made: in that
     stream's memory pool.  A block of the current stream's could still be in
@@ -201,6 +225,8 @@ def _linear(call, size, name, x, w, out, ws, stream):
     ldx = _rows(name, x, in_cols)
     index, T = x.get_device(), x.shape[0]
     _one("w", w, index)
+    if stream is not None:
+        _one_device(index, stream)
     if out is None:
         with _on(stream):
             out = x.new_empty((T, out_cols))
@@ -212,10 +238,8 @@ def _linear(call, size, name, x, w, out, ws, stream):
             raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {x.device}")
     ws, wp, wn = _ws(ws, lambda: size(T, w), w.device, index, stream)
     s = _raw_stream(index) if stream is None else stream.cuda_stream
-    rc = _call(call)(x.data_ptr(), ldx, T, _TYPES[x.dtype], w.data.data_ptr(), w.m, w.n, w._group, out.data_ptr(), ldo,
-                     wp, wn, s)
-    if rc != _b.BAKRON_SUCCESS:
-        raise _b.BakronError(rc, call)
+    _run(call, index, x.data_ptr(), ldx, T, _TYPES[x.dtype], w.data.data_ptr(), w.m, w.n, w._group, out.data_ptr(), ldo,
+         wp, wn, s)
     return out
 
 
@@ -253,6 +277,7 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
         if w._group != w_gate._group:
             raise ValueError("the three stacks must have one group_size")
     _b._check_dev("router", router, dtype, (E, h))
+    _one_device(index, stream, router=router)
     if out is None:
         with _on(stream):
             out = {"y": x.new_empty((T, h)), "ids": x.new_empty((T, top_k), dtype=torch.int32),
@@ -265,11 +290,10 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
             raise ValueError(f"out['y'] must have shape ({T}, {h}), got {tuple(out['y'].shape)}")
         _b._check_dev("out['ids']", out["ids"], torch.int32, (T, top_k))
         _b._check_dev("out['weights']", out["weights"], torch.float32, (T, top_k))
+        _one_device(index, None, **{f"out['{k}']": out[k] for k in ("y", "ids", "weights")})
     ws, wp, wn = _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), w_gate.device, index, stream)
     s = _raw_stream(index) if stream is None else stream.cuda_stream
-    rc = _call("bakron_q4_moe")(x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate.data.data_ptr(),
-                                w_up.data.data_ptr(), w_down.data.data_ptr(), h, f, E, top_k, w_gate._group,
-                                out["y"].data_ptr(), ldy, out["ids"].data_ptr(), out["weights"].data_ptr(), wp, wn, s)
-    if rc != _b.BAKRON_SUCCESS:
-        raise _b.BakronError(rc, "bakron_q4_moe")
+    _run("bakron_q4_moe", index, x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate.data.data_ptr(),
+         w_up.data.data_ptr(), w_down.data.data_ptr(), h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy,
+         out["ids"].data_ptr(), out["weights"].data_ptr(), wp, wn, s)
     return out
