@@ -121,3 +121,14 @@ def test_tensors_of_two_devices_are_refused(monkeypatch):
         with pytest.raises(ValueError, match="stream is on"):
             call(*args, stream=Stream(), **kw)
     assert len(calls.made) == 1
+
+
+def test_a_workspace_has_all_the_bytes_that_it_counts(monkeypatch):
+    calls = Calls(monkeypatch)
+    x, w = OnDevice.make(0, 300, 128), layer(0, 64, 128)
+    for call, v in ((q4.q4_linear, x), (q4.q4_linear_grad, OnDevice.make(0, 300, 64))):
+        for ws in (OnDevice.make(0, 1, dtype=torch.uint8).expand(1 << 20), OnDevice.make(0, 1 << 20, dtype=torch.uint8)[::2]):
+            ws.at = 0
+            with pytest.raises(ValueError, match="contiguous"):
+                call(v, w, ws=ws)
+    assert not calls.made

@@ -154,6 +154,8 @@ def _ws(ws, size, device, index, stream):
             ws = _b.workspace(need, device)
     elif ws.get_device() != index:
         raise ValueError(f"ws is on {ws.device}, not on {device}")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")   # its bytes are counted as if each were its own
     return ws, ws.data_ptr(), ws.nbytes
 
 
