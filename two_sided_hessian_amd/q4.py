@@ -245,17 +245,46 @@ def _linear(call, size, name, x, w, out, ws, stream):
     return out
 
 
+class _Differentiable(torch.autograd.Function):
+    """q4_linear and q4_linear_grad, each the other's derivative (the codes and
+    grids have none)."""
+
+    @staticmethod
+    def forward(ctx, v, w, call, back, ws, stream):
+        ctx.w, ctx.back = w, back
+        return call(v, w, ws=ws, stream=stream)
+
+    @staticmethod
+    def backward(ctx, g):
+        # (a sum's gradient, say, is one value expanded)
+        return ctx.back(g.contiguous(), ctx.w), None, None, None, None, None
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
 def q4_linear(x, w, *, out=None, ws=None, stream=None):
     """bakron_q4_linear: y = x W^T (tokens x m) of one packed layer, x tokens x n
     in bfloat16 or float16 (rows contiguous, any row stride).  ``out``: where
-    to write y; ``ws``: a workspace of q4_linear_workspace_bytes."""
+    to write y; ``ws``: a workspace of q4_linear_workspace_bytes.  Where x
+    requires a gradient (and ``out`` is not given), autograd takes it with
+    q4_linear_grad."""
+    if _wants_grad(x):
+        if out is not None:
+            raise ValueError("out cannot be given where x requires a gradient")
+        return _Differentiable.apply(x, w, q4_linear, q4_linear_grad, ws, stream)
     return _linear("bakron_q4_linear", q4_linear_workspace_bytes, "x", x, w, out, ws, stream)
 
 
 def q4_linear_grad(dy, w, *, out=None, ws=None, stream=None):
     """bakron_q4_linear_grad: dx = dy W (tokens x n), the gradient of q4_linear
-    with respect to x.  ``out``, ``ws`` (q4_linear_grad_workspace_bytes): as
-    there."""
+    with respect to x.  ``out``, ``ws`` (q4_linear_grad_workspace_bytes) and
+    autograd: as there."""
+    if _wants_grad(dy):
+        if out is not None:
+            raise ValueError("out cannot be given where dy requires a gradient")
+        return _Differentiable.apply(dy, w, q4_linear_grad, q4_linear, ws, stream)
     return _linear("bakron_q4_linear_grad", q4_linear_grad_workspace_bytes, "dy", dy, w, out, ws, stream)
 
 
@@ -265,7 +294,10 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
     w_down a stack of hidden x ffn layers.  Returns dict(y, ids, weights): the
     layer's output, the chosen experts (int32 tokens x top_k, largest logit
     first) and their shares (float32).  ``out``: a dict of the three to write
-    to; ``ws``: a workspace of q4_moe_workspace_bytes."""
+    to; ``ws``: a workspace of q4_moe_workspace_bytes.  It has no gradient:
+    x and router that require one are refused unless under torch.no_grad()."""
+    if _wants_grad(x, router):
+        raise ValueError("q4_moe has no gradient: call it under torch.no_grad() or with detached tensors")
     if not isinstance(w_gate, Q4Weight):
         raise TypeError("w_gate must be a Q4Weight (q4_pack)")
     f, h, E = w_gate.m, w_gate.n, w_gate.count
