@@ -42,7 +42,9 @@ _TYPES = {torch.bfloat16: BAKRON_Q4_BF16, torch.float16: BAKRON_Q4_FP16}
 class Q4Weight:
     """One layer (count 1) or a stack of ``count`` layers of m x n in the
     packed layout, with group_size columns per grid (None: one grid per row).
-    ``data`` is the device buffer (uint8) that holds it."""
+    ``data`` is the device buffer (uint8) that holds it.  ``w[e]`` is layer e of
+    a stack alone, on the same memory: what q4_linear takes (an expert layer
+    for more tokens than q4_moe does goes expert by expert)."""
 
     __slots__ = ("data", "count", "m", "n", "group_size", "_group")
 
@@ -53,6 +55,15 @@ class Q4Weight:
     @property
     def device(self):
         return self.data.device
+
+    def __len__(self):
+        return self.count
+
+    def __getitem__(self, e):
+        if not 0 <= e < self.count:
+            raise IndexError(f"layer {e} of {self.count}")
+        size = _b.lib().bakron_q4_packed_bytes(1, self.m, self.n, self._group)
+        return Q4Weight(self.data[e * size:(e + 1) * size], 1, self.m, self.n, self.group_size)
 
     def __repr__(self):
         return f"Q4Weight(count={self.count}, m={self.m}, n={self.n}, group_size={self.group_size})"
