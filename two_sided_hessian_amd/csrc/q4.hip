@@ -12,6 +12,9 @@ namespace bk {
 // (four lanes a row's 64 bytes; a wave writes one block of 1 KB).  HBM bounds
 // it: 1.5 bytes a code (4096 x 14336: 19.6 us, 4.5 TB/s).
 
+// Rows of codes may start at any byte.
+typedef u32x4 u32x4_byte __attribute__((aligned(1)));
+
 // a dword of codes from eight codes, four to a dword
 __device__ __forceinline__ uint32_t pack8(uint32_t lo, uint32_t hi)
 {
@@ -46,7 +49,7 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
             if (scale[(layer * m + row) * G + g] == 0.f) continue;   // weights of 0: see k_q4_pack_grid
             u32x4 v = {0u, 0u, 0u, 0u};
             if (c0 + 16 <= n) {
-                v = *reinterpret_cast<const u32x4_any*>(src + c0);
+                v = *reinterpret_cast<const u32x4_byte*>(src + c0);
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
