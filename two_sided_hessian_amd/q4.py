@@ -98,6 +98,9 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
     _b._check_dev("zero", zero, torch.float32, gshape)
     index = codes.get_device()
     _one_device(index, stream, scale=scale, zero=zero)
+    if _device() != index:
+        with torch.cuda.device(index):
+            return q4_pack(codes, scale, zero, group_size=group_size, stream=stream, check=check)
     if check and codes.numel():
         with _on(stream):
             size = scale.abs()
@@ -107,11 +110,10 @@ def q4_pack(codes, scale, zero, *, group_size=None, stream=None, check=True):
             raise _b.GridError("codes must lie in [0, 15]")
         if not finite:
             raise _b.GridError("scale must be 0 or of magnitude 2^-100 .. 2^100, zero finite")
-    with _on(stream):
-        data = _b.workspace(_b.lib().bakron_q4_packed_bytes(count, m, n, g), codes.device)
-    _hand_over(stream, data)
+    data, = _made(stream, lambda: (_b.workspace(_b.lib().bakron_q4_packed_bytes(count, m, n, g), codes.device),))
     s = _raw_stream(index) if stream is None else stream.cuda_stream
-    _run("bakron_q4_pack", index, codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), count, m, n, g, data.data_ptr(), s)
+    call = "bakron_q4_pack"
+    _check(_calls[call](codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), count, m, n, g, data.data_ptr(), s), call)
     return Q4Weight(data, count, m, n, group_size)
 
 
@@ -155,19 +157,17 @@ def _one(name, w, index, count=1):
         raise ValueError(f"{name} is on {w.device}, not on cuda:{index}")
 
 
-def _ws(ws, size, device, index, stream):
-    """The workspace as (tensor, pointer, bytes); size() bytes if none is given."""
-    if ws is None:
-        need = size()
-        if not need:
-            return None, None, 0
-        with _on(stream):
-            ws = _b.workspace(need, device)
-    elif ws.get_device() != index:
-        raise ValueError(f"ws is on {ws.device}, not on {device}")
-    elif not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")   # its bytes are counted as if each were its own
-    return ws, ws.data_ptr(), ws.nbytes
+def _workspace(need, device, stream):
+    if not need:
+        return None
+    with _on(stream):
+        return _b.workspace(need, device)
+
+
+def _refuse(ws, index):
+    if ws.get_device() != index:
+        raise ValueError(f"ws is on {ws.device}, not on cuda:{index}")
+    raise ValueError("ws must be contiguous")   # its bytes are counted as if each were its own
 
 
 # The current stream's handle without a Stream object around it (a call of
@@ -188,17 +188,10 @@ def _one_device(index, stream, **tensors):
 
 
 _device = torch._C._cuda_getDevice
+_grad_on = torch.is_grad_enabled
 
 
-def _run(call, index, *args):
-    """The library's call with the tensors' device current: kernels go to the
-    current device, and the default stream's handle names no device."""
-    f = _call(call)
-    if _device() == index:
-        rc = f(*args)
-    else:
-        with torch.cuda.device(index):
-            rc = f(*args)
+def _check(rc, call):
     if rc != _b.BAKRON_SUCCESS:
         raise _b.BakronError(rc, call)
 
@@ -211,24 +204,30 @@ def _on(stream):
     return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _hand_over(stream, *results):
-    """Results made on ``stream`` that the caller will use on the current one:
-    torch's allocator has to wait for that too before it hands them out
-    again."""
-    if stream is not None:
-        here = torch.cuda.current_stream(stream.device)
-        for t in results:
-            t.record_stream(here)
+def _made(stream, make):
+    """Results of a call on ``stream``, made there, that the caller will use on
+    the current one: torch's allocator has to wait for that too before it
+    hands them out again."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        results = make()
+    for t in results:
+        t.record_stream(here)
+    return results
 
 
-_calls = {}
+class _Calls(dict):
+    """The library's functions by name (an attribute of it is looked up anew
+    each time)."""
+
+    def __missing__(self, name):
+        f = self[name] = getattr(_b.lib(), name)
+        return f
 
 
-def _call(name):
-    f = _calls.get(name)
-    if f is None:
-        f = _calls[name] = getattr(_b.lib(), name)
-    return f
+_calls = _Calls()
 
 
 def _linear(call, size, name, x, w, out, ws, stream):
@@ -236,23 +235,39 @@ def _linear(call, size, name, x, w, out, ws, stream):
         raise TypeError("w must be a Q4Weight (q4_pack)")
     in_cols, out_cols = (w.n, w.m) if name == "x" else (w.m, w.n)
     ldx = _rows(name, x, in_cols)
-    index, T = x.get_device(), x.shape[0]
-    _one("w", w, index)
-    if stream is not None:
+    index, T, data = x.get_device(), x.shape[0], w.data
+    if w.count != 1 or data.get_device() != index:
+        _one("w", w, index)
+    if _device() != index:
+        # kernels go to the current device, and the default stream's handle
+        # names none
+        with torch.cuda.device(index):
+            return _linear(call, size, name, x, w, out, ws, stream)
+    if stream is None:
+        s = _raw_stream(index)
+    else:
         _one_device(index, stream)
+        s = stream.cuda_stream
+    if x.requires_grad and _grad_on():
+        if out is not None:
+            raise ValueError(f"out cannot be given where {name} requires a gradient")
+        both = (q4_linear, q4_linear_grad) if name == "x" else (q4_linear_grad, q4_linear)
+        return _Differentiable.apply(x, w, *both, ws, stream)
     if out is None:
-        with _on(stream):
-            out = x.new_empty((T, out_cols))
-        _hand_over(stream, out)
+        out = x.new_empty((T, out_cols)) if stream is None else _made(stream, lambda: (x.new_empty((T, out_cols)),))[0]
         ldo = out_cols
     else:
         ldo = _rows("out", out, out_cols, x.dtype)
         if out.shape[0] != T or out.get_device() != index:
             raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {x.device}")
-    ws, wp, wn = _ws(ws, lambda: size(T, w), w.device, index, stream)
-    s = _raw_stream(index) if stream is None else stream.cuda_stream
-    _run(call, index, x.data_ptr(), ldx, T, _TYPES[x.dtype], w.data.data_ptr(), w.m, w.n, w._group, out.data_ptr(), ldo,
-         wp, wn, s)
+    if ws is None:
+        ws = _workspace(size(T, w), x.device, stream)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        _refuse(ws, index)
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+    rc = _calls[call](x.data_ptr(), ldx, T, _TYPES[x.dtype], data.data_ptr(), w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn, s)
+    if rc:
+        _check(rc, call)
     return out
 
 
@@ -271,20 +286,12 @@ class _Differentiable(torch.autograd.Function):
         return ctx.back(g.contiguous(), ctx.w), None, None, None, None, None
 
 
-def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
-
-
 def q4_linear(x, w, *, out=None, ws=None, stream=None):
     """bakron_q4_linear: y = x W^T (tokens x m) of one packed layer, x tokens x n
     in bfloat16 or float16 (rows contiguous, any row stride).  ``out``: where
     to write y; ``ws``: a workspace of q4_linear_workspace_bytes.  Where x
     requires a gradient (and ``out`` is not given), autograd takes it with
     q4_linear_grad."""
-    if _wants_grad(x):
-        if out is not None:
-            raise ValueError("out cannot be given where x requires a gradient")
-        return _Differentiable.apply(x, w, q4_linear, q4_linear_grad, ws, stream)
     return _linear("bakron_q4_linear", q4_linear_workspace_bytes, "x", x, w, out, ws, stream)
 
 
@@ -292,10 +299,6 @@ def q4_linear_grad(dy, w, *, out=None, ws=None, stream=None):
     """bakron_q4_linear_grad: dx = dy W (tokens x n), the gradient of q4_linear
     with respect to x.  ``out``, ``ws`` (q4_linear_grad_workspace_bytes) and
     autograd: as there."""
-    if _wants_grad(dy):
-        if out is not None:
-            raise ValueError("out cannot be given where dy requires a gradient")
-        return _Differentiable.apply(dy, w, q4_linear_grad, q4_linear, ws, stream)
     return _linear("bakron_q4_linear_grad", q4_linear_grad_workspace_bytes, "dy", dy, w, out, ws, stream)
 
 
@@ -307,38 +310,56 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
     first) and their shares (float32).  ``out``: a dict of the three to write
     to; ``ws``: a workspace of q4_moe_workspace_bytes.  It has no gradient:
     x and router that require one are refused unless under torch.no_grad()."""
-    if _wants_grad(x, router):
-        raise ValueError("q4_moe has no gradient: call it under torch.no_grad() or with detached tensors")
     if not isinstance(w_gate, Q4Weight):
         raise TypeError("w_gate must be a Q4Weight (q4_pack)")
     f, h, E = w_gate.m, w_gate.n, w_gate.count
     ldx = _rows("x", x, h)
     index, T, dtype = x.get_device(), x.shape[0], x.dtype
-    _one("w_gate", w_gate, index, E)
-    for name, w, shape in (("w_up", w_up, (f, h)), ("w_down", w_down, (h, f))):
-        _one(name, w, index, E)
-        if (w.m, w.n) != shape:
-            raise ValueError(f"{name} must be {shape}, got {(w.m, w.n)}")
-        if w._group != w_gate._group:
+    if w_gate.data.get_device() != index:
+        _one("w_gate", w_gate, index, E)
+    group = w_gate._group
+    for name, w, m, n in (("w_up", w_up, f, h), ("w_down", w_down, h, f)):
+        if not isinstance(w, Q4Weight) or w.count != E or w.data.get_device() != index:
+            _one(name, w, index, E)
+        if w.m != m or w.n != n:
+            raise ValueError(f"{name} must be {(m, n)}, got {(w.m, w.n)}")
+        if w._group != group:
             raise ValueError("the three stacks must have one group_size")
-    _b._check_dev("router", router, dtype, (E, h))
-    _one_device(index, stream, router=router)
-    if out is None:
-        with _on(stream):
-            out = {"y": x.new_empty((T, h)), "ids": x.new_empty((T, top_k), dtype=torch.int32),
-                   "weights": x.new_empty((T, top_k), dtype=torch.float32)}
-        _hand_over(stream, *out.values())
-        ldy = h
+    if not (isinstance(router, torch.Tensor) and router.dtype == dtype and router.get_device() == index and
+            router.shape == (E, h) and router.is_contiguous()):
+        _b._check_dev("router", router, dtype, (E, h))
+        _one_device(index, None, router=router)
+    if _device() != index:
+        with torch.cuda.device(index):
+            return q4_moe(x, router, w_gate, w_up, w_down, top_k, out=out, ws=ws, stream=stream)
+    if stream is None:
+        s = _raw_stream(index)
     else:
-        ldy = _rows("out['y']", out["y"], h, dtype)
-        if out["y"].shape[0] != T:
-            raise ValueError(f"out['y'] must have shape ({T}, {h}), got {tuple(out['y'].shape)}")
-        _b._check_dev("out['ids']", out["ids"], torch.int32, (T, top_k))
-        _b._check_dev("out['weights']", out["weights"], torch.float32, (T, top_k))
-        _one_device(index, None, **{f"out['{k}']": out[k] for k in ("y", "ids", "weights")})
-    ws, wp, wn = _ws(ws, lambda: q4_moe_workspace_bytes(T, w_gate, top_k), w_gate.device, index, stream)
-    s = _raw_stream(index) if stream is None else stream.cuda_stream
-    _run("bakron_q4_moe", index, x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate.data.data_ptr(),
-         w_up.data.data_ptr(), w_down.data.data_ptr(), h, f, E, top_k, w_gate._group, out["y"].data_ptr(), ldy,
-         out["ids"].data_ptr(), out["weights"].data_ptr(), wp, wn, s)
+        _one_device(index, stream)
+        s = stream.cuda_stream
+    if (x.requires_grad or router.requires_grad) and _grad_on():
+        raise ValueError("q4_moe has no gradient: call it under torch.no_grad() or with detached tensors")
+    if out is None:
+        y, ids, weights = _made(stream, lambda: (x.new_empty((T, h)), x.new_empty((T, top_k), dtype=torch.int32),
+                                                 x.new_empty((T, top_k), dtype=torch.float32)))
+        out, ldy = {"y": y, "ids": ids, "weights": weights}, h
+    else:
+        y, ids, weights = out["y"], out["ids"], out["weights"]
+        ldy = _rows("out['y']", y, h, dtype)
+        if y.shape[0] != T:
+            raise ValueError(f"out['y'] must have shape ({T}, {h}), got {tuple(y.shape)}")
+        _b._check_dev("out['ids']", ids, torch.int32, (T, top_k))
+        _b._check_dev("out['weights']", weights, torch.float32, (T, top_k))
+        _one_device(index, None, **{"out['y']": y, "out['ids']": ids, "out['weights']": weights})
+    if ws is None:
+        ws = _workspace(q4_moe_workspace_bytes(T, w_gate, top_k), x.device, stream)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        _refuse(ws, index)
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+    call = "bakron_q4_moe"
+    rc = _calls[call](x.data_ptr(), ldx, T, _TYPES[dtype], router.data_ptr(), w_gate.data.data_ptr(), w_up.data.data_ptr(),
+                      w_down.data.data_ptr(), h, f, E, top_k, group, y.data_ptr(), ldy, ids.data_ptr(),
+                      weights.data_ptr(), wp, wn, s)
+    if rc:
+        _check(rc, call)
     return out
