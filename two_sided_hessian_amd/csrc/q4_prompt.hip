@@ -319,48 +319,48 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
 #pragma unroll
                     for (int a = 0; a < TA; ++a) xf[v][a] = *reinterpret_cast<const vec*>(s + x_lane[v] + 4096 * a);
                 if (left == 0) {
-                    const bool first = c == 2 * kb0;
-                    if (!first) {
-                        // the end of a piece: its zero points
-                        float z[2];
+                    // the end of a piece (or the start): its zero points, and
+                    // where its group ends too, the next one's steps
+                    const bool first = c == 2 * kb0, change = first || in_group == w.gb;
+                    f32x2 s1[2];
+                    float z[2], ratio[2];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) z[b] = -(sz[b].y + kQ4Offset);
-                        if (OWN) {
-#pragma unroll
-                            for (int a = 0; a < TA; ++a)
-#pragma unroll
-                                for (int r = 0; r < 16; ++r) {
-#pragma unroll
-                                    for (int b = 0; b < 2; ++b) acc[a][b][r] = fmaf(z[b], sx[a][r], acc[a][b][r]);
-                                    sx[a][r] = 0.f;
-                                }
-                        } else if (open) {
+                    for (int b = 0; b < 2; ++b) {
+                        s1[b] = *reinterpret_cast<const f32x2*>(lds + g_lane + bx * P::GBUF + 256 * b);
+                        z[b] = -(sz[b].y + kQ4Offset);
+                    }
+                    if (!OWN && !first) {
+                        if (open) {
 #pragma unroll
                             for (int b = 0; b < 2; ++b) z[b] = h ? z[b] : z_open[b];
                             zero_points<TA>(acc, xs, z);
-                            open = false;
                             pair += 2;
                             load_sums();
                         } else {
 #pragma unroll
                             for (int b = 0; b < 2; ++b) z_open[b] = z[b];
-                            open = true;
                         }
+                        open = !open;
                     }
-                    if (first || in_group == w.gb) {
-                        if (!first) in_group = 0;
-                        const char* g = lds + g_lane + bx * P::GBUF;
+                    if (change && !first) in_group = 0;
+                    if (OWN || change) {   // (OWN: one body for both; its code is read anew by every short launch)
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
-                            const f32x2 s1 = *reinterpret_cast<const f32x2*>(g + 256 * b);
-                            const float ratio = sz[b].x * __builtin_amdgcn_rcpf(s1.x);
-                            sz[b] = s1;
-                            z_open[b] *= ratio;
+                            ratio[b] = change ? sz[b].x * __builtin_amdgcn_rcpf(s1[b].x) : 1.f;
+                            sz[b] = s1[b];   // (unchanged within a group)
+                            z_open[b] *= ratio[b];
 #pragma unroll
                             for (int a = 0; a < TA; ++a)
 #pragma unroll
-                                for (int r = 0; r < 16; ++r) acc[a][b][r] *= ratio;
+                                for (int r = 0; r < 16; ++r)
+                                    acc[a][b][r] = (OWN ? fmaf(z[b], sx[a][r], acc[a][b][r]) : acc[a][b][r]) * ratio[b];
                         }
+                    }
+                    if (OWN) {
+#pragma unroll
+                        for (int a = 0; a < TA; ++a)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) sx[a][r] = 0.f;
                     }
                     left = min(kPiece - in_group % kPiece, w.gb - in_group);
                     in_group += left;
