@@ -408,8 +408,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_q4_moe_down(const uint16_t*
     // The last split of a row tile to get here adds all of them, in split
     // order.  Partial sums are stored and loaded past the XCD's own cache
     // (device-scope atomics), and each wave's stores have completed before the
-    // tile's counter (cleared by k_q4_router) is raised: what a device-wide
-    // fence would do for all of the cache (measured at 80 us for a launch).
+    // tile's counter (cleared by k_q4_router) is raised.  That order is this
+    // chip's, not the language's: a device-scope store counts as complete
+    // (vmcnt) once it has reached the memory that all XCDs read, device-scope
+    // loads read there, and the loads below are issued after the counter's
+    // answer.  The language's model asks for a release and an acquire, which
+    // write back and drop the whole cache (measured at 80 us for a launch).
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0)
