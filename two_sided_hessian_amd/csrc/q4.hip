@@ -10,7 +10,7 @@ namespace bk {
 //
 // One thread per 16-byte unit: 32 codes of one row, read as two runs of 16
 // (four lanes a row's 64 bytes; a wave writes one block of 1 KB).  HBM bounds
-// it: 1.5 bytes a code (4096 x 14336: 19.6 us, 4.5 TB/s).
+// it: 1.5 bytes a code (4096 x 14336: 18.9 us, 4.7 TB/s).
 
 // Rows of codes may start at any byte.
 typedef u32x4 u32x4_byte __attribute__((aligned(1)));
@@ -64,8 +64,10 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
 
 // Grids, and the units: the exponent, rounded up, of the largest weight of each
 // group's columns (a maximum of integers, which does not depend on the order it
-// is taken in).  A workgroup takes row tiles in turn, 16 lanes a row; a few
-// workgroups per layer, so that few atomics meet at a unit.
+// is taken in).  A row has LANES lanes, as many as it has groups, 16 at most, and
+// a workgroup 16 / LANES row tiles at a time; at most so many workgroups per layer
+// that few atomics meet at a unit.  4096 x 14336 in groups of 128: 11.8 us (128
+// workgroups: 15.5); 65536 rows with a grid each: 5.9 (16 lanes a row: 15.5).
 //
 // A step of 0 (every weight 0, whatever the codes) is written as the row's
 // smallest step, zero point 0, on codes of 0: kernels divide by steps, and
@@ -73,34 +75,37 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ cod
 // 16 sum x under the present one and taking it off again.  Under a step above
 // the row's others (1, say) that difference's float32 error would bury them.
 // Rows without any step take the smallest normal number.
-constexpr int kPackGridBlocks = 128;
+constexpr int kPackGridBlocks = 512;
 constexpr float kPackNoStep = 0x1p-126f;
 
+template <int LANES>
 __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ scale, const float* __restrict__ zero,
                                                       int64_t m, int RT, int G, int64_t layer_bytes, int64_t grid_at,
                                                       int64_t unit_at, char* __restrict__ packed)
 {
-    __shared__ float tops[kQ4MaxHalves];   // a group has 64 columns at least
+    constexpr int TILES = 16 / LANES;
+    __shared__ unsigned tops[kQ4MaxHalves];   // floats from 0 on; a group has 64 columns at least
     __shared__ float least[16][kQ4Rows];
     const int64_t layer = blockIdx.y;
-    const int r = threadIdx.x & 15, g0 = threadIdx.x >> 4;
-    for (int g = threadIdx.x; g < G; g += 256) tops[g] = 0.f;
-    for (int tile = blockIdx.x; tile < RT; tile += gridDim.x) {
+    const int r = threadIdx.x & 15, q = threadIdx.x >> 4, g0 = q % LANES;
+    for (int g = threadIdx.x; g < G; g += 256) tops[g] = 0u;
+    for (int tile0 = blockIdx.x * TILES; tile0 < RT; tile0 += gridDim.x * TILES) {
+        const int tile = tile0 + q / LANES;
         const int64_t row = (int64_t)tile * kQ4Rows + r;
         const int64_t at = (layer * m + row) * G;
         float low = INFINITY;
         if (row < m)
-            for (int g = g0; g < G; g += 16) {
+            for (int g = g0; g < G; g += LANES) {
                 const float s = fabsf(scale[at + g]);
                 if (s > 0.f) low = fminf(low, s);
             }
-        least[g0][r] = low;
+        least[q][r] = low;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) low = fminf(low, least[i][r]);
+        for (int i = 0; i < LANES; ++i) low = fminf(low, least[q / LANES * LANES + i][r]);
         if (low == INFINITY) low = kPackNoStep;
         f32x2* out = reinterpret_cast<f32x2*>(packed + layer * layer_bytes + grid_at) + (int64_t)tile * G * kQ4Rows + r;
-        for (int g = g0; g < G; g += 16) {
+        for (int g = g0; g < G && tile < RT; g += LANES) {
             f32x2 v = {0.f, 0.f};
             float top = 0.f;
             if (row < m) {
@@ -110,14 +115,14 @@ __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ 
                 else top = fabsf(v.x) * fmaxf(fabsf(v.y), fabsf(15.f - v.y));
             }
             out[g * kQ4Rows] = v;
-            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-            if (r == 0) tops[g] = fmaxf(tops[g], top);   // (group g is this thread's alone)
+            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));   // (16 rows, all here)
+            if (r == 0) atomicMax(&tops[g], __float_as_uint(top));
         }
-        __syncthreads();   // the next tile's minima overwrite these
+        __syncthreads();   // the next tiles' minima overwrite these
     }
     unsigned* units = reinterpret_cast<unsigned*>(packed + layer * layer_bytes + unit_at);
     for (int g = threadIdx.x; g < G; g += 256) {
-        const float top = tops[g];
+        const float top = __uint_as_float(tops[g]);
         if (top > 0.f && top < INFINITY) atomicMax(&units[g], max(min((__float_as_uint(top) >> 23) + 1u, 254u), 1u) << 23);
     }
 }
@@ -254,9 +259,12 @@ int bakron_q4_pack(const uint8_t* codes, const float* scale, const float* zero, 
     bk::launch(nullptr, bk::KK_Q4_PACK, 0.0, 1.5 * mn, bk::k_q4_pack,
                dim3((unsigned)bk::ceil_div((int64_t)d.RT * d.KB, 4), (unsigned)count), dim3(256), stream, codes, scale,
                m, n, d.RT, d.KB, d.G, d.gb, (int64_t)d.bytes, (int64_t)d.unit_at, out);
-    bk::launch(nullptr, bk::KK_Q4_PACK_GRID, 0.0, 16.0 * count * m * d.G, bk::k_q4_pack_grid,
-               dim3((unsigned)std::min(bk::kPackGridBlocks, d.RT), (unsigned)count), dim3(256), stream,
-               scale, zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
+    const int lanes = d.G > 8 ? 16 : d.G > 4 ? 8 : d.G > 2 ? 4 : d.G;
+    auto* grids = lanes == 16 ? bk::k_q4_pack_grid<16> : lanes == 8 ? bk::k_q4_pack_grid<8>
+                : lanes == 4 ? bk::k_q4_pack_grid<4> : lanes == 2 ? bk::k_q4_pack_grid<2> : bk::k_q4_pack_grid<1>;
+    bk::launch(nullptr, bk::KK_Q4_PACK_GRID, 0.0, 16.0 * count * m * d.G, grids,
+               dim3((unsigned)std::min<int64_t>(bk::kPackGridBlocks, bk::ceil_div(d.RT, 16 / lanes)), (unsigned)count),
+               dim3(256), stream, scale, zero, m, d.RT, d.G, (int64_t)d.bytes, (int64_t)d.grid_at, (int64_t)d.unit_at, out);
     return hipGetLastError() == hipSuccess ? BAKRON_SUCCESS : BAKRON_ERR_HIP;
 }
 
