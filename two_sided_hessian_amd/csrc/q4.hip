@@ -133,12 +133,14 @@ __global__ __launch_bounds__(256) void k_q4_pack_grid(const float* __restrict__ 
 // column blocks in turn (FewSpan) and are joined through LDS in wave order,
 // so the result does not depend on timing.
 //
-// Measured (a copy of 1 GiB reaches 5.1 TB/s): two tokens x 28672 x 8192, groups
-// of 128: 25.6 us, 5.1 TB/s; one token x 4096 x 14336: 7.7 us, 4.3 TB/s, of which
-// 2.8 are those of a 1024 x 1024 layer, a launch and a round trip; 16 tokens x
-// 14336 x 4096, groups of 64: 9.9 us, 3.7 TB/s; 64 tokens x 4096 x 4096: 11.5 us,
-// where expanding for four tiles of tokens at once holds too many registers
-// for more waves.
+// Measured, layers from HBM (1.2 GB of them in turn) and one layer over and over,
+// from the Infinity Cache: two tokens x 28672 x 8192, groups of 128: 25.8 us, 5.1
+// TB/s (the rate of a 1 GiB copy), and 22.3; one token x 4096 x 14336: 9.4 us, 3.5
+// TB/s, and 6.7, of which 2.2 are those of a 1024 x 1024 layer, a launch and a
+// round trip; 16 tokens x 14336 x 4096, groups of 64: 12.2 us, 3.0 TB/s, and 9.3;
+// 64 tokens x 4096 x 4096: 11.4 us and 10.1: 256 workgroups of 16 rows each read all
+// of x, 134 MB through the L2 caches, and expanding for four tiles of tokens at
+// once holds too many registers for more waves.
 template <class X, int TQ, int R, int WAVES, int U, bool HALF>
 __global__ __launch_bounds__(64 * WAVES) void k_q4_few(const uint16_t* __restrict__ x, int64_t ldx, int T, Q4Layer w,
                                                        uint16_t* __restrict__ y, int64_t ldy)

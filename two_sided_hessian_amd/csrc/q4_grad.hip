@@ -23,11 +23,13 @@
 // one barrier per chunk orders everything.  Few tiles share out their rows of
 // W over several workgroups, joined by k_q4_join.
 //
-// Measured: 2048 tokens x 4096 x 14336, groups of 128: 240 - 251 us, 960 - 1000
-// TFLOP/s (a large 16-bit product of the vendor's library: 1240).  LDS bounds
-// it: besides the fragments, every weight is written to it once and read by
-// the tiles of two wave rows.  300 tokens x 1000 x 1531, unaligned: 16.5 us, of
-// which the copy of dy takes 3.5 and the join 3 - 4.
+// Measured: 2048 tokens x 4096 x 14336, groups of 128: 239 - 252 us, 950 - 1010
+// TFLOP/s (a large 16-bit product of the vendor's library: 1240).  No unit is
+// full: of the cycles in which a CU has work MFMAs take 0.50, LDS instructions
+// 0.45 (besides the fragments, every weight is written once and read by the
+// tiles of two wave rows) and vector instructions 0.36; two waves a SIMD and a
+// barrier a chunk overlap them only in part.  300 tokens x 1000 x 1531,
+// unaligned: 16.5 us, of which the copy of dy takes 3.4 and the join 3.8.
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"

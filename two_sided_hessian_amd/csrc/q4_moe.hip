@@ -24,8 +24,8 @@
 //     split order.  No result depends on timing.
 // HBM bounds it: the chosen experts' codes and grids are read once.  Measured,
 // router, up and down in turn: one token, 2 of 8 experts of 4096 x 14336, groups
-// of 128: 4, 28 (4.7 TB/s) and 15 - 19 us, the call 50 - 56; 16 tokens, 6 of 64
-// experts of 2048 x 1024, groups of 64: 6, 40 (3.1 TB/s) and 27, the call 74:
+// of 128: 5, 29 (4.5 TB/s) and 16 us, the call 50; 16 tokens, 6 of 64 experts of
+// 2048 x 1024, groups of 64: 6, 40 (3.5 TB/s) and 27, the call 69 - 72:
 // choosing, first round trips and the joins weigh more in short rows, and grids
 // are a fifth of the bytes; 16 tokens, 2 of 16 experts of 4096 x 14336: 309 us,
 // 4.5 TB/s over all.

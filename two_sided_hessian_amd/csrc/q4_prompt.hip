@@ -33,13 +33,13 @@
 //
 // Measured, in the rate of 2 T m n (a large 16-bit product of the vendor's
 // library reaches 1240 TFLOP/s): 8192 tokens x 8192 x 8192, one grid per row,
-// 780 - 820 us, 1340 - 1410 TFLOP/s; in groups of 128, 910 us, 1210; 2048 x 4096
-// x 4096, groups of 128, 70 - 76 us, 900 - 980; 777 x 4099 x 2050, groups of 64,
-// unaligned, 35 - 37 us, 350.  MFMAs bound it, and the power limit their clock
-// (1.9 GHz): 2840 cycles a chunk against 2048 of MFMAs; with TA = 2, 1690
-// against 1024: LDS reads, expansion and staging add about 180, 150 and 220.
-// Groups of 64 change the accumulators' step at every chunk, 128 at every
-// other: 13 % of the 8192 case.
+// 777 - 830 us, 1320 - 1410 TFLOP/s; in groups of 128, 910 - 935 us, 1180 - 1210;
+// 2048 x 4096 x 4096, groups of 128, 72 - 78 us, 880 - 950; 777 x 4099 x 2050,
+// groups of 64, unaligned, 34.6 - 36 us, 360 - 380.  MFMAs bound it, and the power
+// limit their clock (1.9 GHz): of the cycles in which a CU has work they take
+// 0.75 in the 8192 case and 0.52 in the 2048 one (TA = 2), where vector
+// instructions (expansion, MFMA issue) take 0.52 too.  Groups of 64 change the
+// accumulators' step at every chunk, 128 at every other: 12 % of the 8192 case.
 #include <algorithm>
 
 #include "../../include/bakron_q4.h"
@@ -53,7 +53,7 @@ namespace bk {
 // One wave per token: lanes sum 8 columns, 8 lanes a 64-column half (the loads
 // of four spans of 512 columns together), and the halves of a piece are added
 // in order.  COPY: the row goes to `copy` too, columns n .. 64 ceil(n / 64) - 1
-// zero.  HBM bounds it: 37 us for 8192 x 8192 (3.6 TB/s), 5 for 2048 x 4096.
+// zero.  HBM bounds it: 33 us for 8192 x 8192 (4.1 TB/s), 5 for 2048 x 4096.
 constexpr int kSumsHalves = BAKRON_MAX_DIM / 64;
 
 // Pieces of the columns, in halves of 64: a group's first, second, ... kPiece,
