@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libbakron.so")
 SOURCES = ["factor.hip", "solve.hip", "gptq.hip", "kfac.hip", "antidiag.hip", "capi.hip", "noalloc.hip",
-           "q4.hip", "q4_prompt.hip", "q4_grad.hip", "q4_moe.hip"]
+           "q4.hip", "q4_prompt.hip", "q4_grad.hip", "q4_moe.hip", "q4_experts.hip",
+           "moe_route.hip", "moe_rows.hip", "moe_gated.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -84,6 +84,13 @@ inline void launch_shm(Prof* p, int kind, double flops, double bytes, void (*ker
     p->recs.push_back(r);
 }
 
+// A launch of a call that has no *_profiled form.
+template <typename... KArgs, typename... Args>
+inline void enqueue(void (*kernel)(KArgs...), dim3 g, dim3 b, hipStream_t s, Args... args)
+{
+    hipLaunchKernelGGL(kernel, g, b, 0, s, static_cast<KArgs>(args)...);
+}
+
 // A library-owned stream (default priority, non-blocking) for work that a
 // call forks off the caller's stream and joins back with events.  A fixed
 // pool of kSideSlots streams per device, created on first use and kept for

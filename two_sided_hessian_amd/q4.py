@@ -139,7 +139,7 @@ def _rows(name, t, cols, like=None):
     if len(shape) != 2 or shape[1] != cols:
         raise ValueError(f"{name} must have shape (tokens, {cols}), got {tuple(shape)}")
     ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if cols > 1 and inner != 1 and shape[0]:   # (no rows: any strides, as autograd's are)
         raise ValueError(f"{name} must have contiguous rows")
     if shape[0] <= 1 or cols == 0:
         return cols
