@@ -1,27 +1,35 @@
 """Which kernel form the experts' products take for a problem: the library's
 choice (csrc/q4_experts.hip experts_plan, experts_grad_plan, experts_run),
 written out again so that a test can say which form it is meant to reach."""
-from q4_forms import GRAD, PROMPT, ceil_div
+from q4_forms import ceil_div
 
 FEW_ROWS = 32
+PRODUCT = [(256, 256, (128.0, 80.0, 56.0)), (128, 128, (42.0, 28.0, 28.0))]
+GRAD = [(256, 256, (130.0, 88.0, 64.0))]
 
 
-def blocks_about(R, E, tokens):
+def estimate(shape, R, E, cols, depth, splits):
+    rows, width, us = shape
     some = min(R, E)
-    return max(some, R // tokens + some // 2)
+    c, nc = R / some, ceil_div(cols, width)
+    tile, one = us[0], c / rows * us[0] + 0.25 * (us[1] + us[2])
+    if c <= rows // 4:
+        tile = one = us[2]
+    elif c <= rows // 2:
+        tile = one = us[1]
+    work = max(some * nc * one / 256 + 0.4 * tile / splits, tile / splits)
+    return work * depth / 4096 + (2.0 + 8.0e-6 / 4 * splits * R * cols if splits > 1 else 0.0)
 
 
-def choose(shapes, R, E, cols, depth, most):
-    """(rows, columns) of the tile and the workgroups that share its terms."""
+def choose(shapes, R, E, cols, depth, deepest):
+    """(rows, columns) of the largest tile and the workgroups that share its depth."""
     best, least = None, 0.0
-    for tokens, width, cost in shapes:
-        tiles = blocks_about(R, E, tokens) * ceil_div(cols, width)
+    for shape in shapes:
         s = 1
-        while s == 1 or (s <= most and tiles * s <= 1024):
-            us = (ceil_div(tiles * s, 256) * cost * depth / (4096.0 * s) +
-                  (2.0 + 8.0e-6 / 4 * s * R * cols if s > 1 else 0.0))
+        while s == 1 or (s <= deepest and (R // shape[0] + min(R, E)) * ceil_div(cols, shape[1]) * s <= 2048):
+            us = estimate(shape, R, E, cols, depth, s)
             if least == 0.0 or us < least:
-                least, best = us, (tokens, width, s)
+                least, best = us, (shape[0], shape[1], s)
             s += 1
     return best
 
@@ -31,7 +39,7 @@ def experts_form(R, E, m, n):
     if R <= FEW_ROWS * E:
         waves = ceil_div(ceil_div(m, 16), 2) * min(R, E)
         return "few", 8 if 8 * waves <= 8192 else 4 if 4 * waves <= 8192 else 2
-    return choose(PROMPT, R, E, m, n, min(8, ceil_div(n, 128) // 2))
+    return choose(PRODUCT, R, E, m, n, min(8, ceil_div(n, 128) // 2))
 
 
 def experts_grad_form(R, E, m, n):

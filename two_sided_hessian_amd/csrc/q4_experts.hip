@@ -24,89 +24,144 @@ namespace bk {
 constexpr int kExperts = BAKRON_MOE_MAX_EXPERTS;
 static_assert(kExperts <= 4 * 64, "four experts a lane");
 
-// The rows of block `block` of BT rows each, counted expert by expert; blocks(total)
-// says which one is wanted (-1: none).  A wave's work, the same in every wave.
+// Sums of v over lanes 0 .. this one (DPP: shifts within rows of 16 lanes, then
+// the rows' last lanes to the rows after them).
+__device__ __forceinline__ int lanes_upto(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+}
+
+// The first lane whose `upto` is above `want` (held below the last one's, so that there
+// is one); the rest of want there.
+__device__ __forceinline__ int lane_of(int upto, int sum, int& want)
+{
+    want = min(want, __builtin_amdgcn_readlane(upto, 63) - 1);
+    const int l = __ffsll((unsigned long long)__ballot(upto > want)) - 1;
+    want -= __builtin_amdgcn_readlane(upto - sum, l);
+    return l;
+}
+
+// A lane's four experts: their first rows, held in [0, R].
+struct ExpertLane {
+    int o[5];
+    __device__ __forceinline__ ExpertLane(const int32_t* __restrict__ offsets, int E, int R)
+    {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int u = 0; u < 5; ++u) o[u] = min(max(offsets[min(4 * lane + u, E)], 0), R);
+    }
+    __device__ __forceinline__ int rows(int u) const { return max(o[u + 1] - o[u], 0); }
+};
+
+// Rows of one expert: block k of those that `count` finds in lane l.
 struct ExpertRows {
     int e, t0, t1;   // the expert, the block's first row, and the expert's end
 };
-template <class Pick>
-__device__ __forceinline__ bool expert_rows(const int32_t* __restrict__ offsets, int E, int R, int BT, Pick pick, ExpertRows& out)
+template <class Count>
+__device__ __forceinline__ int expert_at(const ExpertLane& lane, int l, int& k, Count count, ExpertRows& out)
 {
-    const int lane = threadIdx.x & 63;
-    int o[5];
+    int u = 0;
 #pragma unroll
-    for (int u = 0; u < 5; ++u) o[u] = min(max(offsets[min(4 * lane + u, E)], 0), R);
-    int tiles[4], sum = 0;
+    for (int v = 0; v < 3; ++v) {
+        const int n = __builtin_amdgcn_readlane(count(lane.rows(v)), l);
+        if (u == v && k >= n) k -= n, ++u;
+    }
+    int first = 0, last = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        tiles[u] = (max(o[u + 1] - o[u], 0) + BT - 1) / BT;
-        sum += tiles[u];
-    }
-    int upto = sum;
-    for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(upto, off);
-        if (lane >= off) upto += v;
-    }
-    const int want = pick(__builtin_amdgcn_readlane(upto, 63));
-    if (want < 0) return false;
-    const unsigned long long at = __ballot(upto > want);
-    if (!at) return false;
-    const int l = __ffsll(at) - 1;
-    int k = want - __builtin_amdgcn_readlane(upto - sum, l);
-    int e = 4 * l, first = __builtin_amdgcn_readlane(o[0], l), last = __builtin_amdgcn_readlane(o[1], l);
+    for (int v = 0; v < 4; ++v)
+        if (u == v) first = __builtin_amdgcn_readlane(lane.o[v], l), last = __builtin_amdgcn_readlane(lane.o[v + 1], l);
+    out = ExpertRows{4 * l + u, first, last};
+    return u;
+}
+
+// The tile of this workgroup.  An expert's rows go into blocks of 64 TA, the last
+// one cut; what is cut takes a body for 128 or 64 rows where that is enough.  The
+// order of tiles is that of their cost, bodies for more rows first, so that the
+// short ones fill up what the long ones leave; `cls` is 0 for 64 TA rows, 1 for half
+// of that, 2 for a quarter.  nc: tiles beside each other.  A wave's work, the same
+// in every wave.
+template <int TA>
+__device__ __forceinline__ bool expert_tile(const int32_t* __restrict__ offsets, int E, int R, int nc, ExpertRows& rows, int& bc,
+                                            int& cls)
+{
+    constexpr int BT = 64 * TA;
+    static_assert(TA == 2 || TA == 4, "");
+    const ExpertLane lane(offsets, E, R);
+    const auto big = [](int c) { return c / BT + (c % BT > BT / 2); };
+    const auto half = [](int c) { return (int)(TA == 4 ? c % BT > 64 && c % BT <= 128 : c % BT > 0 && c % BT <= 64); };
+    const auto quarter = [](int c) { return (int)(TA == 4 && c % BT > 0 && c % BT <= 64); };
+    int bigs = 0, rest = 0;   // rest: halves, and quarters in the upper 16 bits
 #pragma unroll
-    for (int u = 0; u < 3; ++u) {
-        const int n = __builtin_amdgcn_readlane(tiles[u], l);
-        if (e == 4 * l + u && k >= n) {
-            k -= n;
-            ++e;
-            first = __builtin_amdgcn_readlane(o[u + 1], l);
-            last = __builtin_amdgcn_readlane(o[u + 2], l);
-        }
+    for (int u = 0; u < 4; ++u) bigs += big(lane.rows(u)), rest += half(lane.rows(u)) | quarter(lane.rows(u)) << 16;
+    const int bigs_upto = lanes_upto(bigs), rest_upto = lanes_upto(rest);
+    const int nb = __builtin_amdgcn_readlane(bigs_upto, 63), nh = __builtin_amdgcn_readlane(rest_upto, 63) & 0xFFFF,
+              nq = __builtin_amdgcn_readlane(rest_upto, 63) >> 16;
+    int64_t b = blockIdx.x;
+    int bt;
+    if (b < (int64_t)nb * nc) {
+        cls = 0;
+        tile_at((unsigned)b, nb, nc, bt, bc);
+        const int l = lane_of(bigs_upto, bigs, bt);
+        expert_at(lane, l, bt, big, rows);
+        rows.t0 += bt * BT;
+        return true;
     }
-    out = ExpertRows{e, first + k * BT, last};
+    b -= (int64_t)nb * nc;
+    if (b < nh * nc) {
+        cls = 1;
+        tile_at((unsigned)b, nh, nc, bt, bc);
+        const int l = lane_of(rest_upto & 0xFFFF, rest & 0xFFFF, bt);
+        expert_at(lane, l, bt, half, rows);
+    } else {
+        b -= nh * nc;
+        if (b >= nq * nc) return false;
+        cls = 2;
+        tile_at((unsigned)b, nq, nc, bt, bc);
+        const int l = lane_of(rest_upto >> 16, rest >> 16, bt);
+        expert_at(lane, l, bt, quarter, rows);
+    }
+    rows.t0 += (rows.t1 - rows.t0) / BT * BT;
     return true;
 }
 
-// The output tile of this workgroup: block of rows and column bc of nc.
-template <int BT>
-__device__ __forceinline__ bool expert_tile(const int32_t* __restrict__ offsets, int E, int R, int most, int nc,
-                                            ExpertRows& rows, int& bc)
-{
-    return expert_rows(offsets, E, R, BT, [&](int nt) {
-        nt = min(nt, most);
-        if ((int)blockIdx.x >= nt * nc) return -1;
-        int bt;
-        tile_of(nt, nc, bt, bc);
-        return bt;
-    }, rows);
-}
-
-template <class X, int TA, int WR, bool OWN>
+// Tiles of 256, 128 and 64 rows by 256 of W (WR = 4), or of 128 and 64 by 128 (WR = 2).
+// OWN (WR = 2): the rows' sums are made beside the products (q4_prompt.hpp).
+template <class X, int WR, bool OWN>
 __global__ __launch_bounds__(128 * WR, 2) void k_q4_experts(const uint16_t* __restrict__ x, int64_t ldx, int R,
                                                             const int32_t* __restrict__ offsets, int E, Q4Layer stack,
                                                             int64_t layer_bytes, const float* __restrict__ sums, int64_t lds_,
-                                                            uint16_t* __restrict__ y, int64_t ldy, int most, int nr,
+                                                            uint16_t* __restrict__ y, int64_t ldy, int nr,
                                                             float* __restrict__ part)
 {
+    constexpr int BYTES = std::max(std::max(Prompt<WR, WR>::LDS, Prompt<WR / 2, WR>::LDS), Prompt<1, WR>::LDS);
     ExpertRows rows;
-    int br;
-    if (!expert_tile<64 * TA>(offsets, E, R, most, nr, rows, br)) return;
+    int br, cls;
+    if (!expert_tile<WR>(offsets, E, R, nr, rows, br, cls)) return;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
-    prompt_tile<X, TA, WR, OWN>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    if (cls == 0) prompt_tile<X, WR, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    else if (cls == 1) prompt_tile<X, WR / 2, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    else if (WR == 4) prompt_tile<X, 1, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
 }
 
-template <class X, int TA>
+template <class X>
 __global__ __launch_bounds__(512) void k_q4_experts_grad(const uint16_t* __restrict__ dy, int64_t lddy, int R,
                                                          const int32_t* __restrict__ offsets, int E, Q4Layer stack,
                                                          int64_t layer_bytes, uint16_t* __restrict__ dx, int64_t lddx,
-                                                         int most, int nj, float* __restrict__ part)
+                                                         int nj, float* __restrict__ part)
 {
+    constexpr int BYTES = std::max(std::max(Grad<4>::LDS, Grad<2>::LDS), Grad<1>::LDS);
     ExpertRows rows;
-    int bj;
-    if (!expert_tile<64 * TA>(offsets, E, R, most, nj, rows, bj)) return;
+    int bj, cls;
+    if (!expert_tile<4>(offsets, E, R, nj, rows, bj, cls)) return;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
-    grad_tile<X, TA>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    if (cls == 0) grad_tile<X, 4, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    else if (cls == 1) grad_tile<X, 2, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    else grad_tile<X, 1, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
 }
 
 // The sum of `splits` partial results, in order, for the rows that some expert
@@ -189,9 +244,17 @@ __global__ __launch_bounds__(512, 4) void k_q4_experts_few(const uint16_t* __res
                                                            int64_t layer_bytes, uint16_t* __restrict__ y, int64_t ldy)
 {
     __shared__ __align__(16) char lds[kFewLds];
+    const ExpertLane lane(offsets, E, R);
+    const auto blocks = [](int c) { return (c + kFewRows - 1) / kFewRows; };
+    int sum = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum += blocks(lane.rows(u));
+    const int upto = lanes_upto(sum);
+    int k = blockIdx.y;
+    if (k >= __builtin_amdgcn_readlane(upto, 63)) return;
     ExpertRows rows;
-    const int want = blockIdx.y;
-    if (!expert_rows(offsets, E, R, kFewRows, [&](int) { return want; }, rows)) return;
+    expert_at(lane, lane_of(upto, sum, k), k, blocks, rows);
+    rows.t0 += k * kFewRows;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
     const int rt0 = 16 / WS * blockIdx.x, n = min(kFewRows, rows.t1 - rows.t0);
     if (n <= 4) few_rows_of<X, 1, 2, WS, HALF>(x, ldx, w, rt0, rows.t0, n, lds, y, ldy);
@@ -202,20 +265,51 @@ __global__ __launch_bounds__(512, 4) void k_q4_experts_few(const uint16_t* __res
 // --------------------------------------------------------------------- host
 
 struct ExpertsPlan {
-    bool few;
-    int TA, WR, splits;
-    int64_t most;      // blocks of rows that there can be
+    bool few, own;
+    int WR, splits;
+    int64_t tiles;     // of rows, that there can be
     int pieces;
     int64_t lds_, ldc;
     size_t copy, part, bytes;
 };
 
-// Blocks of `tokens` rows: at most, and about how many there will be.
-static int64_t blocks_most(int64_t R, int64_t E, int64_t tokens) { return R / tokens + std::min(R, E); }
-static int64_t blocks_about(int64_t R, int64_t E, int64_t tokens)
+// Blocks of at most `rows` rows that R rows of E experts can make.
+static int64_t blocks_most(int64_t R, int64_t E, int64_t rows) { return R / rows + std::min(R, E); }
+
+// A product's tiles: their rows (and halves and quarters of them), columns, and what
+// each takes in us for a depth of 4096, the chip full of them.
+struct ExpertShape {
+    int rows, cols;
+    double us[3];
+};
+
+// What a launch is expected to take with its depth shared out `splits` times, were the
+// rows dealt out evenly but for where they end in a block: the work over 256 CUs, and
+// two fifths of a tile for the CUs that finish last.
+static double experts_us(const ExpertShape& s, int64_t R, int64_t E, int64_t cols, int64_t depth, int splits)
 {
-    const int64_t some = std::min(R, E);
-    return std::max(some, R / tokens + some / 2);
+    const double some = (double)std::min(R, E), c = R / some, nc = (double)ceil_div(cols, s.cols);
+    double tile = s.us[0], us = c / s.rows * s.us[0] + 0.25 * (s.us[1] + s.us[2]);
+    if (c <= s.rows / 4) tile = us = s.us[2];
+    else if (c <= s.rows / 2) tile = us = s.us[1];
+    const double work = std::max(some * nc * us / 256 + 0.4 * tile / splits, tile / splits);
+    // and a launch that joins the parts, which go there and back at 4 TB/s
+    return work * depth / 4096 + (splits > 1 ? 2.0 + 8.0e-6 / 4 * splits * R * cols : 0.0);
+}
+
+// The least of it over shapes and splits, with `deepest` splits at most.
+template <int N>
+static int experts_choose(const ExpertShape (&shapes)[N], int64_t R, int64_t E, int64_t cols, int64_t depth, int64_t deepest,
+                          int& splits)
+{
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < N; ++i)
+        for (int s = 1; s == 1 || (s <= deepest && blocks_most(R, E, shapes[i].rows) * ceil_div(cols, shapes[i].cols) * s <= 2048); ++s) {
+            const double us = experts_us(shapes[i], R, E, cols, depth, s);
+            if (least == 0.0 || us < least) least = us, best = i, splits = s;
+        }
+    return best;
 }
 
 static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int gb)
@@ -223,14 +317,10 @@ static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int 
     ExpertsPlan p{};
     p.few = R <= kFewRows * E;
     if (p.few) return p;
-    // the linear layer's tiles and costs (q4_prompt.hip)
-    static constexpr TileShape shapes[] = {{256, 256, 128.0}, {128, 256, 80.0}, {128, 128, 42.0}, {64, 128, 28.0}};
-    const TileChoice c = tile_choose_of(shapes, [=](int tokens) { return blocks_about(R, E, tokens); }, R, m, n,
-                                        std::min<int64_t>(8, ceil_div(n, kQ4Cols) / 2));
-    p.TA = shapes[c.shape].tokens / 64;
-    p.WR = shapes[c.shape].cols / 64;
-    p.splits = c.splits;
-    p.most = blocks_most(R, E, shapes[c.shape].tokens);
+    static constexpr ExpertShape shapes[] = {{256, 256, {128.0, 80.0, 56.0}}, {128, 128, {42.0, 28.0, 28.0}}};
+    const ExpertShape& s = shapes[experts_choose(shapes, R, E, m, n, std::min<int64_t>(8, ceil_div(n, kQ4Cols) / 2), p.splits)];
+    p.WR = s.cols / 64;
+    p.tiles = blocks_most(R, E, s.rows);
     p.lds_ = ceil_div(R, 256) * 256 + 256;   // a block's sums are read as a whole, whichever row it begins at
     p.ldc = ceil_div(n, 64) * 64;
     p.pieces = piece_at((int)((n - 1) / 64), gb) + 1;
@@ -243,12 +333,9 @@ static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int 
 static ExpertsPlan experts_grad_plan(int64_t R, int64_t E, int64_t m, int64_t n)
 {
     ExpertsPlan p{};
-    static constexpr TileShape shapes[] = {{256, 256, 130.0}, {128, 256, 88.0}, {64, 256, 64.0}};   // as in q4_grad.hip
-    const TileChoice c = tile_choose_of(shapes, [=](int tokens) { return blocks_about(R, E, tokens); }, R, n, m,
-                                        std::min<int64_t>(16, ceil_div(m, 64) / 2));
-    p.TA = shapes[c.shape].tokens / 64;
-    p.splits = c.splits;
-    p.most = blocks_most(R, E, shapes[c.shape].tokens);
+    static constexpr ExpertShape shapes[] = {{256, 256, {130.0, 88.0, 64.0}}};   // as in q4_grad.hip
+    experts_choose(shapes, R, E, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2), p.splits);
+    p.tiles = blocks_most(R, E, 256);
     p.ldc = ceil_div(m, 64) * 64;
     p.part = align_up((size_t)R * p.ldc * 2);
     p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * R * n * 4) : 0);
@@ -283,13 +370,13 @@ static void experts_few(const ExpertsCall& c, const Q4Layer& w)
             (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout);
 }
 
-template <class X, int TA, int WR, bool OWN>
+template <class X, int WR, bool OWN>
 static void experts_launch(const ExpertsCall& c, const ExpertsPlan& p, const Q4Layer& w, const uint16_t* x, int64_t ldx)
 {
     const int nr = (int)ceil_div(w.m, 64 * WR);
-    enqueue(k_q4_experts<X, TA, WR, OWN>, dim3((unsigned)(p.most * nr), (unsigned)p.splits), dim3(128 * WR), c.s, x, ldx,
+    enqueue(k_q4_experts<X, WR, OWN>, dim3((unsigned)(p.tiles * nr), (unsigned)p.splits), dim3(128 * WR), c.s, x, ldx,
             (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, reinterpret_cast<const float*>(c.ws), p.lds_, c.out,
-            c.ldout, (int)p.most, nr, reinterpret_cast<float*>(c.ws + p.part));
+            c.ldout, nr, reinterpret_cast<float*>(c.ws + p.part));
 }
 
 template <class X>
@@ -306,29 +393,18 @@ static void experts_run(const ExpertsCall& c)
     }
     // (the staging offsets of a block of rows are 31 bits)
     const bool direct = w.n % 64 == 0 && c.ldin % 8 == 0 && c.ldin <= (1 << 21) && aligned16(c.in);
-    const bool own = p.TA == 1 && (direct || p.splits > 1);   // as in q4_prompt.hip
+    const bool own = p.WR == 2 && direct;
     const uint16_t* x = c.in;
     int64_t ldx = c.ldin;
     uint16_t* copy = reinterpret_cast<uint16_t*>(c.ws + p.copy);
     if (!own)
         enqueue(direct ? k_q4_sums<X, false> : k_q4_sums<X, true>, dim3((unsigned)ceil_div(c.rows, 4)), dim3(256), c.s, x, ldx,
                 (int)c.rows, w.n, w.gb, p.pieces, reinterpret_cast<float*>(c.ws), p.lds_, copy, p.ldc);
-    else if (!direct) copy_enqueue<X>(x, ldx, c.rows, w.n, copy, p.ldc, c.s);
     if (!direct) x = copy, ldx = p.ldc;
-    if (p.TA == 4) experts_launch<X, 4, 4, false>(c, p, w, x, ldx);
-    else if (p.TA == 2 && p.WR == 2) experts_launch<X, 2, 2, false>(c, p, w, x, ldx);
-    else if (p.TA == 2) experts_launch<X, 2, 4, false>(c, p, w, x, ldx);
-    else if (own) experts_launch<X, 1, 2, true>(c, p, w, x, ldx);
-    else experts_launch<X, 1, 2, false>(c, p, w, x, ldx);
+    if (p.WR == 4) experts_launch<X, 4, false>(c, p, w, x, ldx);
+    else if (own) experts_launch<X, 2, true>(c, p, w, x, ldx);
+    else experts_launch<X, 2, false>(c, p, w, x, ldx);
     if (p.splits > 1) experts_join<X>(c, reinterpret_cast<const float*>(c.ws + p.part), p.splits, w.m);
-}
-
-template <class X, int TA>
-static void experts_grad_launch(const ExpertsCall& c, const ExpertsPlan& p, const Q4Layer& w, const uint16_t* dy, int64_t lddy)
-{
-    const int nj = (int)ceil_div(w.n, 256);
-    enqueue(k_q4_experts_grad<X, TA>, dim3((unsigned)(p.most * nj), (unsigned)p.splits), dim3(512), c.s, dy, lddy, (int)c.rows,
-            c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, (int)p.most, nj, reinterpret_cast<float*>(c.ws + p.part));
 }
 
 template <class X>
@@ -343,9 +419,9 @@ static void experts_grad_run(const ExpertsCall& c)
         dy = reinterpret_cast<const uint16_t*>(c.ws);
         lddy = p.ldc;
     }
-    if (p.TA == 4) experts_grad_launch<X, 4>(c, p, w, dy, lddy);
-    else if (p.TA == 2) experts_grad_launch<X, 2>(c, p, w, dy, lddy);
-    else experts_grad_launch<X, 1>(c, p, w, dy, lddy);
+    const int nj = (int)ceil_div(w.n, 256);
+    enqueue(k_q4_experts_grad<X>, dim3((unsigned)(p.tiles * nj), (unsigned)p.splits), dim3(512), c.s, dy, lddy, (int)c.rows,
+            c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, nj, reinterpret_cast<float*>(c.ws + p.part));
     if (p.splits > 1) experts_join<X>(c, reinterpret_cast<const float*>(c.ws + p.part), p.splits, w.n);
 }
 

@@ -47,14 +47,15 @@ struct GradRaw {
 // blockIdx.y of gridDim.y shares the rows of W; more than one of them writes
 // float32 partial sums to part[blockIdx.y][token][column], part_rows tokens a part,
 // instead of dx.
-template <class X, int TA>
+template <class X, int TA, int BYTES = Grad<TA>::LDS>
 __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64_t lddy, int t0, int T,
                                           const Q4Layer& w, uint16_t* __restrict__ dx, int64_t lddx, int bj,
                                           float* __restrict__ part, int64_t part_rows)
 {
     typedef Grad<TA> P;
     typedef typename X::vec vec;
-    __shared__ __align__(16) char lds[P::LDS];
+    static_assert(BYTES >= P::LDS);
+    char(&lds)[BYTES] = tile_lds<BYTES>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, ml = lane & 31;
     const int wt = wave >> 2, wj = wave & 3;

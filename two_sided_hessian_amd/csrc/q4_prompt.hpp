@@ -190,7 +190,7 @@ __device__ __forceinline__ void zero_points(f32x16 (&acc)[TA][2], const float (&
 // OWN: the sums of x come from a product with ones.  blockIdx.y of gridDim.y
 // shares the columns; more than one of them writes float32 partial sums to
 // part[blockIdx.y][token][row], part_rows tokens a part, instead of y.
-template <class X, int TA, int WR, bool OWN>
+template <class X, int TA, int WR, bool OWN, int BYTES = Prompt<TA, WR>::LDS>
 __device__ __forceinline__ void prompt_tile(const uint16_t* __restrict__ x, int64_t ldx, int t0, int T,
                                             const Q4Layer& w, const float* __restrict__ sums, int64_t lds_,
                                             uint16_t* __restrict__ y, int64_t ldy, int br, float* __restrict__ part,
@@ -198,7 +198,8 @@ __device__ __forceinline__ void prompt_tile(const uint16_t* __restrict__ x, int6
 {
     typedef Prompt<TA, WR> P;
     typedef typename X::vec vec;
-    __shared__ __align__(16) char lds[P::LDS];
+    static_assert(BYTES >= P::LDS);
+    char(&lds)[BYTES] = tile_lds<BYTES>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, ml = lane & 31;
     const int wt = wave / WR, wr = wave % WR;

@@ -9,6 +9,11 @@ namespace bk {
 
 constexpr int kStoreBytes = 32 * 72 * 2;   // LDS of a wave in tile_store
 
+// The LDS of a workgroup whose tile bodies need BYTES at most: one array,
+// however many bodies a kernel chooses from.
+template <int BYTES>
+__shared__ __align__(16) char tile_lds[BYTES];
+
 // Waits until at most `left` loads of this wave are in flight (they complete
 // in order), then for the other waves.
 template <int LEFT>
@@ -20,9 +25,9 @@ __device__ __forceinline__ void tile_wait()
 // Workgroups are dealt to the eight XCDs round-robin; each XCD gets a
 // contiguous run of the tile order below, so that its L2 sees few tokens and
 // rows at a time: runs of 4 token blocks share their rows of W.
-__device__ __forceinline__ void tile_of(int nt, int nr, int& bt, int& br)
+__device__ __forceinline__ void tile_at(unsigned b, int nt, int nr, int& bt, int& br)
 {
-    const unsigned total = (unsigned)nt * nr, b = blockIdx.x;
+    const unsigned total = (unsigned)nt * nr;
     const unsigned per = total / 8, rest = total % 8, xcd = b % 8;
     const unsigned p = xcd * per + min(xcd, rest) + b / 8;
     const unsigned band = 4u * nr, g = p / band;
@@ -30,6 +35,7 @@ __device__ __forceinline__ void tile_of(int nt, int nr, int& bt, int& br)
     bt = (int)(4 * g + (p - g * band) % h);
     br = (int)((p - g * band) / h);
 }
+__device__ __forceinline__ void tile_of(int nt, int nr, int& bt, int& br) { tile_at(blockIdx.x, nt, nr, bt, br); }
 
 // Results through LDS, 32 tokens x 64 columns of a wave at a time, so that
 // they leave as 16-byte stores (to any address); cut rows leave one by one.  acc:
