@@ -1,19 +1,23 @@
 """Build libbakron.so in-tree with hipcc for gfx950.
 
 Each .hip file under csrc/ is compiled separately (in parallel) into
-_build/ and linked into two_sided_hessian_amd/libbakron.so.
+_build/ and linked into two_sided_hessian_amd/libbakron.so.  fast_calls.cpp
+becomes two_sided_hessian_amd/_fast.so beside it, a Python module that calls
+the library (host code only, torch's headers).
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libbakron.so")
+FAST = os.path.join(HERE, "_fast.so")
 SOURCES = ["factor.hip", "solve.hip", "gptq.hip", "kfac.hip", "antidiag.hip", "capi.hip", "noalloc.hip",
            "q4.hip", "q4_prompt.hip", "q4_grad.hip", "q4_moe.hip", "q4_experts.hip",
            "moe_route.hip", "moe_rows.hip", "moe_gated.hip"]
@@ -30,9 +34,23 @@ FLAGS = [
 ]
 
 
+def fast_command(out: str) -> list:
+    """The compiler's command line for fast_calls.cpp."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_path("include"), os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), "/opt/rocm/include"]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{p}" for p in include), os.path.join(CSRC, "fast_calls.cpp"), "-o", out, "-L" + os.path.join(root, "lib"),
+            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     procs = []
+    fast = FAST + ".tmp%d" % os.getpid()
+    procs.append(("fast_calls.cpp", subprocess.Popen(fast_command(fast), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     objs = []
     for s in SOURCES:
         obj = os.path.join(BUILD, s.replace(".hip", ".o"))
@@ -55,6 +73,7 @@ def build(verbose: bool = False) -> str:
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    os.replace(fast, FAST)
     return LIB
 
 

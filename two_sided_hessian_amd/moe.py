@@ -4,7 +4,10 @@ order, rows there and back, the experts' products, their inner activation with
 8-bit checkpoints, and the whole layer.
 
 Arguments are checked as in q4.py: no tensor is looked into, every arithmetic
-step runs in the library's HIP kernels, and there is no fallback.
+step runs in the library's HIP kernels, and there is no fallback.  Calls whose
+outputs are given (decoding steps, captured or not) are tried by _fast first,
+which checks and enqueues them in native code (csrc/fast_calls.cpp) and leaves
+everything else, refusals among it, to the code here.
 
 Autograd: moe_route (weights), moe_gather, moe_combine, q4_experts, gated_act
 and q4_moe_layer take part in it where an input requires a gradient and ``out``
@@ -52,6 +55,34 @@ _b.SIGNATURES.update({
 _TYPES = dict(_q._TYPES)
 _TYPES3 = _TYPES | {torch.float32: BAKRON_MOE_F32}
 _ACTS = {"silu": BAKRON_MOE_SILU, "gelu": BAKRON_MOE_GELU}
+
+
+try:
+    from . import _fast
+except ImportError:                      # not built: the same calls through ctypes, 3 us more each on the host
+    _fast = None
+
+
+def _not_here(*_):
+    return False
+
+
+def _native(name):
+    return getattr(_fast, name, _not_here)
+
+
+_route_at, _route_grad_at, _gather_at, _combine_at, _combine_grad_at, _experts_at, _experts_grad_at, _pack_at, _gated_at, \
+    _gated_grad_at = map(_native, ("route", "route_grad", "gather", "combine", "combine_grad", "experts", "experts_grad", "pack",
+                                   "gated", "gated_grad"))
+_ready = _fast is None
+
+
+def _get_ready():
+    """The library's functions for _fast, which declines every call until then."""
+    global _ready
+    _b.lib()
+    _fast.load(_b.LIB_PATH, Q4Weight, Checkpoint8)
+    _ready = True
 
 
 def _type_of(name, dtype):
@@ -107,6 +138,8 @@ def _stream_of(index, stream):
 
 def _run(call, *args):
     rc = _calls[call](*args)
+    if not _ready:
+        _get_ready()
     if rc:
         _check(rc, call)
 
@@ -167,6 +200,8 @@ def moe_route(logits, top_k, *, out=None, ws=None, stream=None):
     experts + 1).  ``out``: a dict of the five to write to; ``ws``: a workspace of
     moe_route_workspace_bytes.  Autograd: the weights' gradient is taken with
     moe_route_grad."""
+    if out is not None and stream is None and _route_at(logits, top_k, out, ws):
+        return out
     ld = _matrix("logits", logits)
     T, E = logits.shape
     k, index = _top_k(top_k), logits.get_device()
@@ -196,6 +231,8 @@ def moe_route_grad(dweights, weights, ids, experts, *, dtype=torch.float32, out=
     """bakron_moe_route_grad: the gradient of moe_route's weights with respect to
     the logits, tokens x experts of ``dtype`` (or of out's), zero where an expert
     was not chosen."""
+    if out is not None and stream is None and _route_grad_at(dweights, weights, ids, experts, out):
+        return out
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda or ids.dim() != 2:
         raise TypeError("ids must be a CUDA (HIP) tensor, tokens x top_k")
     (T, k), index, E = ids.shape, ids.get_device(), int(experts)
@@ -246,6 +283,8 @@ def moe_gather(x, place, *, out=None, stream=None):
     (moe_route).  Returns tokens * top_k x columns; ``out``: where to write it (any
     number of rows).  Rows that no choice has stay as they are (in a new result:
     undefined).  Autograd: its gradient is moe_combine without weights."""
+    if out is not None and stream is None and _gather_at(x, place, out):
+        return out
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a CUDA (HIP) tensor, tokens x columns")
     n = x.shape[1]
@@ -318,6 +357,8 @@ def moe_combine(ys, place, weights=None, *, out=None, stream=None):
     nothing).  ys: rows x columns in bfloat16 or float16; weights: float32 tokens x
     top_k.  ``out``: where to write y.  Autograd: the gradients are those of
     moe_combine_grad (without weights: moe_gather)."""
+    if out is not None and stream is None and _combine_at(ys, place, weights, out):
+        return out
     if not isinstance(ys, torch.Tensor) or ys.dim() != 2:
         raise TypeError("ys must be a CUDA (HIP) tensor, rows x columns")
     rows, n = ys.shape
@@ -344,6 +385,8 @@ def moe_combine_grad(dy, ys, place, weights, *, out=None, stream=None):
     dys[place[t, j]] = weights[t, j] dy[t] and dweights[t, j] = dy[t] . ys[place[t, j]].
     ``out``: a dict of the two to write to.  Rows of dys that no choice has stay as
     they are (in a new result: undefined)."""
+    if out is not None and stream is None and _combine_grad_at(dy, ys, place, weights, out):
+        return out
     if not isinstance(ys, torch.Tensor) or ys.dim() != 2:
         raise TypeError("ys must be a CUDA (HIP) tensor, rows x columns")
     rows, n = ys.shape
@@ -431,6 +474,8 @@ def q4_experts(x, w, offsets, *, out=None, ws=None, stream=None):
     device (moe_route).  Rows from offsets[-1] on stay as they are (in a new
     result: undefined).  ``ws``: a workspace of q4_experts_workspace_bytes.
     Autograd: with respect to x, by q4_experts_grad."""
+    if out is not None and stream is None and _experts_at(x, w, offsets, out, ws):
+        return out
     return _experts("bakron_q4_experts", q4_experts_workspace_bytes, "x", x, w, offsets, out, ws, stream)
 
 
@@ -438,6 +483,8 @@ def q4_experts_grad(dy, w, offsets, *, out=None, ws=None, stream=None):
     """bakron_q4_experts_grad: dx[p] = dy[p] W_e, the gradient of q4_experts with
     respect to x.  ``out``, ``ws`` (q4_experts_grad_workspace_bytes) and autograd: as
     there."""
+    if out is not None and stream is None and _experts_grad_at(dy, w, offsets, out, ws):
+        return out
     return _experts("bakron_q4_experts_grad", q4_experts_grad_workspace_bytes, "dy", dy, w, offsets, out, ws, stream)
 
 
@@ -483,6 +530,8 @@ def _checkpoint(name, ck, rows, cols, dtype, index):
 def ck8_pack(x, *, out=None, stream=None):
     """bakron_ck8_pack: the 8-bit checkpoint of a matrix in bfloat16 or float16
     (rows contiguous).  ``out``: a Checkpoint8 of its size and type to write to."""
+    if out is not None and stream is None and _pack_at(x, out):
+        return out
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a CUDA (HIP) tensor, rows x columns")
     rows, n = x.shape
@@ -556,6 +605,8 @@ def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, strea
     int32 of one element on the device, rows from it on are left as they are
     (moe_route's offsets[-1:]).  ``out``: where to write h.  Autograd keeps a and b as
     checkpoints: the gradient is gated_act_grad's."""
+    if out is not None and stream is None and _gated_at(a, b, _ACTS.get(act, -1), checkpoint or None, count, out):
+        return (out, *checkpoint) if checkpoint else out
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise TypeError("a must be a CUDA (HIP) tensor, rows x columns")
     rows, n = a.shape
@@ -590,6 +641,8 @@ def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, strea
 def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=None):
     """bakron_gated_act_grad: (da, db), the gradients of gated_act from the
     checkpoints of a and b.  ``out``: a pair to write to; ``count``: as there."""
+    if out is not None and stream is None and _gated_grad_at(dh, ck_a, ck_b, _ACTS.get(act, -1), count, *out):
+        return tuple(out)
     if not isinstance(dh, torch.Tensor) or dh.dim() != 2:
         raise TypeError("dh must be a CUDA (HIP) tensor, rows x columns")
     rows, n = dh.shape
