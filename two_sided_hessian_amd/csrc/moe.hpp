@@ -81,6 +81,41 @@ __device__ __forceinline__ u32x4 down8(const float (&f)[8])
     return u32x4{X::down2(f[0], f[1]), X::down2(f[2], f[3]), X::down2(f[4], f[5]), X::down2(f[6], f[7])};
 }
 
+// Rows of 8-column units over threads: 2^log lanes a run of a row's units, a row's
+// runs (`chunks` of them) in workgroups beside each other, so that what is in flight
+// lies together in memory.
+struct UnitAt {
+    int64_t r, by;   // the first row and the step to the next
+    int u;
+    __device__ __forceinline__ UnitAt(int log, int chunks)
+    {
+        const unsigned chunk = blockIdx.x % chunks, group = blockIdx.x / chunks;
+        r = ((int64_t)group << (8 - log)) + (threadIdx.x >> log);
+        by = (int64_t)(gridDim.x / chunks) << (8 - log);
+        u = (int)(threadIdx.x & ((1u << log) - 1)) + (int)(chunk << log);
+    }
+};
+constexpr int64_t kUnitBlocks = 1 << 22;   // of a launch; more rows are taken in turn
+struct UnitGrid {
+    int log, chunks;
+    unsigned blocks;   // of 256 threads, a multiple of chunks
+};
+// As many lanes a run as leave one in 16 idle at most: 256 where they fit (16384 x
+// 14336, forward with checkpoints and backward: 322 + 319 us with 256 lanes, 334 + 314
+// with 64; with a workgroup's four rows below each other and runs of rows as the faster
+// index 407 + 400).
+inline UnitGrid unit_grid(int64_t rows, int64_t units, int least)
+{
+    UnitGrid g;
+    g.log = least;
+    while (g.log < 6 && (1 << g.log) < units) ++g.log;
+    for (int log = 8; log > 6; --log)
+        if (g.log == 6 && (ceil_div(units, 1 << log) << log) - units <= units / 16) g.log = log;
+    g.chunks = (int)ceil_div(units, 1 << g.log);
+    g.blocks = (unsigned)(std::min(kUnitBlocks / g.chunks, ceil_div(rows, 256 >> g.log)) * g.chunks);
+    return g;
+}
+
 // Layer e of a stack
 __device__ __forceinline__ Q4Layer expert_layer(Q4Layer w, int e, int64_t layer_bytes)
 {

@@ -77,17 +77,6 @@ __device__ __forceinline__ void ck8_values(u32x2 c, uint32_t step, float (&f)[8]
         for (int e = 0; e < 4; ++e) f[4 * i + e] = (float)(int8_t)(c[i] >> 8 * e) * s;
 }
 
-// Rows and units of a thread, as in moe_rows.hip: 2^log lanes a run of units.
-struct GatedAt {
-    int64_t r, by;
-    int u;
-    __device__ __forceinline__ GatedAt(int log)
-        : r(((int64_t)blockIdx.x * 256 + threadIdx.x) >> log), by((int64_t)gridDim.x * 256 >> log),
-          u((int)(threadIdx.x & ((1u << log) - 1)) + ((int)blockIdx.y << log))
-    {
-    }
-};
-
 __device__ __forceinline__ int64_t rows_of(int64_t rows, const int32_t* __restrict__ count)
 {
     return count ? min(rows, (int64_t)max(*count, 0)) : rows;
@@ -103,9 +92,9 @@ __device__ __forceinline__ void ck8_store(const Ck8& ck, int64_t row, int units,
 
 template <class X>
 __global__ __launch_bounds__(256) void k_ck8_pack(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows, int n, int units,
-                                                  int log, Ck8 ck)
+                                                  int log, int chunks, Ck8 ck)
 {
-    const GatedAt at(log);
+    const UnitAt at(log, chunks);
     if (at.u >= units) return;
     for (int64_t r = at.r; r < rows; r += at.by) {
         u32x4 v = {0u, 0u, 0u, 0u};
@@ -117,10 +106,10 @@ __global__ __launch_bounds__(256) void k_ck8_pack(const uint16_t* __restrict__ x
 }
 
 template <class X>
-__global__ __launch_bounds__(256) void k_ck8_unpack(Ck8 ck, int64_t rows, int n, int units, int log,
+__global__ __launch_bounds__(256) void k_ck8_unpack(Ck8 ck, int64_t rows, int n, int units, int log, int chunks,
                                                     typename RawOf<X>::type* __restrict__ x, int64_t ldx)
 {
-    const GatedAt at(log);
+    const UnitAt at(log, chunks);
     if (8 * at.u >= n) return;
     for (int64_t r = at.r; r < rows; r += at.by) {
         float f[8];
@@ -161,11 +150,11 @@ __device__ __forceinline__ float gate_p(float v, float& dt)
 
 template <class X, bool GELU, bool KEEP>
 __global__ __launch_bounds__(256) void k_gated_act(const uint16_t* __restrict__ a, int64_t lda, const uint16_t* __restrict__ b,
-                                                   int64_t ldb, int64_t rows, int n, int units, int log,
+                                                   int64_t ldb, int64_t rows, int n, int units, int log, int chunks,
                                                    const int32_t* __restrict__ count, uint16_t* __restrict__ h, int64_t ldh,
                                                    Ck8 cka, Ck8 ckb)
 {
-    const GatedAt at(log);
+    const UnitAt at(log, chunks);
     const int c = 8 * at.u;
     if (at.u >= units) return;
     rows = rows_of(rows, count);
@@ -190,11 +179,11 @@ __global__ __launch_bounds__(256) void k_gated_act(const uint16_t* __restrict__ 
 
 template <class X, bool GELU>
 __global__ __launch_bounds__(256) void k_gated_grad(const uint16_t* __restrict__ dh, int64_t lddh, Ck8 cka, Ck8 ckb,
-                                                    int64_t rows, int n, int units, int log,
+                                                    int64_t rows, int n, int units, int log, int chunks,
                                                     const int32_t* __restrict__ count, uint16_t* __restrict__ da, int64_t ldda,
                                                     uint16_t* __restrict__ db, int64_t lddb)
 {
-    const GatedAt at(log);
+    const UnitAt at(log, chunks);
     const int c = 8 * at.u;
     if (c >= n) return;
     rows = rows_of(rows, count);
@@ -222,18 +211,13 @@ __global__ __launch_bounds__(256) void k_gated_grad(const uint16_t* __restrict__
 // --------------------------------------------------------------------- host
 
 struct GatedGrid {
-    int units, log;
-    dim3 grid;
+    int units;
+    UnitGrid at;
 };
 static GatedGrid gated_grid(int64_t rows, int64_t cols)
 {
-    GatedGrid g;
-    g.units = (int)ceil_div(cols, kCkBlock) * 4;
-    g.log = 2;
-    while (g.log < 6 && (1 << g.log) < g.units) ++g.log;
-    g.grid = dim3((unsigned)std::min<int64_t>(1 << 20, ceil_div(rows << g.log, 256)),
-                  (unsigned)ceil_div(g.units, 1 << g.log));
-    return g;
+    const int units = (int)ceil_div(cols, kCkBlock) * 4;
+    return {units, unit_grid(rows, units, 2)};
 }
 
 static bool gated_size_ok(int64_t rows, int64_t cols)
@@ -248,8 +232,8 @@ static void gated_enqueue(const void* a, int64_t lda, const void* b, int64_t ldb
     const GatedGrid g = gated_grid(rows, cols);
     auto* kernel = gelu ? (ck_a ? k_gated_act<X, true, true> : k_gated_act<X, true, false>)
                         : (ck_a ? k_gated_act<X, false, true> : k_gated_act<X, false, false>);
-    enqueue(kernel, g.grid, dim3(256), s, static_cast<const uint16_t*>(a), lda, static_cast<const uint16_t*>(b), ldb, rows,
-            (int)cols, g.units, g.log, count, static_cast<uint16_t*>(h), ldh, ck8_of(ck_a, rows, cols),
+    enqueue(kernel, dim3(g.at.blocks), dim3(256), s, static_cast<const uint16_t*>(a), lda, static_cast<const uint16_t*>(b), ldb, rows,
+            (int)cols, g.units, g.at.log, g.at.chunks, count, static_cast<uint16_t*>(h), ldh, ck8_of(ck_a, rows, cols),
             ck8_of(ck_b, rows, cols));
 }
 
@@ -258,16 +242,16 @@ static void gated_grad_enqueue(const void* dh, int64_t lddh, const void* ck_a, c
                                bool gelu, const int32_t* count, void* da, int64_t ldda, void* db, int64_t lddb, hipStream_t s)
 {
     const GatedGrid g = gated_grid(rows, cols);
-    enqueue(gelu ? k_gated_grad<X, true> : k_gated_grad<X, false>, g.grid, dim3(256), s, static_cast<const uint16_t*>(dh),
+    enqueue(gelu ? k_gated_grad<X, true> : k_gated_grad<X, false>, dim3(g.at.blocks), dim3(256), s, static_cast<const uint16_t*>(dh),
             lddh, ck8_of(const_cast<void*>(ck_a), rows, cols), ck8_of(const_cast<void*>(ck_b), rows, cols), rows, (int)cols,
-            g.units, g.log, count, static_cast<uint16_t*>(da), ldda, static_cast<uint16_t*>(db), lddb);
+            g.units, g.at.log, g.at.chunks, count, static_cast<uint16_t*>(da), ldda, static_cast<uint16_t*>(db), lddb);
 }
 
 template <class X>
 static void unpack_enqueue(const void* ck, int64_t rows, int64_t cols, void* x, int64_t ldx, hipStream_t s)
 {
     const GatedGrid g = gated_grid(rows, cols);
-    enqueue(k_ck8_unpack<X>, g.grid, dim3(256), s, ck8_of(const_cast<void*>(ck), rows, cols), rows, (int)cols, g.units, g.log,
+    enqueue(k_ck8_unpack<X>, dim3(g.at.blocks), dim3(256), s, ck8_of(const_cast<void*>(ck), rows, cols), rows, (int)cols, g.units, g.at.log, g.at.chunks,
             static_cast<typename RawOf<X>::type*>(x), ldx);
 }
 
@@ -290,8 +274,8 @@ int bakron_ck8_pack(const void* x, int64_t ldx, int64_t rows, int32_t type, int6
     if (!x || !ck) return BAKRON_ERR_NULL_POINTER;
     if (!bk::moe_at(x, 2) || !bk::moe_at(ck, bk::kAlign)) return BAKRON_ERR_BAD_ARG;
     const bk::GatedGrid g = bk::gated_grid(rows, cols);
-    bk::enqueue(type == BAKRON_Q4_BF16 ? bk::k_ck8_pack<bk::Bf16> : bk::k_ck8_pack<bk::Fp16>, g.grid, dim3(256), stream,
-                static_cast<const uint16_t*>(x), ldx, rows, (int)cols, g.units, g.log, bk::ck8_of(ck, rows, cols));
+    bk::enqueue(type == BAKRON_Q4_BF16 ? bk::k_ck8_pack<bk::Bf16> : bk::k_ck8_pack<bk::Fp16>, dim3(g.at.blocks), dim3(256), stream,
+                static_cast<const uint16_t*>(x), ldx, rows, (int)cols, g.units, g.at.log, g.at.chunks, bk::ck8_of(ck, rows, cols));
     return bk::moe_done();
 }
 

@@ -11,12 +11,14 @@
 // a choice per thread; its place among the workgroup's choices of that expert
 // is a count of equal keys below it: in the wave by comparing the bits of all
 // keys at once (a ballot per bit), over the waves by a table in LDS.  That
-// order does not depend on timing.  One workgroup does all of a few tokens; more
+// order does not depend on timing.  One workgroup does all of up to 64 tokens; more
 // write their counts, and k_moe_place adds, for every choice, the counts of the
 // experts and workgroups before it.
 //
 // Latency bounds it: a launch and its round trips, twice where there is more
-// than one workgroup.
+// than one workgroup.  One token, 2 of 8: 3.2 us; 16 tokens, 6 of 64: 4.1; 64: 5.4; 256:
+// 8.6; 8192: 10.4; 16384, 8 of 128: 14.2.  (One workgroup for 256 tokens, a pass after
+// the other: 16.6.)
 #include <algorithm>
 
 #include "moe.hpp"
@@ -25,8 +27,7 @@ namespace bk {
 
 constexpr int kRouteTokens = 64;   // tokens of a workgroup's pass: 16 lanes each
 constexpr int kRouteWaves = 16;
-constexpr int kRouteBlocks = 128;  // workgroups at most
-constexpr int kRouteAlone = 256;   // up to so many tokens one workgroup does all
+constexpr int kRouteBlocks = 256;  // workgroups at most (16384 tokens, 8 of 128: 14.2 us, with 128 18.8)
 constexpr int kRouteKeys = BAKRON_MOE_MAX_EXPERTS + 1;
 static_assert(kRouteTokens * BAKRON_MOE_MAX_TOP_K == 64 * kRouteWaves, "a choice per thread");
 
@@ -67,8 +68,8 @@ __device__ __forceinline__ void route_scan(int* v, int n)
 }
 
 // Workgroup b: tokens [b per, min((b + 1) per, T)), per a multiple of 64 where
-// there is more than one.  A lone workgroup (counts null) finishes place, order
-// and offsets; otherwise place gets a choice's place among the workgroup's of its
+// there is more than one.  A lone workgroup (counts null, 64 tokens at most) finishes
+// place, order and offsets; otherwise place gets a choice's place among the workgroup's of its
 // expert, and counts[b][0 .. E] how many there are.
 template <class L, int NV>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(const typename RawOf<L>::type* __restrict__ logits, int64_t ld,
@@ -134,35 +135,30 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(const typename R
         if (on && rank == 0) table[wave][key] = __popcll(same);
         __syncthreads();
         if (tid <= E) {
-            int s = hist[tid];
+            int c[kRouteWaves], s = hist[tid];
 #pragma unroll
-            for (int w = 0; w < kRouteWaves; ++w) {
-                const int c = table[w][tid];
-                table[w][tid] = s;
-                s += c;
-            }
+            for (int w = 0; w < kRouteWaves; ++w) c[w] = table[w][tid];
+#pragma unroll
+            for (int w = 0; w < kRouteWaves; ++w) table[w][tid] = s, s += c[w];
             hist[tid] = s;
         }
         __syncthreads();
-        if (on) place[(int64_t)t0 * k + tid] = table[wave][key] + rank;
-        __syncthreads();   // the next pass clears the table and writes key_of
+        if (counts) {
+            if (on) place[(int64_t)t0 * k + tid] = table[wave][key] + rank;
+            __syncthreads();   // the next pass clears the table and writes key_of
+            continue;
+        }
+        // alone, and this was the only pass
+        route_scan(hist, E + 1);
+        __syncthreads();
+        if (tid <= E) offsets[tid] = hist[tid];
+        if (on) {
+            const int at = hist[key] + table[wave][key] + rank;
+            order[at] = key < E ? tid : -1;
+            place[tid] = key < E ? at : -1;
+        }
     }
-    if (counts) {
-        if (tid < pitch) counts[(int64_t)blockIdx.x * pitch + tid] = tid <= E ? hist[tid] : 0;
-        return;
-    }
-    __syncthreads();
-    route_scan(hist, E + 1);
-    __syncthreads();
-    if (tid <= E) offsets[tid] = hist[tid];
-    for (int t0 = first; t0 < last; t0 += kRouteTokens) {
-        const int p = t0 * k + tid;
-        if (tid >= min(kRouteTokens, last - t0) * k) break;
-        const int id = ids[p], e = id < 0 ? E : id;   // (this thread's own writes, or a wave's before a barrier)
-        const int at = hist[e] + place[p];
-        order[at] = id < 0 ? -1 : p;
-        place[p] = id < 0 ? -1 : at;
-    }
+    if (counts && tid < pitch) counts[(int64_t)blockIdx.x * pitch + tid] = tid <= E ? hist[tid] : 0;
 }
 
 // The same workgroups again: counts before, four keys (a 16-byte load) per thread
@@ -178,6 +174,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_place(const int32_t* _
     __shared__ int base[kRouteKeys + 3], start[kRouteKeys + 3];
     const int tid = threadIdx.x, quads = pitch / 4, groups = N / quads;
     const int q = tid % quads, g = tid / quads, me = blockIdx.x;
+    const int first = me * per * k, last = (int)min((int64_t)T, (int64_t)(me + 1) * per) * k;
+    int p = first + tid, id = -1, local = 0;   // the first choice, read beside the counts
+    if (p < last) id = ids[p], local = place[p];
     i32x4 b = {0, 0, 0, 0}, a = {0, 0, 0, 0};
     if (g < groups) {
 #pragma unroll 8
@@ -190,8 +189,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_place(const int32_t* _
         total[tid] = a;
     }
     __syncthreads();
-    if (tid < pitch && tid <= E) {
+    if (tid <= E) {
         int s = 0, t = 0;
+#pragma unroll 8
         for (int i = 0; i < groups; ++i) {
             s += reinterpret_cast<const int*>(before)[i * pitch + tid];
             t += reinterpret_cast<const int*>(total)[i * pitch + tid];
@@ -203,12 +203,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_place(const int32_t* _
     route_scan(start, E + 1);
     __syncthreads();
     if (me == 0 && tid <= E) offsets[tid] = start[tid];
-    const int first = me * per * k, last = (int)min((int64_t)T, (int64_t)(me + 1) * per) * k;
-    for (int p = first + tid; p < last; p += N) {
-        const int id = ids[p], e = id < 0 ? E : id;
-        const int at = start[e] + base[e] + place[p];
+    while (p < last) {
+        const int e = id < 0 ? E : id, at = start[e] + base[e] + local;
         order[at] = id < 0 ? -1 : p;
         place[p] = id < 0 ? -1 : at;
+        p += N;
+        if (p < last) id = ids[p], local = place[p];
     }
 }
 
@@ -251,11 +251,6 @@ static RoutePlan route_plan(int64_t T, int64_t E)
 {
     RoutePlan p;
     p.pitch = (int)ceil_div(E + 1, 4) * 4;
-    if (T <= kRouteAlone) {
-        p.blocks = 1;
-        p.per = (int)T;
-        return p;
-    }
     const int64_t passes = ceil_div(T, kRouteTokens);
     p.per = (int)ceil_div(passes, kRouteBlocks) * kRouteTokens;
     p.blocks = (int)ceil_div(T, p.per);

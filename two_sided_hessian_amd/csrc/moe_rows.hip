@@ -7,9 +7,7 @@
 //
 // HBM bounds all three, so every row is moved once: the work is laid out by
 // token, whose row (x, y or dy) is in registers while its top_k sorted rows are
-// written or read, every load of a lane before its first use.  A lane has 8
-// columns (16 bytes); 2^LOG lanes, a whole wave where the row is long enough, a
-// token's run of columns.  A place outside [0, rows) is no row: loads go to row 0
+// written or read, every load of a lane before its first use.  A place outside [0, rows) is no row: loads go to row 0
 // then, whose value is not used, so that they stay in one run.
 #include <algorithm>
 
@@ -19,28 +17,17 @@ namespace bk {
 
 constexpr int kRowsTopK = BAKRON_MOE_MAX_PLACES;
 
-// Tokens and columns of a thread: blockIdx.y counts runs of 8 << log columns.
-struct RowsAt {
-    int64_t t, by;   // the first token and the step to the next
-    int c;
-    __device__ __forceinline__ RowsAt(int log)
-        : t(((int64_t)blockIdx.x * 256 + threadIdx.x) >> log), by((int64_t)gridDim.x * 256 >> log),
-          c(8 * ((int)(threadIdx.x & ((1u << log) - 1)) + ((int)blockIdx.y << log)))
-    {
-    }
-};
-
 __global__ __launch_bounds__(256) void k_moe_gather(const uint16_t* __restrict__ x, int64_t ldx, int T, int n, int k,
                                                     const int32_t* __restrict__ place, uint16_t* __restrict__ xs,
-                                                    int64_t ldxs, int rows, int log)
+                                                    int64_t ldxs, int rows, int log, int chunks)
 {
-    const RowsAt at(log);
-    if (at.c >= n) return;
-    for (int64_t t = at.t; t < T; t += at.by) {
-        const u32x4 v = load8(x + t * ldx, at.c, n);
+    const UnitAt at(log, chunks);
+    if (8 * at.u >= n) return;
+    for (int64_t t = at.r; t < T; t += at.by) {
+        const u32x4 v = load8(x + t * ldx, 8 * at.u, n);
         for (int j = 0; j < k; ++j) {
             const int p = place[t * k + j];
-            if ((unsigned)p < (unsigned)rows) store8(xs + (int64_t)p * ldxs, at.c, n, v);
+            if ((unsigned)p < (unsigned)rows) store8(xs + (int64_t)p * ldxs, 8 * at.u, n, v);
         }
     }
 }
@@ -50,11 +37,11 @@ template <class X, int K, bool W>
 __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t* __restrict__ ys, int64_t ldys, int rows, int T, int n,
                                                      int k, const int32_t* __restrict__ place,
                                                      const float* __restrict__ weights, uint16_t* __restrict__ y,
-                                                     int64_t ldy, int log)
+                                                     int64_t ldy, int log, int chunks)
 {
-    const RowsAt at(log);
-    if (at.c >= n) return;
-    for (int64_t t = at.t; t < T; t += at.by) {
+    const UnitAt at(log, chunks);
+    if (8 * at.u >= n) return;
+    for (int64_t t = at.r; t < T; t += at.by) {
         u32x4 v[K];
         float w[K];
         bool on[K];
@@ -64,7 +51,7 @@ __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t* __restrict_
             const int p = place[c];
             on[j] = j < k && (unsigned)p < (unsigned)rows;
             w[j] = W ? weights[c] : 1.f;
-            v[j] = load8(ys + (int64_t)(on[j] ? p : 0) * ldys, at.c, n);
+            v[j] = load8(ys + (int64_t)(on[j] ? p : 0) * ldys, 8 * at.u, n);
         }
         float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -74,7 +61,7 @@ __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t* __restrict_
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] = on[j] ? (W ? fmaf(w[j], f[e], sum[e]) : sum[e] + f[e]) : sum[e];
         }
-        store8(y + t * ldy, at.c, n, down8<X>(sum));
+        store8(y + t * ldy, 8 * at.u, n, down8<X>(sum));
     }
 }
 
@@ -152,28 +139,14 @@ __global__ __launch_bounds__(256) void k_moe_zero(float* __restrict__ v, int64_t
 
 // --------------------------------------------------------------------- host
 
-constexpr int64_t kRowsBlocks = 1 << 20;   // of a launch; more work is taken in turn
-
-struct RowsGrid {
-    int log;
-    dim3 grid;
-};
-static RowsGrid rows_grid(int64_t T, int64_t n)
-{
-    const int64_t units = ceil_div(n, 8);
-    int log = 0;
-    while (log < 6 && (1 << log) < units) ++log;
-    return {log, dim3((unsigned)std::min(kRowsBlocks, ceil_div(T << log, 256)), (unsigned)ceil_div(units, 1 << log))};
-}
-
 template <class X, int K>
 static void combine_enqueue(const void* ys, int64_t ldys, int64_t rows, int64_t n, int k, const int32_t* place,
                             const float* weights, int64_t T, void* y, int64_t ldy, hipStream_t s)
 {
-    const RowsGrid g = rows_grid(T, n);
-    enqueue(weights ? k_moe_combine<X, K, true> : k_moe_combine<X, K, false>, g.grid, dim3(256), s,
+    const UnitGrid g = unit_grid(T, ceil_div(n, 8), 0);
+    enqueue(weights ? k_moe_combine<X, K, true> : k_moe_combine<X, K, false>, dim3(g.blocks), dim3(256), s,
             static_cast<const uint16_t*>(ys), ldys, (int)rows, (int)T, (int)n, k, place, weights,
-            static_cast<uint16_t*>(y), ldy, g.log);
+            static_cast<uint16_t*>(y), ldy, g.log, g.chunks);
 }
 
 template <class X, int K>
@@ -181,9 +154,12 @@ static void combine_grad_enqueue(const void* dy, int64_t lddy, const void* ys, i
                                  const int32_t* place, const float* weights, int64_t T, void* dys, int64_t lddys,
                                  float* dweights, hipStream_t s)
 {
-    const bool few = T < 4096 && n > 512;   // a wave per token would leave CUs idle
-    enqueue(few ? k_moe_combine_grad<X, K, 4> : k_moe_combine_grad<X, K, 1>,
-            dim3((unsigned)std::min(kRowsBlocks, few ? T : ceil_div(T, 4))), dim3(256), s,
+    // Four waves share a token wherever a wave's 512 columns do not take a row whole:
+    // what is in flight lies together (8192 tokens of 2 x 4096: 65 us, and 79 with a wave
+    // per token).
+    const bool wide = n > 512;
+    enqueue(wide ? k_moe_combine_grad<X, K, 4> : k_moe_combine_grad<X, K, 1>,
+            dim3((unsigned)std::min(kUnitBlocks, wide ? T : ceil_div(T, 4))), dim3(256), s,
             static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(ys), ldys, (int)rows, (int)T, (int)n, k,
             place, weights, static_cast<uint16_t*>(dys), lddys, dweights);
 }
@@ -218,9 +194,9 @@ int bakron_moe_gather(const void* x, int64_t ldx, int64_t tokens, int32_t type, 
     if (c < 0) return c;
     if (c == 1 || rows == 0) return BAKRON_SUCCESS;
     if (!x || !xs) return BAKRON_ERR_NULL_POINTER;
-    const bk::RowsGrid g = bk::rows_grid(tokens, cols);
-    bk::enqueue(bk::k_moe_gather, g.grid, dim3(256), stream, static_cast<const uint16_t*>(x), ldx, (int)tokens, (int)cols,
-                top_k, place, static_cast<uint16_t*>(xs), ldxs, (int)rows, g.log);
+    const bk::UnitGrid g = bk::unit_grid(tokens, bk::ceil_div(cols, 8), 0);
+    bk::enqueue(bk::k_moe_gather, dim3(g.blocks), dim3(256), stream, static_cast<const uint16_t*>(x), ldx, (int)tokens, (int)cols,
+                top_k, place, static_cast<uint16_t*>(xs), ldxs, (int)rows, g.log, g.chunks);
     return bk::moe_done();
 }
 
