@@ -3,45 +3,43 @@ choice (csrc/q4_experts.hip experts_plan, experts_grad_plan, experts_run),
 written out again so that a test can say which form it is meant to reach."""
 from q4_forms import ceil_div
 
-FEW_ROWS = 32
-PRODUCT = [(256, 256, (128.0, 80.0, 56.0)), (128, 128, (42.0, 28.0, 28.0))]
+FEW_MEAN = 48
+PRODUCT = [(256, 256, (128.0, 80.0, 56.0)), (128, 128, (39.0, 28.0, 28.0)), (64, 128, (28.0, 28.0, 28.0))]
 GRAD = [(256, 256, (130.0, 88.0, 64.0))]
 
 
-def estimate(shape, R, E, cols, depth, splits):
-    rows, width, us = shape
-    some = min(R, E)
-    c, nc = R / some, ceil_div(cols, width)
-    tile, one = us[0], c / rows * us[0] + 0.25 * (us[1] + us[2])
-    if c <= rows // 4:
-        tile = one = us[2]
-    elif c <= rows // 2:
-        tile = one = us[1]
-    work = max(some * nc * one / 256 + 0.4 * tile / splits, tile / splits)
-    return work * depth / 4096 + (2.0 + 8.0e-6 / 4 * splits * R * cols if splits > 1 else 0.0)
-
-
 def choose(shapes, R, E, cols, depth, deepest):
-    """(rows, columns) of the largest tile and the workgroups that share its depth."""
-    best, least = None, 0.0
-    for shape in shapes:
+    """(rows, columns) of the largest tile, the workgroups that share its depth, and
+    the time that is expected of it."""
+    some, best = min(R, E), None
+    for rows, width, us in shapes:
+        work = tile = 0.0
+        for q in range(8):
+            c = max(1, int((0.475 + 0.15 * q) * R / some))
+            rest = c % rows
+            cut = 0.0 if rest == 0 else us[2 if rest <= rows // 4 else 1 if rest <= rows // 2 else 0]
+            work += c // rows * us[0] + cut
+            tile = max(tile, us[0] if c >= rows else cut)
+        work *= some * ceil_div(cols, width) / (8.0 * 256)
         s = 1
-        while s == 1 or (s <= deepest and (R // shape[0] + min(R, E)) * ceil_div(cols, shape[1]) * s <= 2048):
-            us = estimate(shape, R, E, cols, depth, s)
-            if least == 0.0 or us < least:
-                least, best = us, (shape[0], shape[1], s)
+        while s == 1 or (s <= deepest and (R // rows + some) * ceil_div(cols, width) * s <= 2048):
+            t = max(work + 0.4 * tile / s, tile / s) * depth / 4096 + (2.0 + 8.0e-6 / 4 * s * R * cols if s > 1 else 0.0)
+            if best is None or t < best[3]:
+                best = rows, width, s, t
             s += 1
     return best
 
 
 def experts_form(R, E, m, n):
-    """q4_experts: ("few", waves of a pair of row tiles) or (rows, columns, splits)."""
-    if R <= FEW_ROWS * E:
+    """q4_experts: ("few", waves of a pair of row tiles) or (rows, splits, sums): with
+    sums beside the products where x's rows are aligned."""
+    if R <= FEW_MEAN * E:
         waves = ceil_div(ceil_div(m, 16), 2) * min(R, E)
         return "few", 8 if 8 * waves <= 8192 else 4 if 4 * waves <= 8192 else 2
-    return choose(PRODUCT, R, E, m, n, min(8, ceil_div(n, 128) // 2))
+    rows, _, splits, us = choose(PRODUCT, R, E, m, n, min(8, ceil_div(n, 128) // 2))
+    return rows, splits, rows == 64 and n % 64 == 0 and us < 30.0
 
 
 def experts_grad_form(R, E, m, n):
-    """q4_experts_grad."""
-    return choose(GRAD, R, E, n, m, min(16, ceil_div(m, 64) // 2))
+    """q4_experts_grad: the workgroups that share a tile's depth."""
+    return choose(GRAD, R, E, n, m, min(16, ceil_div(m, 64) // 2))[2]

@@ -79,29 +79,30 @@ def check(R, E, m, n, group, dtype, grad, seed, offsets=None, pad=0, out_pad=0):
 TYPES = [torch.bfloat16, torch.float16]
 # rows, experts, m, n, group: one row to many per expert, each kernel form
 SHAPES = [(1, 1, 1, 1, 0), (1, 8, 130, 300, 64), (6, 64, 33, 515, 192), (16, 5, 100, 64, 0), (96, 3, 64, 130, 64),
-          (17, 16, 5099, 72, 0), (318, 256, 146, 200, 0), (150, 2, 100, 1000, 128), (1782, 40, 720, 70, 64), (5393, 5, 21, 981, 128),
-          (373, 8, 7837, 65, 0), (5042, 5, 2406, 66, 64), (1996, 16, 2778, 128, 64), (42, 1, 200, 300, 64), (69, 1, 70, 520, 128),
-          (700, 9, 260, 640, 0), (6000, 16, 2778, 66, 64)]
+          (287, 256, 280, 70, 64), (15, 16, 2244, 72, 0), (150, 2, 100, 1000, 128), (4521, 40, 278, 70, 64), (4485, 40, 259, 128, 0),
+          (2497, 40, 34, 1180, 128), (2353, 16, 33, 1472, 0), (6000, 16, 4000, 66, 64), (8000, 16, 4096, 64, 0), (63, 1, 36, 43, 0),
+          (50, 1, 70, 64, 64), (58, 1, 70, 927, 128), (49, 1, 70, 768, 64), (700, 9, 260, 640, 0)]
 GRADS = [(1, 1, 1, 1, 0), (3, 8, 130, 300, 64), (6, 64, 515, 33, 0), (96, 3, 64, 130, 64), (300, 256, 65, 265, 64),
          (4980, 40, 30, 581, 192), (5260, 40, 337, 8, 64), (2189, 8, 66, 3491, 0), (5214, 16, 991, 8, 0), (33, 1, 264, 100, 64),
          (700, 9, 260, 640, 128), (1200, 3, 1030, 300, 64)]
 
 
 def test_the_shapes_reach_every_form():
-    forms = {experts_form(*s[:4]) for s in SHAPES}
+    forms = [experts_form(*s[:4]) + (s[3] % 64 == 0,) for s in SHAPES]
     assert {f[1] for f in forms if f[0] == "few"} == {2, 4, 8}
-    assert {(f[0], f[2] > 1) for f in forms if f[0] != "few"} == {(256, False), (128, False), (128, True)}
-    # with sums beside the products (n a multiple of 64), and from the pass over x
-    assert {s[3] % 64 == 0 for s in SHAPES if experts_form(*s[:4])[0] == 128} == {True, False}
-    assert {experts_grad_form(*s[:4])[2] > 1 for s in GRADS} == {True, False}
-    # blocks of every number of rows: 256, 128 and 64 of them, and cut ones
-    for shapes, form in ((SHAPES, experts_form), (GRADS, experts_grad_form)):
+    forms = {(f[0], f[1] > 1, *f[2:]) for f in forms if f[0] != "few"}   # rows, shared out, own sums, aligned
+    assert forms >= {(256, False, False, a) for a in (True, False)}
+    assert forms >= {(128, shared, False, a) for shared in (True, False) for a in (True, False)}
+    assert forms >= {(64, shared, a, a) for shared in (True, False) for a in (True, False)}
+    assert {experts_grad_form(*s[:4]) > 1 for s in GRADS} == {True, False}
+    # blocks of every number of rows, behind whole ones and alone
+    for shapes, most in ((SHAPES, 256), (SHAPES, 128), (SHAPES, 64), (GRADS, 256)):
         rest = set()
         for R, E, m, n, _ in shapes:
-            if form(R, E, m, n)[0] == 256:
+            if shapes is GRADS or experts_form(R, E, m, n)[0] == most:
                 c = np.diff(spread(R, E, R + n))
-                rest |= {(1 if r <= 64 else 2 if r <= 128 else 4, x >= 256) for x in c for r in [x % 256] if r}
-        assert rest == {(b, more) for b in (1, 2, 4) for more in (True, False)}
+                rest |= {(1 if r <= 64 else 2 if r <= 128 else 4, x >= most) for x in c for r in [x % most] if r}
+        assert rest == {(b, more) for b in (1, 2, 4) if 32 * b < most for more in (True, False)}, most
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["bf16", "fp16"])

@@ -90,10 +90,9 @@ __device__ __forceinline__ bool expert_tile(const int32_t* __restrict__ offsets,
                                             int& cls)
 {
     constexpr int BT = 64 * TA;
-    static_assert(TA == 2 || TA == 4, "");
     const ExpertLane lane(offsets, E, R);
-    const auto big = [](int c) { return c / BT + (c % BT > BT / 2); };
-    const auto half = [](int c) { return (int)(TA == 4 ? c % BT > 64 && c % BT <= 128 : c % BT > 0 && c % BT <= 64); };
+    const auto big = [](int c) { return c / BT + (TA == 1 ? c % BT > 0 : c % BT > BT / 2); };
+    const auto half = [](int c) { return (int)(TA > 1 && c % BT > BT / 4 * (TA / 4) && c % BT <= BT / 2); };
     const auto quarter = [](int c) { return (int)(TA == 4 && c % BT > 0 && c % BT <= 64); };
     int bigs = 0, rest = 0;   // rest: halves, and quarters in the upper 16 bits
 #pragma unroll
@@ -129,23 +128,22 @@ __device__ __forceinline__ bool expert_tile(const int32_t* __restrict__ offsets,
     return true;
 }
 
-// Tiles of 256, 128 and 64 rows by 256 of W (WR = 4), or of 128 and 64 by 128 (WR = 2).
-// OWN (WR = 2): the rows' sums are made beside the products (q4_prompt.hpp).
-template <class X, int WR, bool OWN>
+// Tiles of up to 64 TA rows by 64 WR of W.  OWN (WR = 2): the rows' sums are made beside the products (q4_prompt.hpp).
+template <class X, int TA, int WR, bool OWN>
 __global__ __launch_bounds__(128 * WR, 2) void k_q4_experts(const uint16_t* __restrict__ x, int64_t ldx, int R,
                                                             const int32_t* __restrict__ offsets, int E, Q4Layer stack,
                                                             int64_t layer_bytes, const float* __restrict__ sums, int64_t lds_,
                                                             uint16_t* __restrict__ y, int64_t ldy, int nr,
                                                             float* __restrict__ part)
 {
-    constexpr int BYTES = std::max(std::max(Prompt<WR, WR>::LDS, Prompt<WR / 2, WR>::LDS), Prompt<1, WR>::LDS);
+    constexpr int HALF = TA > 1 ? TA / 2 : 1, BYTES = std::max(std::max(Prompt<TA, WR>::LDS, Prompt<HALF, WR>::LDS), Prompt<1, WR>::LDS);
     ExpertRows rows;
     int br, cls;
-    if (!expert_tile<WR>(offsets, E, R, nr, rows, br, cls)) return;
+    if (!expert_tile<TA>(offsets, E, R, nr, rows, br, cls)) return;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
-    if (cls == 0) prompt_tile<X, WR, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
-    else if (cls == 1) prompt_tile<X, WR / 2, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
-    else if (WR == 4) prompt_tile<X, 1, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    if (cls == 0) prompt_tile<X, TA, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    else if (cls == 1 && TA > 1) prompt_tile<X, HALF, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    else if (TA > 2) prompt_tile<X, 1, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
 }
 
 template <class X>
@@ -201,7 +199,11 @@ __global__ __launch_bounds__(256) void k_q4_experts_zero(uint16_t* __restrict__ 
 // A wave has two row tiles of W, which share the rows' fragments; WS waves share
 // the columns of a pair and are joined in wave order.
 
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 32;   // of a block
+// Up to so many rows per expert on average (6 of 64 experts of 1024 x 2048, 39 rows each:
+// 36.6 us, and 43.6 in tiles of 64 rows; 48: 40.8 and 44.8; 60: 49.0 and 49.7; 2 of 8 of
+// 14336 x 4096, 50 each: 117 and 102).
+constexpr int kFewMean = 48;
 constexpr int kFewLds = 8 * std::max(few_lds(kFewRows / 4), 16 * 64 * 4);   // staged rows, then the joining sums
 
 template <class X, int TQ, int U, int WS, bool HALF>
@@ -265,8 +267,9 @@ __global__ __launch_bounds__(512, 4) void k_q4_experts_few(const uint16_t* __res
 // --------------------------------------------------------------------- host
 
 struct ExpertsPlan {
-    bool few, own;
-    int WR, splits;
+    bool few;
+    int TA, WR, splits;
+    double us;         // that it is expected to take
     int64_t tiles;     // of rows, that there can be
     int pieces;
     int64_t lds_, ldc;
@@ -283,42 +286,65 @@ struct ExpertShape {
     double us[3];
 };
 
-// What a launch is expected to take with its depth shared out `splits` times, were the
-// rows dealt out evenly but for where they end in a block: the work over 256 CUs, and
-// two fifths of a tile for the CUs that finish last.
-static double experts_us(const ExpertShape& s, int64_t R, int64_t E, int64_t cols, int64_t depth, int splits)
+// What a launch is expected to take with its depth shared out `splits` times: the work
+// over 256 CUs, and two fifths of a long tile for the CUs that finish last.  The rows
+// are not dealt out evenly: experts have 0.4 to 1.6 times the mean.
+struct ExpertWork {
+    double all, tile;   // of a depth of 4096: all tiles over 256 CUs, and the longest
+};
+static ExpertWork experts_work(const ExpertShape& s, int64_t R, int64_t E, int64_t cols)
 {
-    const double some = (double)std::min(R, E), c = R / some, nc = (double)ceil_div(cols, s.cols);
-    double tile = s.us[0], us = c / s.rows * s.us[0] + 0.25 * (s.us[1] + s.us[2]);
-    if (c <= s.rows / 4) tile = us = s.us[2];
-    else if (c <= s.rows / 2) tile = us = s.us[1];
-    const double work = std::max(some * nc * us / 256 + 0.4 * tile / splits, tile / splits);
-    // and a launch that joins the parts, which go there and back at 4 TB/s
-    return work * depth / 4096 + (splits > 1 ? 2.0 + 8.0e-6 / 4 * splits * R * cols : 0.0);
+    const int64_t some = std::min(R, E);
+    ExpertWork w{0.0, 0.0};
+    for (int q = 0; q < 8; ++q) {
+        const int64_t c = std::max<int64_t>(1, (int64_t)((0.475 + 0.15 * q) * R / some)), rest = c % s.rows;
+        const double cut = rest == 0 ? 0.0 : s.us[rest <= s.rows / 4 ? 2 : rest <= s.rows / 2 ? 1 : 0];
+        w.all += (double)(c / s.rows) * s.us[0] + cut;
+        w.tile = std::max(w.tile, c >= s.rows ? s.us[0] : cut);
+    }
+    w.all *= some * ceil_div(cols, s.cols) / (8.0 * 256);
+    return w;
+}
+static double experts_us(const ExpertWork& w, int64_t R, int64_t cols, int64_t depth, int splits)
+{
+    // (splits: a launch that joins the parts, which go there and back at 4 TB/s)
+    return std::max(w.all + 0.4 * w.tile / splits, w.tile / splits) * depth / 4096 +
+           (splits > 1 ? 2.0 + 8.0e-6 / 4 * splits * R * cols : 0.0);
 }
 
 // The least of it over shapes and splits, with `deepest` splits at most.
+struct ExpertsChoice {
+    int shape, splits;
+    double us;
+};
 template <int N>
-static int experts_choose(const ExpertShape (&shapes)[N], int64_t R, int64_t E, int64_t cols, int64_t depth, int64_t deepest,
-                          int& splits)
+static ExpertsChoice experts_choose(const ExpertShape (&shapes)[N], int64_t R, int64_t E, int64_t cols, int64_t depth,
+                                    int64_t deepest)
 {
-    int best = 0;
-    double least = 0.0;
-    for (int i = 0; i < N; ++i)
-        for (int s = 1; s == 1 || (s <= deepest && blocks_most(R, E, shapes[i].rows) * ceil_div(cols, shapes[i].cols) * s <= 2048); ++s) {
-            const double us = experts_us(shapes[i], R, E, cols, depth, s);
-            if (least == 0.0 || us < least) least = us, best = i, splits = s;
+    ExpertsChoice best{0, 1, 0.0};
+    for (int i = 0; i < N; ++i) {
+        const ExpertWork w = experts_work(shapes[i], R, E, cols);
+        const int64_t tiles = blocks_most(R, E, shapes[i].rows) * ceil_div(cols, shapes[i].cols);
+        for (int s = 1; s == 1 || (s <= deepest && tiles * s <= 2048); ++s) {
+            const double us = experts_us(w, R, cols, depth, s);
+            if (best.us == 0.0 || us < best.us) best = {i, s, us};
         }
+    }
     return best;
 }
 
 static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int gb)
 {
     ExpertsPlan p{};
-    p.few = R <= kFewRows * E;
+    p.few = R <= kFewMean * E;
     if (p.few) return p;
-    static constexpr ExpertShape shapes[] = {{256, 256, {128.0, 80.0, 56.0}}, {128, 128, {42.0, 28.0, 28.0}}};
-    const ExpertShape& s = shapes[experts_choose(shapes, R, E, m, n, std::min<int64_t>(8, ceil_div(n, kQ4Cols) / 2), p.splits)];
+    static constexpr ExpertShape shapes[] = {
+        {256, 256, {128.0, 80.0, 56.0}}, {128, 128, {39.0, 28.0, 28.0}}, {64, 128, {28.0, 28.0, 28.0}}};
+    const ExpertsChoice c = experts_choose(shapes, R, E, m, n, std::min<int64_t>(8, ceil_div(n, kQ4Cols) / 2));
+    const ExpertShape& s = shapes[c.shape];
+    p.splits = c.splits;
+    p.us = c.us;
+    p.TA = s.rows / 64;
     p.WR = s.cols / 64;
     p.tiles = blocks_most(R, E, s.rows);
     p.lds_ = ceil_div(R, 256) * 256 + 256;   // a block's sums are read as a whole, whichever row it begins at
@@ -334,7 +360,7 @@ static ExpertsPlan experts_grad_plan(int64_t R, int64_t E, int64_t m, int64_t n)
 {
     ExpertsPlan p{};
     static constexpr ExpertShape shapes[] = {{256, 256, {130.0, 88.0, 64.0}}};   // as in q4_grad.hip
-    experts_choose(shapes, R, E, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2), p.splits);
+    p.splits = experts_choose(shapes, R, E, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2)).splits;
     p.tiles = blocks_most(R, E, 256);
     p.ldc = ceil_div(m, 64) * 64;
     p.part = align_up((size_t)R * p.ldc * 2);
@@ -370,11 +396,11 @@ static void experts_few(const ExpertsCall& c, const Q4Layer& w)
             (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout);
 }
 
-template <class X, int WR, bool OWN>
+template <class X, int TA, int WR, bool OWN>
 static void experts_launch(const ExpertsCall& c, const ExpertsPlan& p, const Q4Layer& w, const uint16_t* x, int64_t ldx)
 {
     const int nr = (int)ceil_div(w.m, 64 * WR);
-    enqueue(k_q4_experts<X, WR, OWN>, dim3((unsigned)(p.tiles * nr), (unsigned)p.splits), dim3(128 * WR), c.s, x, ldx,
+    enqueue(k_q4_experts<X, TA, WR, OWN>, dim3((unsigned)(p.tiles * nr), (unsigned)p.splits), dim3(128 * WR), c.s, x, ldx,
             (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, reinterpret_cast<const float*>(c.ws), p.lds_, c.out,
             c.ldout, nr, reinterpret_cast<float*>(c.ws + p.part));
 }
@@ -393,7 +419,10 @@ static void experts_run(const ExpertsCall& c)
     }
     // (the staging offsets of a block of rows are 31 bits)
     const bool direct = w.n % 64 == 0 && c.ldin % 8 == 0 && c.ldin <= (1 << 21) && aligned16(c.in);
-    const bool own = p.WR == 2 && direct;
+    // Sums beside the products are half as many more products, and save a launch: only
+    // where that is what counts, and for tiles of 64 rows (128 rows: 2048 tokens, 4 of 16 of
+    // 2048 x 2048: 102 us, and 92 with the pass).
+    const bool own = p.TA == 1 && direct && p.us < 30.0;
     const uint16_t* x = c.in;
     int64_t ldx = c.ldin;
     uint16_t* copy = reinterpret_cast<uint16_t*>(c.ws + p.copy);
@@ -401,9 +430,9 @@ static void experts_run(const ExpertsCall& c)
         enqueue(direct ? k_q4_sums<X, false> : k_q4_sums<X, true>, dim3((unsigned)ceil_div(c.rows, 4)), dim3(256), c.s, x, ldx,
                 (int)c.rows, w.n, w.gb, p.pieces, reinterpret_cast<float*>(c.ws), p.lds_, copy, p.ldc);
     if (!direct) x = copy, ldx = p.ldc;
-    if (p.WR == 4) experts_launch<X, 4, false>(c, p, w, x, ldx);
-    else if (own) experts_launch<X, 2, true>(c, p, w, x, ldx);
-    else experts_launch<X, 2, false>(c, p, w, x, ldx);
+    if (p.TA == 4) experts_launch<X, 4, 4, false>(c, p, w, x, ldx);
+    else if (p.TA == 2) (own ? experts_launch<X, 2, 2, true> : experts_launch<X, 2, 2, false>)(c, p, w, x, ldx);
+    else (own ? experts_launch<X, 1, 2, true> : experts_launch<X, 1, 2, false>)(c, p, w, x, ldx);
     if (p.splits > 1) experts_join<X>(c, reinterpret_cast<const float*>(c.ws + p.part), p.splits, w.m);
 }
 
