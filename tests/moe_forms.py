@@ -40,6 +40,13 @@ def experts_form(R, E, m, n):
     return rows, splits, rows == 64 and n % 64 == 0 and us < 30.0
 
 
-def experts_grad_form(R, E, m, n):
-    """q4_experts_grad: the workgroups that share a tile's depth."""
-    return choose(GRAD, R, E, n, m, min(16, ceil_div(m, 64) // 2))[2]
+def experts_grad_form(R, E, m, n, group):
+    """q4_experts_grad: ("few" or "tiles", the workgroups that share a block's depth)."""
+    best = choose(GRAD, R, E, n, m, min(16, ceil_div(m, 64) // 2))
+    rows, some = 16 if group // 64 % 2 else 32, min(R, E)
+    blocks = max(some, R // rows + some // 2)
+    groups = blocks * ceil_div(n, 128)
+    splits = max(1, min(16, 512 // groups, ceil_div(m, 32) // 16))
+    if blocks * float(m) * n / ((4.5e6 if rows == 16 else 6.0e6) * min(1.0, groups * splits / 512.0)) <= 1.0 + best[3]:
+        return "few", splits
+    return "tiles", best[2]

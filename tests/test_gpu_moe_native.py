@@ -78,15 +78,21 @@ def test_the_same_results():
     for name in calls(v, native):
         for a, b in zip(flat(native[name]), flat(python[name])):
             assert torch.equal(a, b), name
-    # a gradient that needs a workspace: the native call declines without one
-    args = [v["dm"], v["w"], v["r"]["offsets"], native["experts_grad"], None]
-    need = B.q4_experts_grad_workspace_bytes(80, v["w"])
-    assert need and moe._fast.experts_grad(*args) is False
+    # a call that needs a workspace: declined without one
+    x, out = tokens(600, 128, BF16, 6), torch.empty((600, 64), dtype=BF16, device=DEV)
+    at = torch.arange(9, dtype=I32, device=DEV) * 75
+    need = B.q4_experts_workspace_bytes(600, v["w"])
+    args = [x, v["w"], at, out, None]
+    assert need and moe._fast.experts(*args) is False
     args[-1] = B.workspace(need, DEV)
-    assert moe._fast.experts_grad(*args) is True
-    assert torch.equal(native["experts_grad"], B.q4_experts_grad(v["dm"], v["w"], v["r"]["offsets"]))
+    assert moe._fast.experts(*args) is True
+    assert torch.equal(out, B.q4_experts(x, v["w"], at))
     args[-1] = B.workspace(need, DEV)[:-256]
-    assert moe._fast.experts_grad(*args) is False
+    assert moe._fast.experts(*args) is False
+    dx = torch.empty_like(v["ys"])
+    assert moe._fast.experts_grad(v["dm"], v["w"], v["r"]["offsets"], dx, B.workspace(1 << 20, DEV)) is True
+    last = int(v["r"]["offsets"][-1])
+    assert torch.equal(dx[:last], B.q4_experts_grad(v["dm"], v["w"], v["r"]["offsets"])[:last])
     # and the public calls return what was given to them
     o = outputs(v)
     got = {name: call() for name, (_, call) in calls(v, o).items()}

@@ -82,9 +82,10 @@ SHAPES = [(1, 1, 1, 1, 0), (1, 8, 130, 300, 64), (6, 64, 33, 515, 192), (16, 5, 
           (287, 256, 280, 70, 64), (15, 16, 2244, 72, 0), (150, 2, 100, 1000, 128), (4521, 40, 278, 70, 64), (4485, 40, 259, 128, 0),
           (2497, 40, 34, 1180, 128), (2353, 16, 33, 1472, 0), (6000, 16, 4000, 66, 64), (8000, 16, 4096, 64, 0), (63, 1, 36, 43, 0),
           (50, 1, 70, 64, 64), (58, 1, 70, 927, 128), (49, 1, 70, 768, 64), (700, 9, 260, 640, 0)]
-GRADS = [(1, 1, 1, 1, 0), (3, 8, 130, 300, 64), (6, 64, 515, 33, 0), (96, 3, 64, 130, 64), (300, 256, 65, 265, 64),
-         (4980, 40, 30, 581, 192), (5260, 40, 337, 8, 64), (2189, 8, 66, 3491, 0), (5214, 16, 991, 8, 0), (33, 1, 264, 100, 64),
-         (700, 9, 260, 640, 128), (1200, 3, 1030, 300, 64)]
+GRADS = [(1, 1, 1, 1, 0), (3, 8, 130, 300, 64), (6, 64, 515, 33, 0), (96, 3, 64, 130, 64), (300, 256, 65, 265, 64), (17, 4, 31, 40, 0),
+         (40, 2, 1100, 300, 128), (9, 3, 5000, 70, 64), (200, 8, 2090, 400, 0), (90, 40, 300, 700, 192), (33, 1, 700, 129, 256),
+         (4980, 40, 30, 581, 192), (5260, 40, 337, 8, 64), (70, 1, 264, 100, 64), (7801, 3, 49, 483, 192), (2189, 8, 66, 3491, 0), (4000, 16, 300, 2500, 128),
+         (1558, 24, 64, 2262, 64), (616, 3, 717, 96, 64), (1200, 3, 1030, 1300, 64)]
 
 
 def test_the_shapes_reach_every_form():
@@ -94,12 +95,18 @@ def test_the_shapes_reach_every_form():
     assert forms >= {(256, False, False, a) for a in (True, False)}
     assert forms >= {(128, shared, False, a) for shared in (True, False) for a in (True, False)}
     assert forms >= {(64, shared, a, a) for shared in (True, False) for a in (True, False)}
-    assert {experts_grad_form(*s[:4]) > 1 for s in GRADS} == {True, False}
+    assert {(f, s > 1) for f, s in (experts_grad_form(*s) for s in GRADS)} == {(f, s) for f in ("few", "tiles") for s in (True, False)}
+    # few rows: blocks of up to 16 and 32 of them, grids that end inside a block of columns
+    # or do not, an even and an odd number of row tiles, and a last step that is cut
+    few = [s for s in GRADS if experts_grad_form(*s)[0] == "few"]
+    assert {s[4] // 64 % 2 for s in few} == {0, 1} and {-(-s[2] // 16) % 2 for s in few} == {0, 1} and {s[2] % 32 > 0 for s in few} == {True, False}
+    rest = {min((c - 1) % 32 // 16, 1) for R, E, m, n, g in few if g // 64 % 2 == 0 for c in np.diff(spread(R, E, R + n)) if c}
+    assert rest == {0, 1}
     # blocks of every number of rows, behind whole ones and alone
     for shapes, most in ((SHAPES, 256), (SHAPES, 128), (SHAPES, 64), (GRADS, 256)):
         rest = set()
-        for R, E, m, n, _ in shapes:
-            if shapes is GRADS or experts_form(R, E, m, n)[0] == most:
+        for R, E, m, n, g in shapes:
+            if experts_grad_form(R, E, m, n, g)[0] == "tiles" if shapes is GRADS else experts_form(R, E, m, n)[0] == most:
                 c = np.diff(spread(R, E, R + n))
                 rest |= {(1 if r <= 64 else 2 if r <= 128 else 4, x >= most) for x in c for r in [x % most] if r}
         assert rest == {(b, more) for b in (1, 2, 4) if 32 * b < most for more in (True, False)}, most

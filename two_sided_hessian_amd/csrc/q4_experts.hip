@@ -17,6 +17,7 @@
 
 #include "moe.hpp"
 #include "q4_grad.hpp"
+#include "q4_grad_few.hpp"
 #include "q4_prompt.hpp"
 
 namespace bk {
@@ -264,6 +265,41 @@ __global__ __launch_bounds__(512, 4) void k_q4_experts_few(const uint16_t* __res
     else few_rows_of<X, 8, 1, WS, HALF>(x, ldx, w, rt0, rows.t0, n, lds, y, ldy);
 }
 
+// The gradient: a workgroup has a block of up to 16 SETS rows and 128 columns, its
+// waves the rows of W in turn; blockIdx.z of gridDim.z shares those.
+constexpr int kGradFewWaves = 4;   // (8: 5 to 15 % slower, but for the fewest rows)
+inline int grad_few_rows(int gb) { return gb % 2 ? 16 : 32; }   // of a block: its columns may have two grids
+
+template <class X, int SETS, bool HALF>
+__global__ __launch_bounds__(64 * kGradFewWaves) void k_q4_experts_grad_few(const uint16_t* __restrict__ dy, int64_t lddy, int R,
+                                                                           const int32_t* __restrict__ offsets, int E,
+                                                                           Q4Layer stack, int64_t layer_bytes,
+                                                                           uint16_t* __restrict__ dx, int64_t lddx,
+                                                                           float* __restrict__ part)
+{
+    constexpr int BT = 16 * SETS;
+    __shared__ __align__(16) char lds[kGradFewWaves * std::max(kGradFewStage, kGradFewJoin)];
+    const ExpertLane lane(offsets, E, R);
+    const auto blocks = [](int c) { return (c + BT - 1) / BT; };
+    int sum = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum += blocks(lane.rows(u));
+    const int upto = lanes_upto(sum);
+    int k = blockIdx.y;
+    if (k >= __builtin_amdgcn_readlane(upto, 63)) return;
+    ExpertRows rows;
+    expert_at(lane, lane_of(upto, sum, k), k, blocks, rows);
+    rows.t0 += k * BT;
+    const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
+    const int n = min(BT, rows.t1 - rows.t0), all = (w.m + 31) / 32;
+    const int s0 = all * blockIdx.z / gridDim.z, s1 = all * (blockIdx.z + 1) / gridDim.z;
+    float* to = gridDim.z > 1 ? part + (int64_t)blockIdx.z * R * w.n : nullptr;
+    if (SETS == 1 || n <= 16)
+        grad_few<X, 1, HALF, kGradFewWaves>(dy, lddy, w, blockIdx.x, rows.t0, n, s0, s1, lds, dx, lddx, to, w.n);
+    else
+        grad_few<X, SETS, HALF, kGradFewWaves>(dy, lddy, w, blockIdx.x, rows.t0, n, s0, s1, lds, dx, lddx, to, w.n);
+}
+
 // --------------------------------------------------------------------- host
 
 struct ExpertsPlan {
@@ -278,6 +314,13 @@ struct ExpertsPlan {
 
 // Blocks of at most `rows` rows that R rows of E experts can make.
 static int64_t blocks_most(int64_t R, int64_t E, int64_t rows) { return R / rows + std::min(R, E); }
+
+// About how many there will be.
+static int64_t blocks_about(int64_t R, int64_t E, int64_t rows)
+{
+    const int64_t some = std::min(R, E);
+    return std::max(some, R / rows + some / 2);
+}
 
 // A product's tiles: their rows (and halves and quarters of them), columns, and what
 // each takes in us for a depth of 4096, the chip full of them.
@@ -356,11 +399,25 @@ static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int 
     return p;
 }
 
-static ExpertsPlan experts_grad_plan(int64_t R, int64_t E, int64_t m, int64_t n)
+static ExpertsPlan experts_grad_plan(int64_t R, int64_t E, int64_t m, int64_t n, int gb)
 {
     ExpertsPlan p{};
     static constexpr ExpertShape shapes[] = {{256, 256, {130.0, 88.0, 64.0}}};   // as in q4_grad.hip
-    p.splits = experts_choose(shapes, R, E, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2)).splits;
+    const ExpertsChoice c = experts_choose(shapes, R, E, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2));
+    // Few rows: a block's codes at 6 T/s however many rows it has (4.5 where its columns
+    // have two grids), where there are two workgroups for every CU; the rows of W are shared out towards that, four steps at
+    // least for every wave.  (6 of 64 experts of 2048 x 1024 in groups of 128, 48 rows each:
+    // 51 us, in tiles 62; 96: 88 and 69; groups of 64, 24 rows: 61 and 48; 7 of 43 of 1152 x
+    // 320, 70 rows each: 18 and 31.)
+    const int64_t blocks = blocks_about(R, E, grad_few_rows(gb)), groups = blocks * ceil_div(n, kQ4Cols);
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({16, 512 / groups, ceil_div(m, 32) / (4 * kGradFewWaves)}));
+    p.few = blocks * (double)m * n / ((gb % 2 ? 4.5e6 : 6.0e6) * std::min(1.0, groups * splits / 512.0)) <= 1.0 + c.us;
+    if (p.few) {
+        p.splits = (int)splits;
+        p.bytes = p.splits > 1 ? align_up((size_t)p.splits * R * n * 4) : 0;
+        return p;
+    }
+    p.splits = c.splits;
     p.tiles = blocks_most(R, E, 256);
     p.ldc = ceil_div(m, 64) * 64;
     p.part = align_up((size_t)R * p.ldc * 2);
@@ -440,9 +497,18 @@ template <class X>
 static void experts_grad_run(const ExpertsCall& c)
 {
     const Q4Layer w = q4_layer(c.packed, c.d);
-    const ExpertsPlan p = experts_grad_plan(c.rows, c.E, w.m, w.n);
+    const ExpertsPlan p = experts_grad_plan(c.rows, c.E, w.m, w.n, w.gb);
     const uint16_t* dy = c.in;
     int64_t lddy = c.ldin;
+    if (p.few) {
+        const int rows = grad_few_rows(w.gb);
+        float* part = reinterpret_cast<float*>(c.ws);
+        enqueue(w.gb % 2 ? k_q4_experts_grad_few<X, 1, true> : k_q4_experts_grad_few<X, 2, false>,
+                dim3((unsigned)w.KB, (unsigned)blocks_most(c.rows, c.E, rows), (unsigned)p.splits), dim3(64 * kGradFewWaves), c.s,
+                dy, lddy, (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, part);
+        if (p.splits > 1) experts_join<X>(c, part, p.splits, w.n);
+        return;
+    }
     if (w.m % 64 || lddy % 8 || lddy > (1 << 21) || !aligned16(dy)) {
         copy_enqueue<X>(dy, lddy, c.rows, w.m, reinterpret_cast<uint16_t*>(c.ws), p.ldc, c.s);
         dy = reinterpret_cast<const uint16_t*>(c.ws);
@@ -503,7 +569,7 @@ size_t bakron_q4_experts_workspace_bytes(int64_t rows, int64_t experts, int64_t 
 size_t bakron_q4_experts_grad_workspace_bytes(int64_t rows, int64_t experts, int64_t m, int64_t n, int64_t group_size)
 {
     if (!bk::experts_size_ok(rows, m, n) || !bk::experts_arg_ok(experts, group_size) || rows == 0 || m == 0 || n == 0) return 0;
-    return bk::experts_grad_plan(rows, experts, m, n).bytes;
+    return bk::experts_grad_plan(rows, experts, m, n, bk::q4_dims(m, n, group_size).gb).bytes;
 }
 
 int bakron_q4_experts(const void* x, int64_t ldx, int64_t rows, int32_t type, const void* packed, int64_t experts,
