@@ -173,6 +173,12 @@ def moe_route_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
 _ROUTE = ("ids", "weights", "place", "order", "offsets")
 
 
+def _route_results(logits, k):
+    (T, E), e, i32 = logits.shape, logits.new_empty, torch.int32
+    return (e((T, k), dtype=i32), e((T, k), dtype=torch.float32), e((T, k), dtype=i32), e((T * k,), dtype=i32),
+            e((E + 1,), dtype=i32))
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_k, ws, stream):
@@ -214,11 +220,7 @@ def moe_route(logits, top_k, *, out=None, ws=None, stream=None):
         return dict(zip(_ROUTE, _Route.apply(logits, k, ws, stream)))
     i32 = torch.int32
     if out is None:
-        def make():
-            e = logits.new_empty
-            return (e((T, k), dtype=i32), e((T, k), dtype=torch.float32), e((T, k), dtype=i32), e((T * k,), dtype=i32),
-                    e((E + 1,), dtype=i32))
-        out = dict(zip(_ROUTE, _made(stream, make)))
+        out = dict(zip(_ROUTE, _made(stream, lambda: _route_results(logits, k))))
     at = [_flat(f"out['{name}']", out[name], torch.float32 if name == "weights" else i32,
                 (T * k,) if name == "order" else (E + 1,) if name == "offsets" else (T, k), index) for name in _ROUTE]
     ws = _space(ws, moe_route_workspace_bytes(T, E, k), logits.device, index, stream)
@@ -664,15 +666,30 @@ def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=N
 
 # ------------------------------------------------------------ the whole layer
 
+def _shared(sizes, like):
+    """One workspace for calls that follow each other, or None."""
+    need = max(sizes)
+    return _b.workspace(need, like.device) if need else None
+
+
 def _forward(x, logits, w_gate, w_up, w_down, k, act, keep):
-    r = moe_route(logits, k)
-    offsets, count = r["offsets"], r["offsets"][-1:]
-    xs = moe_gather(x, r["place"])
-    a, b = q4_experts(xs, w_gate, offsets), q4_experts(xs, w_up, offsets)
-    h = gated_act(a, b, act=act, checkpoint=keep, count=count)
-    h, cks = (h[0], h[1:]) if keep else (h, None)
-    ys = q4_experts(h, w_down, offsets)
-    return moe_combine(ys, r["place"], r["weights"]), r, ys, cks
+    # outputs are given everywhere, which is what the native calls take
+    (T, n), f, e = x.shape, w_gate.m, x.new_empty
+    R = T * k
+    ws = _shared((moe_route_workspace_bytes(T, w_gate.count, k), q4_experts_workspace_bytes(R, w_gate),
+                  q4_experts_workspace_bytes(R, w_down)), x)
+    r = moe_route(logits, k, out=dict(zip(_ROUTE, _route_results(logits, k))), ws=ws)
+    place, offsets = r["place"], r["offsets"]
+    count = offsets[-1:]
+    xs = moe_gather(x, place, out=e((R, n)))
+    a, b = (q4_experts(xs, w, offsets, out=e((R, f)), ws=ws) for w in (w_gate, w_up))
+    if keep:
+        h, *cks = gated_act(a, b, act=act, count=count, out=e((R, f)),
+                            checkpoint=tuple(Checkpoint8.empty(R, f, x.dtype, x.device) for _ in range(2)))
+    else:
+        h, cks = gated_act(a, b, act=act, count=count, out=e((R, f))), None
+    ys = q4_experts(h, w_down, offsets, out=e((R, n)), ws=ws)
+    return moe_combine(ys, place, r["weights"], out=e((T, n))), r, ys, cks
 
 
 class _Layer(torch.autograd.Function):
@@ -689,21 +706,25 @@ class _Layer(torch.autograd.Function):
     def backward(ctx, dy):
         ids, weights, place, offsets, ys, ca, cb = ctx.saved_tensors
         w_gate, w_up, w_down = ctx.layers
-        back = moe_combine_grad(dy.contiguous(), ys, place, weights)
+        (R, n), f, e = ys.shape, w_gate.m, ys.new_empty
+        back = moe_combine_grad(dy.contiguous(), ys, place, weights,
+                                out={"dys": e((R, n)), "dweights": torch.empty_like(weights)})
         dlogits = dx = None
         if ctx.needs_input_grad[1]:
-            dlogits = moe_route_grad(back["dweights"], weights, ids, ctx.logits[0], dtype=ctx.logits[1])
+            E, dtype = ctx.logits
+            dlogits = moe_route_grad(back["dweights"], weights, ids, E, out=e((weights.shape[0], E), dtype=dtype))
         if ctx.needs_input_grad[0]:
-            R = ys.shape[0]
-            dh = q4_experts_grad(back["dys"], w_down, offsets)
+            ws = _shared((q4_experts_grad_workspace_bytes(R, w_down), q4_experts_grad_workspace_bytes(R, w_gate)), ys)
+            dh = q4_experts_grad(back["dys"], w_down, offsets, out=e((R, f)), ws=ws)
             da, db = gated_act_grad(dh, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
-                                    count=offsets[-1:])
+                                    count=offsets[-1:], out=(e((R, f)), e((R, f))))
             # both halves of the rows' gradient in one sum: a token's places in
             # the first and in the second
-            dxs = dy.new_empty((2 * R, w_gate.n))
-            q4_experts_grad(da, w_gate, offsets, out=dxs[:R])
-            q4_experts_grad(db, w_up, offsets, out=dxs[R:])
-            dx = moe_combine(dxs, torch.cat((place, torch.where(place < 0, place, place + R)), 1))
+            dxs = e((2 * R, n))
+            q4_experts_grad(da, w_gate, offsets, out=dxs[:R], ws=ws)
+            q4_experts_grad(db, w_up, offsets, out=dxs[R:], ws=ws)
+            both = torch.cat((place, torch.where(place < 0, place, place + R)), 1)
+            dx = moe_combine(dxs, both, out=e((place.shape[0], n)))
         return dx, dlogits, None, None, None, None, None
 
 
