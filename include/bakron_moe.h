@@ -162,7 +162,9 @@ int bakron_q4_experts(const void* x, int64_t ldx, int64_t rows, int32_t type, co
 
 /*
  * bakron_q4_experts_grad -- the gradient of bakron_q4_experts with respect to
- * its rows, dx[p] = dy[p] W_e, rounded as bakron_q4_linear_grad does it.
+ * its rows, dx[p] = dy[p] W_e.  Experts with many rows: each weight is rounded
+ * once to dy's type, as bakron_q4_linear_grad does it.  With few: dy times a
+ * step is kept in two bfloat16 terms (2^-16 relative) and the codes are exact.
  *
  * dy         [in]  rows x m; dx [out] rows x n.  m == 0 writes zeros.
  *                  Everything else as in bakron_q4_experts.

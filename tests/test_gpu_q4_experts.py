@@ -142,6 +142,13 @@ def test_one_expert_has_all_rows(grad):
             check(R, E, m, n, 64, torch.bfloat16, grad, e, offsets)
 
 
+def test_more_blocks_of_rows_than_65535():
+    R, E, m, n = 2_200_000, 2, 8, 8
+    assert experts_grad_form(R, E, m, n, 0)[0] == "few" and R // 32 > 65535
+    for grad in (False, True):
+        check(R, E, m, n, 0, torch.bfloat16, grad, 1, np.array([0, 1_500_001, R]))
+
+
 @pytest.mark.parametrize("grad", [False, True], ids=["product", "grad"])
 @pytest.mark.parametrize("R,E", [(50, 8), (2000, 8)])
 def test_no_rows_at_all(R, E, grad):

@@ -266,7 +266,8 @@ __global__ __launch_bounds__(512, 4) void k_q4_experts_few(const uint16_t* __res
 }
 
 // The gradient: a workgroup has a block of up to 16 SETS rows and 128 columns, its
-// waves the rows of W in turn; blockIdx.z of gridDim.z shares those.
+// waves the rows of W in turn; blockIdx.z of gridDim.z shares those.  (Blocks of rows
+// are x: there can be more of them than y has room for.)
 constexpr int kGradFewWaves = 4;   // (8: 5 to 15 % slower, but for the fewest rows)
 inline int grad_few_rows(int gb) { return gb % 2 ? 16 : 32; }   // of a block: its columns may have two grids
 
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(64 * kGradFewWaves) void k_q4_experts_grad_few(cons
 #pragma unroll
     for (int u = 0; u < 4; ++u) sum += blocks(lane.rows(u));
     const int upto = lanes_upto(sum);
-    int k = blockIdx.y;
+    int k = blockIdx.x;
     if (k >= __builtin_amdgcn_readlane(upto, 63)) return;
     ExpertRows rows;
     expert_at(lane, lane_of(upto, sum, k), k, blocks, rows);
@@ -295,9 +296,9 @@ __global__ __launch_bounds__(64 * kGradFewWaves) void k_q4_experts_grad_few(cons
     const int s0 = all * blockIdx.z / gridDim.z, s1 = all * (blockIdx.z + 1) / gridDim.z;
     float* to = gridDim.z > 1 ? part + (int64_t)blockIdx.z * R * w.n : nullptr;
     if (SETS == 1 || n <= 16)
-        grad_few<X, 1, HALF, kGradFewWaves>(dy, lddy, w, blockIdx.x, rows.t0, n, s0, s1, lds, dx, lddx, to, w.n);
+        grad_few<X, 1, HALF, kGradFewWaves>(dy, lddy, w, blockIdx.y, rows.t0, n, s0, s1, lds, dx, lddx, to, w.n);
     else
-        grad_few<X, SETS, HALF, kGradFewWaves>(dy, lddy, w, blockIdx.x, rows.t0, n, s0, s1, lds, dx, lddx, to, w.n);
+        grad_few<X, SETS, HALF, kGradFewWaves>(dy, lddy, w, blockIdx.y, rows.t0, n, s0, s1, lds, dx, lddx, to, w.n);
 }
 
 // --------------------------------------------------------------------- host
@@ -504,7 +505,7 @@ static void experts_grad_run(const ExpertsCall& c)
         const int rows = grad_few_rows(w.gb);
         float* part = reinterpret_cast<float*>(c.ws);
         enqueue(w.gb % 2 ? k_q4_experts_grad_few<X, 1, true> : k_q4_experts_grad_few<X, 2, false>,
-                dim3((unsigned)w.KB, (unsigned)blocks_most(c.rows, c.E, rows), (unsigned)p.splits), dim3(64 * kGradFewWaves), c.s,
+                dim3((unsigned)blocks_most(c.rows, c.E, rows), (unsigned)w.KB, (unsigned)p.splits), dim3(64 * kGradFewWaves), c.s,
                 dy, lddy, (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, part);
         if (p.splits > 1) experts_join<X>(c, part, p.splits, w.n);
         return;
