@@ -47,7 +47,7 @@ def on(at, *shape, dtype=BF16):
 
 
 def checkpoint(at, rows, cols, dtype=BF16):
-    return moe.Checkpoint8(on(at, 16, dtype=torch.uint8), rows, cols, dtype)
+    return moe.Checkpoint8(on(at, B.lib().bakron_ck8_bytes(rows, cols), dtype=torch.uint8), rows, cols, dtype)
 
 
 def every_call(at, **other):
@@ -182,6 +182,25 @@ def test_a_workspace_has_all_the_bytes_that_it_counts(monkeypatch):
             ws.at = 0
             with pytest.raises(ValueError, match="contiguous"):
                 call(ws)
+    assert not calls.made
+
+
+def test_a_checkpoint_has_all_the_bytes_that_it_counts(monkeypatch):
+    calls = Calls(monkeypatch)
+    x, whole = on(0, 6, 128), checkpoint(0, 6, 128)
+    need = whole.data.numel()
+    apart = on(0, 2 * need, dtype=torch.uint8)[::2]
+    apart.at = 0
+    for data in (on(0, need - 1, dtype=torch.uint8), on(0, 0, dtype=torch.uint8), apart, on(1, need, dtype=torch.uint8),
+                 torch.zeros(need, dtype=torch.uint8)):
+        bad = B.Checkpoint8(data, 6, 128, BF16)
+        for call in (lambda: B.ck8_pack(x, out=bad), lambda: B.gated_act(x, x, checkpoint=(whole, bad)),
+                     lambda: B.gated_act_grad(x, bad, whole), lambda: B.gated_act_grad(x, whole, bad, out=(x, x))):
+            with pytest.raises(ValueError):
+                call()
+        if data.get_device() != 1:
+            with pytest.raises((ValueError, TypeError)):
+                B.ck8_unpack(bad)
     assert not calls.made
 
 

@@ -212,6 +212,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_place(const int32_t* _
     }
 }
 
+// What a wave's lanes have in LDS before and after, kept apart for the compiler (the
+// LDS itself answers a wave in order).
+__device__ __forceinline__ void row_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 16 lanes a token; its row is put together in LDS (a wave's own part).
 template <class L>
 __global__ __launch_bounds__(256) void k_moe_route_grad(const float* __restrict__ dweights, const float* __restrict__ weights,
@@ -233,11 +242,11 @@ __global__ __launch_bounds__(256) void k_moe_route_grad(const float* __restrict_
         }
         const float d = w * (g - row_sum(id < 0 ? 0.f : w * g));
         for (int e = l; e < E; e += 16) row[e] = 0.f;
-        __builtin_amdgcn_wave_barrier();
+        row_order();
         if (id >= 0) row[id] = d;
-        __builtin_amdgcn_wave_barrier();
+        row_order();
         for (int e = l; e < E; e += 16) dlogits[t * ld + e] = L::down(row[e]);
-        __builtin_amdgcn_wave_barrier();
+        row_order();
     }
 }
 

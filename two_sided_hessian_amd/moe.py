@@ -524,9 +524,12 @@ def _checkpoint(name, ck, rows, cols, dtype, index):
         raise TypeError(f"{name} must be a Checkpoint8")
     if (ck.rows, ck.cols) != (rows, cols) or ck.dtype != dtype:
         raise ValueError(f"{name} must be a checkpoint of {rows} x {cols} values of {dtype}, got {ck!r}")
-    if ck.data.get_device() != index:
+    data = ck.data
+    if data.get_device() != index:
         raise ValueError(f"{name} is on {ck.device}, not on cuda:{index}")
-    return ck.data.data_ptr()
+    if not data.is_contiguous() or data.nbytes < _b.lib().bakron_ck8_bytes(rows, cols):
+        raise ValueError(f"{name} must have the bytes of {rows} x {cols} values, one after the other")
+    return data.data_ptr()
 
 
 def ck8_pack(x, *, out=None, stream=None):
@@ -557,6 +560,9 @@ def ck8_unpack(ck, *, dtype=None, out=None, stream=None):
     if not isinstance(ck, Checkpoint8):
         raise TypeError("ck must be a Checkpoint8")
     index = ck.data.get_device()
+    if index < 0:
+        raise TypeError("ck must be on a CUDA (HIP) device")
+    at = _checkpoint("ck", ck, ck.rows, ck.cols, ck.dtype, index)
     if _device() != index:
         with torch.cuda.device(index):
             return ck8_unpack(ck, dtype=dtype, out=out, stream=stream)
@@ -568,7 +574,7 @@ def ck8_unpack(ck, *, dtype=None, out=None, stream=None):
     ld = _matrix("out", out, ck.cols)
     if out.shape[0] != ck.rows or out.get_device() != index:
         raise ValueError(f"out must be a ({ck.rows}, {ck.cols}) tensor on cuda:{index}")
-    _run("bakron_ck8_unpack", ck.data.data_ptr(), ck.rows, ck.cols, _TYPES3[out.dtype], out.data_ptr(), ld, s)
+    _run("bakron_ck8_unpack", at, ck.rows, ck.cols, _TYPES3[out.dtype], out.data_ptr(), ld, s)
     return out
 
 
