@@ -164,26 +164,42 @@ __global__ __launch_bounds__(512) void k_q4_experts_grad(const uint16_t* __restr
 }
 
 // The sum of `splits` partial results, in order, for the rows that some expert
-// has.
+// has: four columns a thread, the last ones of a row where they are fewer.  (Rows of
+// 4096 x 4096, two parts: 35 us; a column a thread 62.)
 template <class X>
 __global__ __launch_bounds__(256) void k_q4_experts_join(const float* __restrict__ part, int splits, int R,
-                                                         const int32_t* __restrict__ offsets, int E, int m,
+                                                         const int32_t* __restrict__ offsets, int E, int m, int log, int chunks,
                                                          uint16_t* __restrict__ y, int64_t ldy)
 {
-    const int col = blockIdx.y * 256 + threadIdx.x, row = blockIdx.x;
-    if (col >= m || row < offsets[0] || row >= offsets[E]) return;
-    const int64_t all = (int64_t)R * m;
-    const float* p = part + (int64_t)row * m + col;
-    constexpr int U = 8;
-    float v = 0.f;
-    for (int u0 = 0; u0 < splits; u0 += U) {
-        float a[U];
+    typedef f32x4 f32x4_any __attribute__((aligned(4)));
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    const UnitAt at(log, chunks);
+    if (4 * at.u >= m) return;
+    const int col = max(min(4 * at.u, m - 4), 0);   // (what two threads write they write alike)
+    const int64_t all = (int64_t)R * m, first = max(offsets[0], 0), last = min(offsets[E], R);
+    for (int64_t row = first + at.r; row < last; row += at.by) {
+        const float* p = part + row * m + col;
+        uint16_t* to = y + row * ldy + col;
+        constexpr int U = 4;
+        if (col + 4 <= m) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            for (int u0 = 0; u0 < splits; u0 += U) {
+                f32x4 a[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) a[u] = p[min(u0 + u, splits - 1) * all];
+                for (int u = 0; u < U; ++u) a[u] = *reinterpret_cast<const f32x4_any*>(p + min(u0 + u, splits - 1) * all);
 #pragma unroll
-        for (int u = 0; u < U; ++u) v += u0 + u < splits ? a[u] : 0.f;
+                for (int u = 0; u < U; ++u)
+                    if (u0 + u < splits) v += a[u];
+            }
+            *reinterpret_cast<u32x2_any*>(to) = u32x2_any{X::down2(v.x, v.y), X::down2(v.z, v.w)};
+        } else {
+            for (int e = 0; e < m; ++e) {
+                float v = 0.f;
+                for (int u = 0; u < splits; ++u) v += p[u * all + e];
+                to[e] = X::down(v);
+            }
+        }
     }
-    y[row * ldy + col] = X::down(v);
 }
 
 // Zeros in the rows that some expert has.
@@ -442,8 +458,9 @@ struct ExpertsCall {
 template <class X>
 static void experts_join(const ExpertsCall& c, const float* part, int splits, int64_t cols)
 {
-    enqueue(k_q4_experts_join<X>, dim3((unsigned)c.rows, (unsigned)ceil_div(cols, 256)), dim3(256), c.s, part, splits,
-            (int)c.rows, c.offsets, (int)c.E, (int)cols, c.out, c.ldout);
+    const UnitGrid g = unit_grid(c.rows, ceil_div(cols, 4), 0);
+    enqueue(k_q4_experts_join<X>, dim3(g.blocks), dim3(256), c.s, part, splits, (int)c.rows, c.offsets, (int)c.E, (int)cols,
+            g.log, g.chunks, c.out, c.ldout);
 }
 
 template <class X, int WS>
