@@ -11,6 +11,8 @@ its 4-bit codes.
    tokens are decoded through projection and experts (q4_linear, q4_moe).
 4. q4_linear_grad takes an output gradient back through the rounded projection:
    what the Kronecker factors of the layers before it are built from.
+5. The whole prompt goes through the experts (q4_moe_layer), and an output
+   gradient back through them to its tokens and its router.
 
 Random weights and inputs; prints how far the rounded block is from the
 float32 one and from the same block with its weights written out.
@@ -129,8 +131,20 @@ def main(argv=None):
     grad_err = rel(dx, dy.float() @ proj_q)
     factor = B.moment(dx.float())
 
+    # 5: the experts for all of the prompt, forward and backward
+    def through(x, layer):
+        x = x.detach().clone().requires_grad_()
+        out = layer(x, x.float() @ router.float().t())
+        out.backward(dy.to(out.dtype))
+        return out.detach(), x.grad
+    got = through(y, lambda x, logits: B.q4_moe_layer(x, logits, packed["gate"], packed["up"], packed["down"], k))
+    want = through(y.float(), lambda x, _: moe_float(x, router, rounded["gate"], rounded["up"], rounded["down"], k))
+    layer_err, layer_grad_err = (rel(a, b) for a, b in zip(got, want))
+
     res = {"prompt against the rounded weights": prompt_err, "experts against the rounded weights": moe_err,
            "gradient against the rounded weights": grad_err,
+           "expert layer against the rounded weights": layer_err,
+           "its gradient against the rounded weights": layer_grad_err,
            "rounded prompt against float32": rel(y, prompt.float() @ proj.t())}
     for what, v in res.items():
         print(f"{what}: {v:.2e}")

@@ -139,8 +139,8 @@ size_t bakron_q4_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t ffn
  *
  * x          [in]  tokens x hidden, row stride ldx.
  * tokens     [in]  0 <= tokens <= BAKRON_Q4_MOE_MAX_TOKENS (BAKRON_ERR_BAD_SIZE
- *                  beyond: bring longer inputs expert by expert to
- *                  bakron_q4_linear; layer e of a stack starts at e times
+ *                  beyond: bakron_moe.h has the layer for any number; layer
+ *                  e of a stack starts at e times
  *                  bakron_q4_packed_bytes(1, ...)).
  * router     [in]  experts x hidden, contiguous, of x's type.
  * gate, up   [in]  stacks of `experts` packed layers, ffn x hidden.

@@ -15,7 +15,8 @@ namespace bk {
 
 // ------------------------------------------------------------ launches
 //
-// Every kernel is launched through launch().  With a Prof attached (the
+// Kernels are launched through launch(), or through enqueue() where a call has
+// no *_profiled form (KernelKind's numbers are the C ABI's).  With a Prof attached (the
 // *_profiled entry points) each launch carries HIP start/stop events
 // (hipExtLaunchKernelGGL records them around the kernel itself) and the
 // launch's algorithmic flops and bytes; the totals per kernel are read back

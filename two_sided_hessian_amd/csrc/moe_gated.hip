@@ -18,7 +18,9 @@
 // float32 each), a few parts in 10^6 at most where p is far below 1: the results
 // are rounded to 16 bits.
 //
-// HBM bounds all of it, and next the vector instructions.
+// HBM bounds all of it, and next the vector instructions (0.65 of a CU's cycles):
+// 16384 x 14336, forward with checkpoints 332 us, backward 324, 5.7 and 5.8 TB/s.
+// 96 x 1024 without: 2.6 us, a launch and a round trip.
 #include <algorithm>
 
 #include "moe.hpp"

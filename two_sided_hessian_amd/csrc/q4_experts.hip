@@ -10,9 +10,21 @@
 // of every expert, and takes its own by a prefix sum over the 64 lanes; what is
 // past the last block ends there.  A block never holds two experts' rows.
 //
-//   * few rows per expert (decoding): codes are what is read.  k_q4_experts_few
-//     has blocks of up to 32 rows and row tiles of W over workgroups; HBM bounds it.
-//   * many: k_q4_experts and k_q4_experts_grad, tiles of 64 .. 256 rows, MFMAs.
+//   * few rows per expert (decoding): codes are what is read, and HBM bounds it.
+//     k_q4_experts_few has blocks of up to 32 rows and row tiles of W over workgroups: 16
+//     tokens, 6 of 64 experts of 1024 x 2048 in groups of 64: 13.0 us a call, 5.2 TB/s of
+//     what has to move, a large copy's rate.  k_q4_experts_grad_few has blocks of 32 rows
+//     (16) and 128 columns: 16 tokens, 2 of 8 of 14336 x 4096: 55 us (floor 50); tiles of 64
+//     rows took 117.  Blocks of 64 rows, two waves a SIMD: 92 us for 103 at 64 tokens, but
+//     162 for 152 at 128 and 63 for 53 at 512 tokens, 6 of 64 of 2048 x 1024.
+//   * many: k_q4_experts and k_q4_experts_grad, tiles of 64 .. 256 rows, MFMAs.  8192
+//     tokens, 2 of 8 of 14336 x 4096: 1676 us and 31 for the rows' sums, 1150 TFLOP/s, MFMAs
+//     busy 0.63 of a CU's cycles and vector instructions 0.46 (steps change every second
+//     chunk in groups of 128).  Gradient, 2048 tokens: 618 us in two parts and 27 to join
+//     them, MFMAs 0.48, LDS 0.43, vector instructions 0.37, and the rows of tiles
+//     that experts' ends cut.  1024 tokens, 6 of 64 of 2048 x 1024: 74 us a call, one tile
+//     per CU whose 32 chunks take 2.3 us each: LDS 0.50, vector instructions 0.45, MFMAs
+//     0.32, and one workgroup's barriers between them.
 #include <algorithm>
 
 #include "moe.hpp"
@@ -165,7 +177,7 @@ __global__ __launch_bounds__(512) void k_q4_experts_grad(const uint16_t* __restr
 
 // The sum of `splits` partial results, in order, for the rows that some expert
 // has: four columns a thread, the last ones of a row where they are fewer.  (Rows of
-// 4096 x 4096, two parts: 35 us; a column a thread 62.)
+// 4096 x 4096, two parts: 27 us; a column a thread 62.)
 template <class X>
 __global__ __launch_bounds__(256) void k_q4_experts_join(const float* __restrict__ part, int splits, int R,
                                                          const int32_t* __restrict__ offsets, int E, int m, int log, int chunks,

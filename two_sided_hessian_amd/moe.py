@@ -743,8 +743,9 @@ def q4_moe_layer(x, logits, w_gate, w_up, w_down, top_k, *, act="silu"):
     float32, bfloat16 or float16 (tokens without a logit above -inf get zeros);
     w_gate, w_up, w_down: stacks as q4_moe takes them.  Between the calls values
     are rounded to x's type.  Autograd: with respect to x and logits, the inner
-    activations kept in 8 bits.  (Up to 64 tokens without a gradient, q4_moe does
-    the same in three launches.)"""
+    activations kept in 8 bits.  (q4_moe has its router inside, three launches and no
+    gradient: for one token, 2 of 8 experts of 14336 x 4096, 46 us and 54 here; 16: 185 and
+    173; 64: 335 and 232.)"""
     if not all(isinstance(w, Q4Weight) for w in (w_gate, w_up, w_down)):
         raise TypeError("w_gate, w_up and w_down must be Q4Weights (q4_pack)")
     E, f, h = w_gate.count, w_gate.m, w_gate.n

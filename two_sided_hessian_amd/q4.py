@@ -43,8 +43,8 @@ class Q4Weight:
     """One layer (count 1) or a stack of ``count`` layers of m x n in the
     packed layout, with group_size columns per grid (None: one grid per row).
     ``data`` is the device buffer (uint8) that holds it.  ``w[e]`` is layer e of
-    a stack alone, on the same memory: what q4_linear takes (an expert layer
-    for more tokens than q4_moe does goes expert by expert)."""
+    a stack alone, on the same memory: what q4_linear takes (q4_experts takes the
+    stack as it is)."""
 
     __slots__ = ("data", "count", "m", "n", "group_size", "_group")
 
@@ -309,7 +309,8 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
     layer's output, the chosen experts (int32 tokens x top_k, largest logit
     first) and their shares (float32).  ``out``: a dict of the three to write
     to; ``ws``: a workspace of q4_moe_workspace_bytes.  It has no gradient:
-    x and router that require one are refused unless under torch.no_grad()."""
+    x and router that require one are refused unless under torch.no_grad()
+    (q4_moe_layer: any number of tokens, with gradients)."""
     if not isinstance(w_gate, Q4Weight):
         raise TypeError("w_gate must be a Q4Weight (q4_pack)")
     f, h, E = w_gate.m, w_gate.n, w_gate.count
