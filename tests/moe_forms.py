@@ -5,7 +5,7 @@ from q4_forms import ceil_div
 
 FEW_MEAN = 48
 PRODUCT = [(256, 256, (128.0, 80.0, 56.0)), (128, 128, (39.0, 28.0, 28.0)), (64, 128, (28.0, 28.0, 28.0))]
-GRAD = [(256, 256, (130.0, 88.0, 64.0))]
+GRAD = [(256, 256, (130.0, 88.0, 64.0)), (128, 128, (44.0, 32.0, 32.0))]
 
 
 def choose(shapes, R, E, cols, depth, deepest):
@@ -41,12 +41,12 @@ def experts_form(R, E, m, n):
 
 
 def experts_grad_form(R, E, m, n, group):
-    """q4_experts_grad: ("few" or "tiles", the workgroups that share a block's depth)."""
+    """q4_experts_grad: ("few" or a tile's rows, the workgroups that share a block's depth)."""
     best = choose(GRAD, R, E, n, m, min(16, ceil_div(m, 64) // 2))
     rows, some = 16 if group // 64 % 2 else 32, min(R, E)
     blocks = max(some, R // rows + some // 2)
     groups = blocks * ceil_div(n, 128)
     splits = max(1, min(16, 512 // groups, ceil_div(m, 32) // 16))
-    if blocks * float(m) * n / ((4.5e6 if rows == 16 else 6.0e6) * min(1.0, groups * splits / 512.0)) <= 1.0 + best[3]:
+    if blocks * float(m) * n / ((4.2e6 if rows == 16 else 5.6e6) * min(1.0, groups * splits / 512.0)) <= 3.0 + best[3]:
         return "few", splits
-    return "tiles", best[2]
+    return best[0], best[2]

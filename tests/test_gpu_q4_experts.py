@@ -85,7 +85,8 @@ SHAPES = [(1, 1, 1, 1, 0), (1, 8, 130, 300, 64), (6, 64, 33, 515, 192), (16, 5, 
 GRADS = [(1, 1, 1, 1, 0), (3, 8, 130, 300, 64), (6, 64, 515, 33, 0), (96, 3, 64, 130, 64), (300, 256, 65, 265, 64), (17, 4, 31, 40, 0),
          (40, 2, 1100, 300, 128), (9, 3, 5000, 70, 64), (200, 8, 2090, 400, 0), (90, 40, 300, 700, 192), (33, 1, 700, 129, 256),
          (4980, 40, 30, 581, 192), (5260, 40, 337, 8, 64), (70, 1, 264, 100, 64), (7801, 3, 49, 483, 192), (2189, 8, 66, 3491, 0), (4000, 16, 300, 2500, 128),
-         (1558, 24, 64, 2262, 64), (616, 3, 717, 96, 64), (1200, 3, 1030, 1300, 64)]
+         (1558, 24, 64, 2262, 64), (616, 3, 717, 96, 64), (1200, 3, 1030, 1300, 64), (8004, 24, 40, 1755, 64), (6734, 16, 64, 2242, 0),
+         (5559, 3, 14462, 129, 0), (92, 3, 560, 95, 192), (107, 3, 412, 376, 192), (524, 16, 428, 127, 64), (4096, 2, 14336, 130, 128)]
 
 
 def test_the_shapes_reach_every_form():
@@ -95,7 +96,7 @@ def test_the_shapes_reach_every_form():
     assert forms >= {(256, False, False, a) for a in (True, False)}
     assert forms >= {(128, shared, False, a) for shared in (True, False) for a in (True, False)}
     assert forms >= {(64, shared, a, a) for shared in (True, False) for a in (True, False)}
-    assert {(f, s > 1) for f, s in (experts_grad_form(*s) for s in GRADS)} == {(f, s) for f in ("few", "tiles") for s in (True, False)}
+    assert {(f, s > 1) for f, s in (experts_grad_form(*s) for s in GRADS)} == {(f, s) for f in ("few", 256, 128) for s in (True, False)}
     # few rows: blocks of up to 16 and 32 of them, grids that end inside a block of columns
     # or do not, an even and an odd number of row tiles, and a last step that is cut
     few = [s for s in GRADS if experts_grad_form(*s)[0] == "few"]
@@ -103,10 +104,10 @@ def test_the_shapes_reach_every_form():
     rest = {min((c - 1) % 32 // 16, 1) for R, E, m, n, g in few if g // 64 % 2 == 0 for c in np.diff(spread(R, E, R + n)) if c}
     assert rest == {0, 1}
     # blocks of every number of rows, behind whole ones and alone
-    for shapes, most in ((SHAPES, 256), (SHAPES, 128), (SHAPES, 64), (GRADS, 256)):
+    for shapes, most in ((SHAPES, 256), (SHAPES, 128), (SHAPES, 64), (GRADS, 256), (GRADS, 128)):
         rest = set()
         for R, E, m, n, g in shapes:
-            if experts_grad_form(R, E, m, n, g)[0] == "tiles" if shapes is GRADS else experts_form(R, E, m, n)[0] == most:
+            if (experts_grad_form(R, E, m, n, g) if shapes is GRADS else experts_form(R, E, m, n))[0] == most:
                 c = np.diff(spread(R, E, R + n))
                 rest |= {(1 if r <= 64 else 2 if r <= 128 else 4, x >= most) for x in c for r in [x % most] if r}
         assert rest == {(b, more) for b in (1, 2, 4) if 32 * b < most for more in (True, False)}, most
@@ -126,7 +127,8 @@ def test_gradients_match_their_formula(R, E, m, n, group, dtype):
 
 @pytest.mark.parametrize("grad", [False, True], ids=["product", "grad"])
 @pytest.mark.parametrize("R,E,m,n,group,pad", [(40, 4, 100, 130, 64, 0), (40, 4, 100, 130, 64, 3), (900, 4, 200, 192, 64, 0),
-                                               (900, 4, 200, 192, 64, 8), (900, 4, 200, 193, 0, 5), (150, 2, 320, 1000, 128, 1)])
+                                               (900, 4, 200, 192, 64, 8), (900, 4, 200, 193, 0, 5), (150, 2, 320, 1000, 128, 1),
+                                               (1500, 4, 1280, 1000, 64, 8), (1500, 4, 1300, 1000, 64, 1)])
 def test_rows_outside_the_experts_and_slices(R, E, m, n, group, pad, grad):
     for dtype in TYPES:
         check(R, E, m, n, group, dtype, grad, 7, spread(R, E, 3, first=5, tail=11), pad=pad, out_pad=pad)

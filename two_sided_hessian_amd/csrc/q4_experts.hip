@@ -16,15 +16,15 @@
 //     what has to move, a large copy's rate.  k_q4_experts_grad_few has blocks of 32 rows
 //     (16) and 128 columns: 16 tokens, 2 of 8 of 14336 x 4096: 55 us (floor 50); tiles of 64
 //     rows took 117.  Blocks of 64 rows, two waves a SIMD: 92 us for 103 at 64 tokens, but
-//     162 for 152 at 128 and 63 for 53 at 512 tokens, 6 of 64 of 2048 x 1024.
+//     162 for 139 at 128 and 63 for 54 at 512 tokens, 6 of 64 of 2048 x 1024.
 //   * many: k_q4_experts and k_q4_experts_grad, tiles of 64 .. 256 rows, MFMAs.  8192
 //     tokens, 2 of 8 of 14336 x 4096: 1676 us and 31 for the rows' sums, 1150 TFLOP/s, MFMAs
 //     busy 0.63 of a CU's cycles and vector instructions 0.46 (steps change every second
 //     chunk in groups of 128).  Gradient, 2048 tokens: 618 us in two parts and 27 to join
 //     them, MFMAs 0.48, LDS 0.43, vector instructions 0.37, and the rows of tiles
-//     that experts' ends cut.  1024 tokens, 6 of 64 of 2048 x 1024: 74 us a call, one tile
-//     per CU whose 32 chunks take 2.3 us each: LDS 0.50, vector instructions 0.45, MFMAs
-//     0.32, and one workgroup's barriers between them.
+//     that experts' ends cut.  1024 tokens, 6 of 64 of 2048 x 1024, in tiles of
+//     128 x 128, two workgroups a CU: 65 us with 40 to 230 rows each, 78 with 4 to 490, whose
+//     700 tiles are 1.4 times what fits at once.
 #include <algorithm>
 
 #include "moe.hpp"
@@ -159,20 +159,21 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_experts(const uint16_t* __re
     else if (TA > 2) prompt_tile<X, 1, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
 }
 
-template <class X>
-__global__ __launch_bounds__(512) void k_q4_experts_grad(const uint16_t* __restrict__ dy, int64_t lddy, int R,
-                                                         const int32_t* __restrict__ offsets, int E, Q4Layer stack,
-                                                         int64_t layer_bytes, uint16_t* __restrict__ dx, int64_t lddx,
-                                                         int nj, float* __restrict__ part)
+// Tiles of up to 64 TA rows by 64 WJ columns.
+template <class X, int TA, int WJ>
+__global__ __launch_bounds__(128 * WJ, 2) void k_q4_experts_grad(const uint16_t* __restrict__ dy, int64_t lddy, int R,
+                                                                 const int32_t* __restrict__ offsets, int E, Q4Layer stack,
+                                                                 int64_t layer_bytes, uint16_t* __restrict__ dx, int64_t lddx,
+                                                                 int nj, float* __restrict__ part)
 {
-    constexpr int BYTES = std::max(std::max(Grad<4>::LDS, Grad<2>::LDS), Grad<1>::LDS);
+    constexpr int HALF = TA / 2, BYTES = std::max(std::max(Grad<TA, WJ>::LDS, Grad<HALF, WJ>::LDS), Grad<1, WJ>::LDS);
     ExpertRows rows;
     int bj, cls;
-    if (!expert_tile<4>(offsets, E, R, nj, rows, bj, cls)) return;
+    if (!expert_tile<TA>(offsets, E, R, nj, rows, bj, cls)) return;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
-    if (cls == 0) grad_tile<X, 4, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
-    else if (cls == 1) grad_tile<X, 2, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
-    else grad_tile<X, 1, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    if (cls == 0) grad_tile<X, TA, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    else if (cls == 1) grad_tile<X, HALF, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    else if (TA > 2) grad_tile<X, 1, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
 }
 
 // The sum of `splits` partial results, in order, for the rows that some expert
@@ -183,7 +184,6 @@ __global__ __launch_bounds__(256) void k_q4_experts_join(const float* __restrict
                                                          const int32_t* __restrict__ offsets, int E, int m, int log, int chunks,
                                                          uint16_t* __restrict__ y, int64_t ldy)
 {
-    typedef f32x4 f32x4_any __attribute__((aligned(4)));
     typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
     const UnitAt at(log, chunks);
     if (4 * at.u >= m) return;
@@ -431,23 +431,32 @@ static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int 
 static ExpertsPlan experts_grad_plan(int64_t R, int64_t E, int64_t m, int64_t n, int gb)
 {
     ExpertsPlan p{};
-    static constexpr ExpertShape shapes[] = {{256, 256, {130.0, 88.0, 64.0}}};   // as in q4_grad.hip
+    // 256 x 256 as in q4_grad.hip.  128 x 128: two workgroups of a CU, which take turns with
+    // its units where a lone one of eight waves leaves them idle at its barriers, but twice
+    // the expansion and LDS writes for a product: where experts have one to two hundred rows, or
+    // there are few tiles (1024 tokens, 6 of 64 of 2048 x 1024, 40 to 230 rows each: 65 us, and
+    // 73 in 256 x 256; 4 to 490: 79 and 77;
+    // 900, 7 of 43 of 1152 x 320: 23 and 32; 512, one of 4096 x 4096: 49 and 60; 2048, 2 of 8
+    // of 14336 x 4096: 685 and 606).
+    static constexpr ExpertShape shapes[] = {{256, 256, {130.0, 88.0, 64.0}}, {128, 128, {44.0, 32.0, 32.0}}};
     const ExpertsChoice c = experts_choose(shapes, R, E, n, m, std::min<int64_t>(16, ceil_div(m, 64) / 2));
-    // Few rows: a block's codes at 6 T/s however many rows it has (4.5 where its columns
-    // have two grids), where there are two workgroups for every CU; the rows of W are shared out towards that, four steps at
-    // least for every wave.  (6 of 64 experts of 2048 x 1024 in groups of 128, 48 rows each:
-    // 51 us, in tiles 62; 96: 88 and 69; groups of 64, 24 rows: 61 and 48; 7 of 43 of 1152 x
-    // 320, 70 rows each: 18 and 31.)
+    // Few rows: a block's codes at 5.6 T/s however many rows it has (4.2 where its columns
+    // have two grids), where there are two workgroups for every CU; the rows of W are shared
+    // out towards that, four steps at least for every wave.  (6 of 64 experts of 2048 x 1024
+    // in groups of 128, 48 rows each: 54 us, in tiles 60; 96: 91 and 65; groups of 64, 32
+    // rows: 67 and 48.  2 of 8 of 5000 x 3500, 10 rows each: 31 and 65, 100: 101 and 85.)
     const int64_t blocks = blocks_about(R, E, grad_few_rows(gb)), groups = blocks * ceil_div(n, kQ4Cols);
     const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({16, 512 / groups, ceil_div(m, 32) / (4 * kGradFewWaves)}));
-    p.few = blocks * (double)m * n / ((gb % 2 ? 4.5e6 : 6.0e6) * std::min(1.0, groups * splits / 512.0)) <= 1.0 + c.us;
+    p.few = blocks * (double)m * n / ((gb % 2 ? 4.2e6 : 5.6e6) * std::min(1.0, groups * splits / 512.0)) <= 3.0 + c.us;
     if (p.few) {
         p.splits = (int)splits;
         p.bytes = p.splits > 1 ? align_up((size_t)p.splits * R * n * 4) : 0;
         return p;
     }
     p.splits = c.splits;
-    p.tiles = blocks_most(R, E, 256);
+    p.TA = shapes[c.shape].rows / 64;
+    p.WR = shapes[c.shape].cols / 64;
+    p.tiles = blocks_most(R, E, shapes[c.shape].rows);
     p.ldc = ceil_div(m, 64) * 64;
     p.part = align_up((size_t)R * p.ldc * 2);
     p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * R * n * 4) : 0);
@@ -544,9 +553,10 @@ static void experts_grad_run(const ExpertsCall& c)
         dy = reinterpret_cast<const uint16_t*>(c.ws);
         lddy = p.ldc;
     }
-    const int nj = (int)ceil_div(w.n, 256);
-    enqueue(k_q4_experts_grad<X>, dim3((unsigned)(p.tiles * nj), (unsigned)p.splits), dim3(512), c.s, dy, lddy, (int)c.rows,
-            c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, nj, reinterpret_cast<float*>(c.ws + p.part));
+    const int nj = (int)ceil_div(w.n, 64 * p.WR);
+    enqueue(p.TA == 4 ? k_q4_experts_grad<X, 4, 4> : k_q4_experts_grad<X, 2, 2>, dim3((unsigned)(p.tiles * nj), (unsigned)p.splits),
+            dim3(128 * p.WR), c.s, dy, lddy, (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, nj,
+            reinterpret_cast<float*>(c.ws + p.part));
     if (p.splits > 1) experts_join<X>(c, reinterpret_cast<const float*>(c.ws + p.part), p.splits, w.n);
 }
 

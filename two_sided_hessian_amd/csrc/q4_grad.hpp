@@ -7,23 +7,25 @@
 
 namespace bk {
 
-template <int TA>
+template <int TA, int WJ = 4>
 struct Grad {
     static constexpr int BT = 64 * TA;              // tokens of a workgroup
-    static constexpr int BJ = 256;                  // columns of a workgroup
+    static constexpr int BJ = 64 * WJ;              // columns of a workgroup of 2 WJ waves
     static constexpr int XBUF = BT * 128;           // bytes of a 64-row chunk of dy
     static constexpr int PITCH = 144;               // bytes of a column's 64 rows in LDS: 9 x 16, spreads the banks
     static constexpr int WBUF = BJ * PITCH;
     // Small tiles: a chunk is shorter than a load's latency, so codes and grids
     // come by direct loads too, some chunks ahead.  TA = 4: a chunk outlasts a
-    // load, and LDS is what bounds it; codes and grids come to registers.
+    // load, and LDS is what bounds it; codes and grids come to registers.  WJ = 2:
+    // one chunk less ahead leaves room for two workgroups of a CU.
     static constexpr bool RAW = TA < 4;
-    static constexpr int AHEAD = TA == 4 ? 1 : TA == 2 ? 2 : 3;
+    static constexpr int AHEAD = TA == 4 ? 1 : (TA == 2 ? 2 : 3) - (WJ == 2);
     static constexpr int NX = AHEAD + 1;
-    static constexpr int XLOADS = BT / 64;
+    static constexpr int XLOADS = BT / 8 / (2 * WJ);
     static constexpr int LOADS = XLOADS + (RAW ? 2 : 0);
     static constexpr int TILE = 1040;               // bytes of a code block in LDS: 65 x 16, spreads the banks
-    static constexpr int RAWBUF = RAW ? 8 * TILE + 2048 : 0;   // codes, then grids [row tile][64 columns][16] of a chunk
+    static constexpr int GRIDS = 2 * WJ * TILE;     // codes [128 columns][row tile], then grids [row tile][64 columns][16]
+    static constexpr int RAWBUF = RAW ? GRIDS + 512 * WJ : 0;   // of a chunk
     static constexpr int WEIGHTS = NX * XBUF, RAWS = WEIGHTS + 2 * WBUF, LDS = RAWS + NX * RAWBUF;
 };
 
@@ -43,22 +45,23 @@ struct GradRaw {
     f32x4 g[2];   // (s, z) of rows 0, 1 and 2, 3
 };
 
-// One output tile: tokens t0 .. min(t0 + 64 TA, T) - 1 by columns 256 bj ...
+// One output tile: tokens t0 .. min(t0 + 64 TA, T) - 1 by columns 64 WJ bj ...
 // blockIdx.y of gridDim.y shares the rows of W; more than one of them writes
 // float32 partial sums to part[blockIdx.y][token][column], part_rows tokens a part,
 // instead of dx.
-template <class X, int TA, int BYTES = Grad<TA>::LDS>
+template <class X, int TA, int WJ = 4, int BYTES = Grad<TA, WJ>::LDS>
 __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64_t lddy, int t0, int T,
                                           const Q4Layer& w, uint16_t* __restrict__ dx, int64_t lddx, int bj,
                                           float* __restrict__ part, int64_t part_rows)
 {
-    typedef Grad<TA> P;
+    typedef Grad<TA, WJ> P;
     typedef typename X::vec vec;
+    constexpr int BLOCKS = WJ / 2;   // of 128 columns
     static_assert(BYTES >= P::LDS);
     char(&lds)[BYTES] = tile_lds<BYTES>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, ml = lane & 31;
-    const int wt = wave >> 2, wj = wave & 3;
+    const int wt = wave / WJ, wj = wave % WJ;
     const int j0 = bj * P::BJ;
     const int all = (w.m + 63) / 64;
     const int c0 = all * blockIdx.y / gridDim.y, c1 = all * (blockIdx.y + 1) / gridDim.y;   // this workgroup's chunks
@@ -68,7 +71,7 @@ __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64
         return unit > 0.f ? unit * X::kUnit : 1.f;
     };
     const int jw = j0 + wj * 64;   // the wave's columns, of one group
-    const float unit = unit_of(min((4 * bj + wj) / w.gb, w.G - 1));
+    const float unit = unit_of(min((WJ * bj + wj) / w.gb, w.G - 1));
 
     // staging of dy
     const Rsrc x = buffer_of(dy + (int64_t)t0 * lddy, 0x7FFFFFFFu);
@@ -81,25 +84,25 @@ __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64
     // load i of chunk c of dy, or (i = XLOADS, XLOADS + 1) of the codes and grids
     // of chunk c + 1, which is expanded a chunk before its products; row tiles
     // beyond RT repeat the last (dy is zero there)
-    const uint32_t g_at = 128 * min((4 * bj + 2 * (wave & 1) + (lane >> 5)) / w.gb, w.G - 1) + 4 * (lane & 31);
+    const uint32_t g_at = 128 * min((WJ * bj + 2 * (wave % BLOCKS) + (lane >> 5)) / w.gb, w.G - 1) + 4 * (lane & 31);
     auto stage = [&](int i, int c, int buf) {
         if (i < P::XLOADS) {
             load_lds16(x, x_at[i], 128 * min(c, c1 - 1), lds + buf * P::XBUF + (wave * P::XLOADS + i) * 1024);
         } else if (i == P::XLOADS) {
             const int64_t rt = min(4 * (c + 1) + (wave & 3), w.RT - 1);
-            load_lds16(buffer_of(w.codes + (rt * w.KB + min(2 * bj + (wave >> 2), w.KB - 1)) * 64, 1024), 16 * lane, 0,
+            load_lds16(buffer_of(w.codes + (rt * w.KB + min(BLOCKS * bj + (wave >> 2), w.KB - 1)) * 64, 1024), 16 * lane, 0,
                        lds + P::RAWS + buf * P::RAWBUF + wave * P::TILE);
         } else {
-            const int64_t rt = min(4 * (c + 1) + (wave >> 1), w.RT - 1);
+            const int64_t rt = min(4 * (c + 1) + wave / BLOCKS, w.RT - 1);
             load_lds4(buffer_of(w.grid + rt * w.G * 16, 0x7FFFFFFFu), g_at, 0,
-                      lds + P::RAWS + buf * P::RAWBUF + 8 * P::TILE + 256 * wave);
+                      lds + P::RAWS + buf * P::RAWBUF + P::GRIDS + 256 * wave);
         }
     };
 
     // expansion: rows 4 a .. 4 a + 3 of the chunk, the eight columns of dword d
     // of unit column q of block kb
     const int a4 = lane & 15, d = lane >> 4, q = wave & 3;
-    const int kb = min(2 * bj + (wave >> 2), w.KB - 1);
+    const int kb = min(BLOCKS * bj + (wave >> 2), w.KB - 1);
     const int g = min((2 * kb + (d >> 1)) / w.gb, w.G - 1);
     const float down = 1.f / unit_of(g);
     const int col = 128 * (wave >> 2) + 64 * (d >> 1) + 16 * q + 8 * (d & 1);
@@ -117,7 +120,7 @@ __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64
         v.g[1] = *reinterpret_cast<const f32x4*>(grid + 16);
     };
     const uint32_t raw_code = P::RAWS + (4 * (wave >> 2) + (a4 >> 2)) * P::TILE + 256 * q + 64 * (a4 & 3) + 4 * d;
-    const uint32_t raw_grid = P::RAWS + 8 * P::TILE + 512 * (a4 >> 2) + 128 * (2 * (wave >> 2) + (d >> 1)) + 32 * (a4 & 3);
+    const uint32_t raw_grid = P::RAWS + P::GRIDS + 128 * WJ * (a4 >> 2) + 128 * (2 * (wave >> 2) + (d >> 1)) + 32 * (a4 & 3);
     auto take = [&](int buf, GradRaw& v) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

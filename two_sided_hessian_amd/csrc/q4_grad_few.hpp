@@ -35,6 +35,8 @@ constexpr int kGradFewPitch = 132;                   // floats of a row of dx in
 constexpr int kGradFewJoin = 16 * kGradFewPitch * 4;
 constexpr int kGradFewTake = 8;                      // steps after which the second sum comes off
 
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
 template <int LEFT>
 __device__ __forceinline__ void wait_loads()
 {
@@ -280,9 +282,15 @@ __device__ __forceinline__ void grad_few(const uint16_t* __restrict__ dy, int64_
             }
             if (t >= n || j >= w.n) continue;
             if (part) {
+                float* p = part + (int64_t)(t0 + t) * ldp + j;
+                if (j + 8 <= w.n) {
+                    *reinterpret_cast<f32x4_any*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4_any*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (j + e < w.n) part[(int64_t)(t0 + t) * ldp + j + e] = v[e];
+                    for (int e = 0; e < 8; ++e)
+                        if (j + e < w.n) p[e] = v[e];
+                }
             } else {
                 store8(dx + (int64_t)(t0 + t) * lddx, j, w.n, down8<X>(v));
             }
