@@ -9,8 +9,8 @@ GRAD = [(256, 256, (130.0, 88.0, 64.0)), (128, 128, (44.0, 32.0, 32.0))]
 
 
 def choose(shapes, R, E, cols, depth, deepest):
-    """(rows, columns) of the largest tile, the workgroups that share its depth, and
-    the time that is expected of it."""
+    """(rows, columns) of the largest tile, the workgroups that share its depth ("tail":
+    only those of the last tiles), and the time that is expected of it."""
     some, best = min(R, E), None
     for rows, width, us in shapes:
         work = tile = 0.0
@@ -27,7 +27,26 @@ def choose(shapes, R, E, cols, depth, deepest):
             if best is None or t < best[3]:
                 best = rows, width, s, t
             s += 1
-    return best
+        if rows == 256:
+            us256, whole, few = us[0] * depth / 4096, work, work <= 3.5 * tile
+    t = whole * depth / 4096 + 0.1 * us256 + 20.0
+    return (256, 256, "tail", t) if us256 >= 40.0 and few and t < best[3] else best
+
+
+def tail(counts, cols, us, deepest):
+    """Of a product whose tail is shared out, experts' rows given: whole tiles, the tiles
+    of the tail, the parts of each, and which bodies (256, 128, 64 rows) they have."""
+    rest = [c % 256 for c in counts]
+    bodies = [256] * sum(c // 256 + (c % 256 > 128) for c in counts) + [128] * sum(64 < c <= 128 for c in rest) + \
+        [64] * sum(0 < c <= 64 for c in rest)
+    nc = ceil_div(cols, 256)
+    tiles, us = len(bodies) * nc, int(100 * us)
+    left, parts, best = tiles % 256, 1, us
+    for s in range(2, deepest + 1):
+        t = ceil_div(left * s, 256) * us // s + 200 + 9 * left * s
+        if left * s <= 512 and t < best:
+            best, parts = t, s
+    return tiles - left, left, parts, {bodies[i // nc] for i in range(tiles - left, tiles)}
 
 
 def experts_form(R, E, m, n):

@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import two_sided_hessian_amd as B
-from moe_forms import experts_form, experts_grad_form
+from moe_forms import experts_form, experts_grad_form, tail
 from test_gpu_q4 import DEV, LINEAR, TINY, U, close, make_layer, pack, rms, tokens, weights64
 
 pytestmark = pytest.mark.gpu
@@ -149,6 +149,33 @@ def test_more_blocks_of_rows_than_65535():
     assert experts_grad_form(R, E, m, n, 0)[0] == "few" and R // 32 > 65535
     for grad in (False, True):
         check(R, E, m, n, 0, torch.bfloat16, grad, 1, np.array([0, 1_500_001, R]))
+
+
+# experts' rows, columns of the result, depth: whole rounds of 256 tiles, and a rest of
+# tiles for 256, 128, and 64 rows; less than a round, which is not worth sharing out
+TAILS = [((2200,), 8300, 3500, {256}), ((0, 1900), 8300, 3520, {128}), ((1796, 0), 9300, 3550, {256, 64}), ((7000,), 1700, 3500, {256, 128})]
+
+
+@pytest.mark.parametrize("grad", [False, True], ids=["product", "grad"])
+@pytest.mark.parametrize("case", range(4))
+def test_the_last_tiles_are_shared_out(case, grad):
+    counts, cols, depth, bodies = TAILS[case]
+    m, n = (depth, cols) if grad else (cols, depth)
+    R, E = sum(counts) + 3, len(counts)
+    assert (experts_grad_form(R, E, m, n, 64) if grad else experts_form(R, E, m, n))[:2] == (256, "tail")
+    whole, left, parts, found = tail(counts, cols, (130.0 if grad else 128.0) * depth / 4096,
+                                     min(16, -(-depth // 64) // 2) if grad else min(8, -(-depth // 128) // 2))
+    assert found == bodies and left and (whole > 0 and parts > 1 if case < 3 else whole == 0 and parts == 1)
+    check(R, E, m, n, 64, TYPES[case % 2], grad, case, np.concatenate(([0], np.cumsum(counts))))
+    w = pack(*make_layer(m, n, 64, 1, lead=(E,)), 64)
+    call = B.q4_experts_grad if grad else B.q4_experts
+    x, out = torch.ones((R, depth), dtype=TYPES[0], device=DEV), torch.full((R, cols), 3.0, dtype=TYPES[0], device=DEV)
+    call(x, w, torch.zeros(E + 1, dtype=torch.int32, device=DEV), out=out)
+    assert (out == 3).all()
+    big = torch.tensor([R, 0, 2 ** 31 - 1], dtype=torch.int32, device=DEV)[-E - 1:]   # no offsets: within the rows all the same
+    wide = torch.full((R + 2, cols), 3.0, dtype=TYPES[0], device=DEV)
+    call(x, w, big, out=wide[1:-1])
+    assert (wide[0] == 3).all() and (wide[-1] == 3).all()
 
 
 @pytest.mark.parametrize("grad", [False, True], ids=["product", "grad"])

@@ -20,9 +20,9 @@
 //   * many: k_q4_experts and k_q4_experts_grad, tiles of 64 .. 256 rows, MFMAs.  8192
 //     tokens, 2 of 8 of 14336 x 4096: 1676 us and 31 for the rows' sums, 1150 TFLOP/s, MFMAs
 //     busy 0.63 of a CU's cycles and vector instructions 0.46 (steps change every second
-//     chunk in groups of 128).  Gradient, 2048 tokens: 618 us in two parts and 27 to join
-//     them, MFMAs 0.48, LDS 0.43, vector instructions 0.37, and the rows of tiles
-//     that experts' ends cut.  1024 tokens, 6 of 64 of 2048 x 1024, in tiles of
+//     chunk in groups of 128).  Gradient, 2048 tokens: 555 us and 14 to join the
+//     tiles that are shared out, MFMAs 0.49, LDS 0.45, vector instructions 0.37, and the rows
+//     of tiles that experts' ends cut.  1024 tokens, 6 of 64 of 2048 x 1024, in tiles of
 //     128 x 128, two workgroups a CU: 65 us with 40 to 230 rows each, 78 with 4 to 490, whose
 //     700 tiles are 1.4 times what fits at once.
 #include <algorithm>
@@ -92,52 +92,113 @@ __device__ __forceinline__ int expert_at(const ExpertLane& lane, int l, int& k, 
     return u;
 }
 
-// The tile of this workgroup.  An expert's rows go into blocks of 64 TA, the last
-// one cut; what is cut takes a body for 128 or 64 rows where that is enough.  The
-// order of tiles is that of their cost, bodies for more rows first, so that the
-// short ones fill up what the long ones leave; `cls` is 0 for 64 TA rows, 1 for half
-// of that, 2 for a quarter.  nc: tiles beside each other.  A wave's work, the same
-// in every wave.
+// The tiles of a launch.  An expert's rows go into blocks of 64 TA, the last one cut;
+// what is cut takes a body for 128 or 64 rows where that is enough.  The order of
+// tiles is that of their cost, bodies for more rows first, so that the short ones
+// fill up what the long ones leave; `cls` is 0 for 64 TA rows, 1 for half of that, 2
+// for a quarter.  nc: tiles beside each other.  A wave's work, the same in every wave.
 template <int TA>
-__device__ __forceinline__ bool expert_tile(const int32_t* __restrict__ offsets, int E, int R, int nc, ExpertRows& rows, int& bc,
-                                            int& cls)
-{
-    constexpr int BT = 64 * TA;
-    const ExpertLane lane(offsets, E, R);
-    const auto big = [](int c) { return c / BT + (TA == 1 ? c % BT > 0 : c % BT > BT / 2); };
-    const auto half = [](int c) { return (int)(TA > 1 && c % BT > BT / 4 * (TA / 4) && c % BT <= BT / 2); };
-    const auto quarter = [](int c) { return (int)(TA == 4 && c % BT > 0 && c % BT <= 64); };
-    int bigs = 0, rest = 0;   // rest: halves, and quarters in the upper 16 bits
+struct ExpertTiles {
+    static constexpr int BT = 64 * TA;
+    ExpertLane lane;
+    int bigs, rest, bigs_upto, rest_upto;   // rest: halves, and quarters in the upper 16 bits
+    int nb, nh, nq;
+
+    static __device__ __forceinline__ int big(int c) { return c / BT + (TA == 1 ? c % BT > 0 : c % BT > BT / 2); }
+    static __device__ __forceinline__ int half(int c) { return TA > 1 && c % BT > BT / 4 * (TA / 4) && c % BT <= BT / 2; }
+    static __device__ __forceinline__ int quarter(int c) { return TA == 4 && c % BT > 0 && c % BT <= 64; }
+
+    __device__ __forceinline__ ExpertTiles(const int32_t* __restrict__ offsets, int E, int R) : lane(offsets, E, R), bigs(0), rest(0)
+    {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) bigs += big(lane.rows(u)), rest += half(lane.rows(u)) | quarter(lane.rows(u)) << 16;
-    const int bigs_upto = lanes_upto(bigs), rest_upto = lanes_upto(rest);
-    const int nb = __builtin_amdgcn_readlane(bigs_upto, 63), nh = __builtin_amdgcn_readlane(rest_upto, 63) & 0xFFFF,
-              nq = __builtin_amdgcn_readlane(rest_upto, 63) >> 16;
-    int64_t b = blockIdx.x;
-    int bt;
-    if (b < (int64_t)nb * nc) {
-        cls = 0;
-        tile_at((unsigned)b, nb, nc, bt, bc);
-        const int l = lane_of(bigs_upto, bigs, bt);
-        expert_at(lane, l, bt, big, rows);
-        rows.t0 += bt * BT;
+        for (int u = 0; u < 4; ++u) bigs += big(lane.rows(u)), rest += half(lane.rows(u)) | quarter(lane.rows(u)) << 16;
+        bigs_upto = lanes_upto(bigs);
+        rest_upto = lanes_upto(rest);
+        nb = __builtin_amdgcn_readlane(bigs_upto, 63);
+        nh = __builtin_amdgcn_readlane(rest_upto, 63) & 0xFFFF;
+        nq = __builtin_amdgcn_readlane(rest_upto, 63) >> 16;
+    }
+    __device__ __forceinline__ int64_t count(int nc) const { return (int64_t)(nb + nh + nq) * nc; }
+    __device__ __forceinline__ bool find(int64_t b, int nc, ExpertRows& rows, int& bc, int& cls) const
+    {
+        int bt;
+        if (b < (int64_t)nb * nc) {
+            cls = 0;
+            tile_at((unsigned)b, nb, nc, bt, bc);
+            const int l = lane_of(bigs_upto, bigs, bt);
+            expert_at(lane, l, bt, big, rows);
+            rows.t0 += bt * BT;
+            return true;
+        }
+        b -= (int64_t)nb * nc;
+        if (b < nh * nc) {
+            cls = 1;
+            tile_at((unsigned)b, nh, nc, bt, bc);
+            const int l = lane_of(rest_upto & 0xFFFF, rest & 0xFFFF, bt);
+            expert_at(lane, l, bt, half, rows);
+        } else {
+            b -= nh * nc;
+            if (b >= nq * nc) return false;
+            cls = 2;
+            tile_at((unsigned)b, nq, nc, bt, bc);
+            const int l = lane_of(rest_upto >> 16, rest >> 16, bt);
+            expert_at(lane, l, bt, quarter, rows);
+        }
+        rows.t0 += (rows.t1 - rows.t0) / BT * BT;
         return true;
     }
-    b -= (int64_t)nb * nc;
-    if (b < nh * nc) {
-        cls = 1;
-        tile_at((unsigned)b, nh, nc, bt, bc);
-        const int l = lane_of(rest_upto & 0xFFFF, rest & 0xFFFF, bt);
-        expert_at(lane, l, bt, half, rows);
-    } else {
-        b -= nh * nc;
-        if (b >= nq * nc) return false;
-        cls = 2;
-        tile_at((unsigned)b, nq, nc, bt, bc);
-        const int l = lane_of(rest_upto >> 16, rest >> 16, bt);
-        expert_at(lane, l, bt, quarter, rows);
+};
+
+// Long tiles on 256 CUs, one each: what is left over after whole rounds of them is
+// shared out, each tile's depth over as many workgroups as end it soonest, and joined by
+// k_q4_experts_tail.  (Whole numbers, so that both kernels find the same.)
+constexpr int kTailCUs = 256, kTailParts = 16, kTailUnits = 512;
+struct ExpertTail {
+    int us;        // hundredths of one that a long tile takes; 0: no tile is shared out
+    int deepest;   // parts of a tile at most
+};
+struct ExpertTailAt {
+    int64_t whole;     // tiles before the tail
+    int left, parts;   // of the tail, and workgroups of each
+    __device__ __forceinline__ ExpertTailAt(int64_t tiles, const ExpertTail& tail) : whole(tiles), left((int)(tiles % kTailCUs)), parts(1)
+    {
+        whole -= left;
+        int best = tail.us;
+        for (int s = 2; s <= tail.deepest && left * s <= kTailUnits; ++s) {
+            // (a launch, and 256 KB there and back at 5.8 TB/s for each part)
+            const int us = (left * s + kTailCUs - 1) / kTailCUs * tail.us / s + 200 + 9 * left * s;
+            if (us < best) best = us, parts = s;
+        }
     }
-    rows.t0 += (rows.t1 - rows.t0) / BT * BT;
+};
+
+// This workgroup's tile, and its part of it: with a tail that is shared out, or
+// (blockIdx.y of gridDim.y) every tile alike.  part: R x cols float32 sums a part, or
+// 64 TA x width ones a unit of the tail.
+template <int TA>
+__device__ __forceinline__ bool expert_tile(const int32_t* __restrict__ offsets, int E, int R, int nc, int cols, int width,
+                                            const ExpertTail& tail, float* part, ExpertRows& rows, int& bc, int& cls,
+                                            TileShare& share)
+{
+    const ExpertTiles<TA> tiles(offsets, E, R);
+    int64_t b = blockIdx.x;
+    int unit = -1;
+    share = TileShare{(int)blockIdx.y, (int)gridDim.y, part + (int64_t)blockIdx.y * R * cols, cols};
+    if (TA == 4 && tail.us) {
+        const ExpertTailAt at(tiles.count(nc), tail);
+        if (b >= at.whole && at.parts > 1) {
+            unit = (int)(b - at.whole);
+            if (unit >= at.left * at.parts) return false;
+            share.k = unit / at.left;
+            share.of = at.parts;
+            b = at.whole + unit % at.left;
+        }
+    }
+    if (!tiles.find(b, nc, rows, bc, cls)) return false;
+    if (unit >= 0) {
+        share.part = part + ((int64_t)unit * 64 * TA - rows.t0) * width - bc * width;
+        share.ld = width;
+    }
     return true;
 }
 
@@ -147,16 +208,17 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_experts(const uint16_t* __re
                                                             const int32_t* __restrict__ offsets, int E, Q4Layer stack,
                                                             int64_t layer_bytes, const float* __restrict__ sums, int64_t lds_,
                                                             uint16_t* __restrict__ y, int64_t ldy, int nr,
-                                                            float* __restrict__ part)
+                                                            ExpertTail tail, float* __restrict__ part)
 {
     constexpr int HALF = TA > 1 ? TA / 2 : 1, BYTES = std::max(std::max(Prompt<TA, WR>::LDS, Prompt<HALF, WR>::LDS), Prompt<1, WR>::LDS);
     ExpertRows rows;
     int br, cls;
-    if (!expert_tile<TA>(offsets, E, R, nr, rows, br, cls)) return;
+    TileShare share;
+    if (!expert_tile<TA>(offsets, E, R, nr, stack.m, 64 * WR, tail, part, rows, br, cls, share)) return;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
-    if (cls == 0) prompt_tile<X, TA, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
-    else if (cls == 1 && TA > 1) prompt_tile<X, HALF, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
-    else if (TA > 2) prompt_tile<X, 1, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, part, R);
+    if (cls == 0) prompt_tile<X, TA, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, share);
+    else if (cls == 1 && TA > 1) prompt_tile<X, HALF, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, share);
+    else if (TA > 2) prompt_tile<X, 1, WR, OWN, BYTES>(x, ldx, rows.t0, rows.t1, w, sums, lds_, y, ldy, br, share);
 }
 
 // Tiles of up to 64 TA rows by 64 WJ columns.
@@ -164,16 +226,17 @@ template <class X, int TA, int WJ>
 __global__ __launch_bounds__(128 * WJ, 2) void k_q4_experts_grad(const uint16_t* __restrict__ dy, int64_t lddy, int R,
                                                                  const int32_t* __restrict__ offsets, int E, Q4Layer stack,
                                                                  int64_t layer_bytes, uint16_t* __restrict__ dx, int64_t lddx,
-                                                                 int nj, float* __restrict__ part)
+                                                                 int nj, ExpertTail tail, float* __restrict__ part)
 {
     constexpr int HALF = TA / 2, BYTES = std::max(std::max(Grad<TA, WJ>::LDS, Grad<HALF, WJ>::LDS), Grad<1, WJ>::LDS);
     ExpertRows rows;
     int bj, cls;
-    if (!expert_tile<TA>(offsets, E, R, nj, rows, bj, cls)) return;
+    TileShare share;
+    if (!expert_tile<TA>(offsets, E, R, nj, stack.n, 64 * WJ, tail, part, rows, bj, cls, share)) return;
     const Q4Layer w = expert_layer(stack, rows.e, layer_bytes);
-    if (cls == 0) grad_tile<X, TA, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
-    else if (cls == 1) grad_tile<X, HALF, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
-    else if (TA > 2) grad_tile<X, 1, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, part, R);
+    if (cls == 0) grad_tile<X, TA, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, share);
+    else if (cls == 1) grad_tile<X, HALF, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, share);
+    else if (TA > 2) grad_tile<X, 1, WJ, BYTES>(dy, lddy, rows.t0, rows.t1, w, dx, lddx, bj, share);
 }
 
 // The sum of `splits` partial results, in order, for the rows that some expert
@@ -210,6 +273,46 @@ __global__ __launch_bounds__(256) void k_q4_experts_join(const float* __restrict
                 for (int u = 0; u < splits; ++u) v += p[u * all + e];
                 to[e] = X::down(v);
             }
+        }
+    }
+}
+
+// The tail's tiles from their parts, in order; kTailBlocks workgroups a tile.
+constexpr int kTailBlocks = 16;
+template <class X>
+__global__ __launch_bounds__(256) void k_q4_experts_tail(const float* __restrict__ part, ExpertTail tail, int R,
+                                                         const int32_t* __restrict__ offsets, int E, int m, int nc,
+                                                         uint16_t* __restrict__ y, int64_t ldy)
+{
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    const int q = blockIdx.x / kTailBlocks, sub = blockIdx.x % kTailBlocks;
+    const ExpertTiles<4> tiles(offsets, E, R);
+    const ExpertTailAt at(tiles.count(nc), tail);
+    if (q >= at.left || at.parts == 1) return;
+    ExpertRows rows;
+    int bc, cls;
+    if (!tiles.find(at.whole + q, nc, rows, bc, cls)) return;
+    const int n = min(256 >> cls, rows.t1 - rows.t0), c = 4 * (threadIdx.x & 63), col = 256 * bc + c;
+    if (col >= m) return;
+    for (int t = 4 * sub + (threadIdx.x >> 6); t < n; t += 4 * kTailBlocks) {
+        const float* p = part + ((int64_t)q * 256 + t) * 256 + c;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int k0 = 0; k0 < at.parts; k0 += 4) {
+            f32x4 a[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                a[u] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(k0 + u, at.parts - 1) * at.left * 65536);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (k0 + u < at.parts) v += a[u];
+        }
+        uint16_t* to = y + (int64_t)(rows.t0 + t) * ldy + col;
+        if (col + 4 <= m) {
+            *reinterpret_cast<u32x2_any*>(to) = u32x2_any{X::down2(v.x, v.y), X::down2(v.z, v.w)};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (col + e < m) to[e] = X::down(v[e]);
         }
     }
 }
@@ -334,6 +437,7 @@ __global__ __launch_bounds__(64 * kGradFewWaves) void k_q4_experts_grad_few(cons
 struct ExpertsPlan {
     bool few;
     int TA, WR, splits;
+    ExpertTail tail;
     double us;         // that it is expected to take
     int64_t tiles;     // of rows, that there can be
     int pieces;
@@ -384,25 +488,44 @@ static double experts_us(const ExpertWork& w, int64_t R, int64_t cols, int64_t d
            (splits > 1 ? 2.0 + 8.0e-6 / 4 * splits * R * cols : 0.0);
 }
 
-// The least of it over shapes and splits, with `deepest` splits at most.
+// The least of it over shapes and splits, with `deepest` splits at most; or shape 0 with
+// its tail shared out (ExpertTail), for tiles of kTailLeast us or more and few rounds of
+// them (gradient, 2 of 8 of 14336 x 4096, 1500 tokens: 420 us, and 462 all in equal parts;
+// 2048: 543 and 611; 6000, three rounds: 1400 and 1533.  Product, 2048 tokens, four rounds:
+// 490 and 484; 8192, fifteen: 1731 and 1706).
 struct ExpertsChoice {
     int shape, splits;
     double us;
+    ExpertTail tail;
 };
+constexpr double kTailLeast = 40.0, kTailRounds = 3.5;
 template <int N>
 static ExpertsChoice experts_choose(const ExpertShape (&shapes)[N], int64_t R, int64_t E, int64_t cols, int64_t depth,
                                     int64_t deepest)
 {
-    ExpertsChoice best{0, 1, 0.0};
+    ExpertsChoice best{0, 1, 0.0, {0, 0}};
     for (int i = 0; i < N; ++i) {
         const ExpertWork w = experts_work(shapes[i], R, E, cols);
         const int64_t tiles = blocks_most(R, E, shapes[i].rows) * ceil_div(cols, shapes[i].cols);
         for (int s = 1; s == 1 || (s <= deepest && tiles * s <= 2048); ++s) {
             const double us = experts_us(w, R, cols, depth, s);
-            if (best.us == 0.0 || us < best.us) best = {i, s, us};
+            if (best.us == 0.0 || us < best.us) best = {i, s, us, {0, 0}};
         }
     }
+    const ExpertWork w = experts_work(shapes[0], R, E, cols);
+    const double tile = shapes[0].us[0] * depth / 4096, us = w.all * depth / 4096 + 0.1 * tile + 20.0;
+    if (tile >= kTailLeast && w.all <= kTailRounds * w.tile && us < best.us)
+        best = {0, 1, us, {(int)std::min(100.0 * tile, 1.0e6), (int)std::min<int64_t>(deepest, kTailParts)}};
     return best;
+}
+
+// Workgroups of a launch, and the bytes of its parts.
+static int64_t experts_grid(const ExpertsPlan& p, int64_t nc) { return p.tiles * nc + (p.tail.us ? kTailUnits : 0); }
+static size_t experts_part_bytes(const ExpertsPlan& p, int64_t R, int64_t cols)
+{
+    if (p.tail.us)
+        return align_up((size_t)std::min<int64_t>(kTailUnits, p.tiles * ceil_div(cols, 256) * kTailParts) * 65536 * 4);
+    return p.splits > 1 ? align_up((size_t)p.splits * R * cols * 4) : 0;
 }
 
 static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int gb)
@@ -415,6 +538,7 @@ static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int 
     const ExpertsChoice c = experts_choose(shapes, R, E, m, n, std::min<int64_t>(8, ceil_div(n, kQ4Cols) / 2));
     const ExpertShape& s = shapes[c.shape];
     p.splits = c.splits;
+    p.tail = c.tail;
     p.us = c.us;
     p.TA = s.rows / 64;
     p.WR = s.cols / 64;
@@ -424,7 +548,7 @@ static ExpertsPlan experts_plan(int64_t R, int64_t E, int64_t m, int64_t n, int 
     p.pieces = piece_at((int)((n - 1) / 64), gb) + 1;
     p.copy = align_up((size_t)p.lds_ * p.pieces * 4);
     p.part = p.copy + align_up((size_t)R * p.ldc * 2);
-    p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * R * m * 4) : 0);
+    p.bytes = p.part + experts_part_bytes(p, R, m);
     return p;
 }
 
@@ -454,12 +578,13 @@ static ExpertsPlan experts_grad_plan(int64_t R, int64_t E, int64_t m, int64_t n,
         return p;
     }
     p.splits = c.splits;
+    p.tail = c.tail;
     p.TA = shapes[c.shape].rows / 64;
     p.WR = shapes[c.shape].cols / 64;
     p.tiles = blocks_most(R, E, shapes[c.shape].rows);
     p.ldc = ceil_div(m, 64) * 64;
     p.part = align_up((size_t)R * p.ldc * 2);
-    p.bytes = p.part + (p.splits > 1 ? align_up((size_t)p.splits * R * n * 4) : 0);
+    p.bytes = p.part + experts_part_bytes(p, R, n);
     return p;
 }
 
@@ -484,6 +609,18 @@ static void experts_join(const ExpertsCall& c, const float* part, int splits, in
             g.log, g.chunks, c.out, c.ldout);
 }
 
+// What a product in tiles left in parts.
+template <class X>
+static void experts_parts(const ExpertsCall& c, const ExpertsPlan& p, int64_t cols)
+{
+    const float* part = reinterpret_cast<const float*>(c.ws + p.part);
+    const int64_t nc = ceil_div(cols, 256);
+    if (p.splits > 1) experts_join<X>(c, part, p.splits, cols);
+    if (p.tail.us)
+        enqueue(k_q4_experts_tail<X>, dim3((unsigned)(std::min<int64_t>(kTailCUs - 1, p.tiles * nc) * kTailBlocks)), dim3(256), c.s,
+                part, p.tail, (int)c.rows, c.offsets, (int)c.E, (int)cols, (int)nc, c.out, c.ldout);
+}
+
 template <class X, int WS>
 static void experts_few(const ExpertsCall& c, const Q4Layer& w)
 {
@@ -496,9 +633,9 @@ template <class X, int TA, int WR, bool OWN>
 static void experts_launch(const ExpertsCall& c, const ExpertsPlan& p, const Q4Layer& w, const uint16_t* x, int64_t ldx)
 {
     const int nr = (int)ceil_div(w.m, 64 * WR);
-    enqueue(k_q4_experts<X, TA, WR, OWN>, dim3((unsigned)(p.tiles * nr), (unsigned)p.splits), dim3(128 * WR), c.s, x, ldx,
+    enqueue(k_q4_experts<X, TA, WR, OWN>, dim3((unsigned)experts_grid(p, nr), (unsigned)p.splits), dim3(128 * WR), c.s, x, ldx,
             (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, reinterpret_cast<const float*>(c.ws), p.lds_, c.out,
-            c.ldout, nr, reinterpret_cast<float*>(c.ws + p.part));
+            c.ldout, nr, p.tail, reinterpret_cast<float*>(c.ws + p.part));
 }
 
 template <class X>
@@ -529,7 +666,7 @@ static void experts_run(const ExpertsCall& c)
     if (p.TA == 4) experts_launch<X, 4, 4, false>(c, p, w, x, ldx);
     else if (p.TA == 2) (own ? experts_launch<X, 2, 2, true> : experts_launch<X, 2, 2, false>)(c, p, w, x, ldx);
     else (own ? experts_launch<X, 1, 2, true> : experts_launch<X, 1, 2, false>)(c, p, w, x, ldx);
-    if (p.splits > 1) experts_join<X>(c, reinterpret_cast<const float*>(c.ws + p.part), p.splits, w.m);
+    experts_parts<X>(c, p, w.m);
 }
 
 template <class X>
@@ -554,10 +691,10 @@ static void experts_grad_run(const ExpertsCall& c)
         lddy = p.ldc;
     }
     const int nj = (int)ceil_div(w.n, 64 * p.WR);
-    enqueue(p.TA == 4 ? k_q4_experts_grad<X, 4, 4> : k_q4_experts_grad<X, 2, 2>, dim3((unsigned)(p.tiles * nj), (unsigned)p.splits),
+    enqueue(p.TA == 4 ? k_q4_experts_grad<X, 4, 4> : k_q4_experts_grad<X, 2, 2>, dim3((unsigned)experts_grid(p, nj), (unsigned)p.splits),
             dim3(128 * p.WR), c.s, dy, lddy, (int)c.rows, c.offsets, (int)c.E, w, (int64_t)c.d.bytes, c.out, c.ldout, nj,
-            reinterpret_cast<float*>(c.ws + p.part));
-    if (p.splits > 1) experts_join<X>(c, reinterpret_cast<const float*>(c.ws + p.part), p.splits, w.n);
+            p.tail, reinterpret_cast<float*>(c.ws + p.part));
+    experts_parts<X>(c, p, w.n);
 }
 
 static bool experts_size_ok(int64_t rows, int64_t m, int64_t n)

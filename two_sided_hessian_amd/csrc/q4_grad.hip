@@ -46,7 +46,8 @@ __global__ __launch_bounds__(512) void k_q4_grad(const uint16_t* __restrict__ dy
     typedef Grad<TA> P;
     int bt, bj;
     tile_of(nt, nj, bt, bj);
-    grad_tile<X, TA>(dy, lddy, bt * P::BT, T, w, dx, lddx, bj, part, T);
+    grad_tile<X, TA>(dy, lddy, bt * P::BT, T, w, dx, lddx, bj,
+                     TileShare{(int)blockIdx.y, (int)gridDim.y, part + (int64_t)blockIdx.y * T * w.n, w.n});
 }
 
 // --------------------------------------------------------------------- host

@@ -46,13 +46,10 @@ struct GradRaw {
 };
 
 // One output tile: tokens t0 .. min(t0 + 64 TA, T) - 1 by columns 64 WJ bj ...
-// blockIdx.y of gridDim.y shares the rows of W; more than one of them writes
-// float32 partial sums to part[blockIdx.y][token][column], part_rows tokens a part,
-// instead of dx.
 template <class X, int TA, int WJ = 4, int BYTES = Grad<TA, WJ>::LDS>
 __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64_t lddy, int t0, int T,
                                           const Q4Layer& w, uint16_t* __restrict__ dx, int64_t lddx, int bj,
-                                          float* __restrict__ part, int64_t part_rows)
+                                          const TileShare& share)
 {
     typedef Grad<TA, WJ> P;
     typedef typename X::vec vec;
@@ -64,7 +61,7 @@ __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64
     const int wt = wave / WJ, wj = wave % WJ;
     const int j0 = bj * P::BJ;
     const int all = (w.m + 63) / 64;
-    const int c0 = all * blockIdx.y / gridDim.y, c1 = all * (blockIdx.y + 1) / gridDim.y;   // this workgroup's chunks
+    const int c0 = all * share.k / share.of, c1 = all * (share.k + 1) / share.of;   // this workgroup's chunks
     // what the weights of group g's columns are divided by; 1 where all are 0
     auto unit_of = [&](int g) {
         const float unit = w.unit[g];
@@ -208,8 +205,7 @@ __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64
     }
     wait_direct_loads();
     const int tw = t0 + 32 * wt * TA;
-    if (gridDim.y > 1) {
-        float* p = part + blockIdx.y * part_rows * w.n;
+    if (share.of > 1) {
 #pragma unroll
         for (int a = 0; a < TA; ++a)
 #pragma unroll
@@ -217,7 +213,7 @@ __device__ __forceinline__ void grad_tile(const uint16_t* __restrict__ dy, int64
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int t = tw + 32 * a + 8 * (r >> 2) + 4 * h + (r & 3), j = jw + 32 * b + ml;
-                    if (t < T && j < w.n) p[(int64_t)t * w.n + j] = unit * acc[a][b][r];
+                    if (t < T && j < w.n) share.part[t * share.ld + j] = unit * acc[a][b][r];
                 }
         return;
     }

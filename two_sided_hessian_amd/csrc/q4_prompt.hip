@@ -57,7 +57,8 @@ __global__ __launch_bounds__(128 * WR, 2) void k_q4_prompt(const uint16_t* __res
     typedef Prompt<TA, WR> P;
     int bt, br;
     tile_of(nt, nr, bt, br);
-    prompt_tile<X, TA, WR, OWN>(x, ldx, bt * P::BT, T, w, sums, lds_, y, ldy, br, part, T);
+    prompt_tile<X, TA, WR, OWN>(x, ldx, bt * P::BT, T, w, sums, lds_, y, ldy, br,
+                                TileShare{(int)blockIdx.y, (int)gridDim.y, part + (int64_t)blockIdx.y * T * w.m, w.m});
 }
 
 // y = the sum of `splits` partial results, in order; blockIdx.x is the token,

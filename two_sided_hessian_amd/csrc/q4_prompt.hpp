@@ -187,14 +187,11 @@ __device__ __forceinline__ void zero_points(f32x16 (&acc)[TA][2], const float (&
 }
 
 // One output tile: tokens t0 .. min(t0 + 64 TA, T) - 1 by rows 64 WR br .. of W.
-// OWN: the sums of x come from a product with ones.  blockIdx.y of gridDim.y
-// shares the columns; more than one of them writes float32 partial sums to
-// part[blockIdx.y][token][row], part_rows tokens a part, instead of y.
+// OWN: the sums of x come from a product with ones.
 template <class X, int TA, int WR, bool OWN, int BYTES = Prompt<TA, WR>::LDS>
 __device__ __forceinline__ void prompt_tile(const uint16_t* __restrict__ x, int64_t ldx, int t0, int T,
                                             const Q4Layer& w, const float* __restrict__ sums, int64_t lds_,
-                                            uint16_t* __restrict__ y, int64_t ldy, int br, float* __restrict__ part,
-                                            int64_t part_rows)
+                                            uint16_t* __restrict__ y, int64_t ldy, int br, const TileShare& share)
 {
     typedef Prompt<TA, WR> P;
     typedef typename X::vec vec;
@@ -204,7 +201,7 @@ __device__ __forceinline__ void prompt_tile(const uint16_t* __restrict__ x, int6
     const int h = lane >> 5, ml = lane & 31;
     const int wt = wave / WR, wr = wave % WR;
     const int rt0 = br * (P::BR / 16);
-    const int kb0 = w.KB * blockIdx.y / gridDim.y, kb1 = w.KB * (blockIdx.y + 1) / gridDim.y;
+    const int kb0 = w.KB * share.k / share.of, kb1 = w.KB * (share.k + 1) / share.of;
     PromptStage<TA, WR> stage(x, ldx, t0, T, w, rt0, kb0, kb1, lds);
     stage.first(kb0);
 #pragma unroll
@@ -374,8 +371,7 @@ __device__ __forceinline__ void prompt_tile(const uint16_t* __restrict__ x, int6
                 acc[a][b][r] = (OWN ? fmaf(-(sz[b].y + kQ4Offset), sx[a][r], acc[a][b][r]) : acc[a][b][r]) * sz[b].x;
     wait_direct_loads();
     const int tw = t0 + 32 * wt * TA, rw = br * P::BR + wr * 64;
-    if (gridDim.y > 1) {
-        float* p = part + blockIdx.y * part_rows * w.m;
+    if (share.of > 1) {
 #pragma unroll
         for (int a = 0; a < TA; ++a)
 #pragma unroll
@@ -383,7 +379,7 @@ __device__ __forceinline__ void prompt_tile(const uint16_t* __restrict__ x, int6
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int t = tw + 32 * a + 8 * (r >> 2) + 4 * h + (r & 3), row = rw + 32 * b + ml;
-                    if (t < T && row < w.m) p[(int64_t)t * w.m + row] = acc[a][b][r];
+                    if (t < T && row < w.m) share.part[t * share.ld + row] = acc[a][b][r];
                 }
         return;
     }

@@ -22,6 +22,15 @@ __device__ __forceinline__ void tile_wait()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
+// Which part of a tile's depth a workgroup takes: part k of `of`.  More than one of
+// them write float32 partial sums instead of results, token t and column j at
+// part[t ld + j].
+struct TileShare {
+    int k, of;
+    float* part;
+    int64_t ld;
+};
+
 // Workgroups are dealt to the eight XCDs round-robin; each XCD gets a
 // contiguous run of the tile order below, so that its L2 sees few tokens and
 // rows at a time: runs of 4 token blocks share their rows of W.
