@@ -156,6 +156,7 @@ constexpr int kTailCUs = 256, kTailParts = 16, kTailUnits = 512;
 struct ExpertTail {
     int us;        // hundredths of one that a long tile takes; 0: no tile is shared out
     int deepest;   // parts of a tile at most
+    int units;     // and of all of them, that there is room for (whatever the offsets say)
 };
 struct ExpertTailAt {
     int64_t whole;     // tiles before the tail
@@ -164,7 +165,7 @@ struct ExpertTailAt {
     {
         whole -= left;
         int best = tail.us;
-        for (int s = 2; s <= tail.deepest && left * s <= kTailUnits; ++s) {
+        for (int s = 2; s <= tail.deepest && left * s <= tail.units; ++s) {
             // (a launch, and 256 KB there and back at 5.8 TB/s for each part)
             const int us = (left * s + kTailCUs - 1) / kTailCUs * tail.us / s + 200 + 9 * left * s;
             if (us < best) best = us, parts = s;
@@ -503,28 +504,28 @@ template <int N>
 static ExpertsChoice experts_choose(const ExpertShape (&shapes)[N], int64_t R, int64_t E, int64_t cols, int64_t depth,
                                     int64_t deepest)
 {
-    ExpertsChoice best{0, 1, 0.0, {0, 0}};
+    ExpertsChoice best{0, 1, 0.0, {0, 0, 0}};
     for (int i = 0; i < N; ++i) {
         const ExpertWork w = experts_work(shapes[i], R, E, cols);
         const int64_t tiles = blocks_most(R, E, shapes[i].rows) * ceil_div(cols, shapes[i].cols);
         for (int s = 1; s == 1 || (s <= deepest && tiles * s <= 2048); ++s) {
             const double us = experts_us(w, R, cols, depth, s);
-            if (best.us == 0.0 || us < best.us) best = {i, s, us, {0, 0}};
+            if (best.us == 0.0 || us < best.us) best = {i, s, us, {0, 0, 0}};
         }
     }
     const ExpertWork w = experts_work(shapes[0], R, E, cols);
     const double tile = shapes[0].us[0] * depth / 4096, us = w.all * depth / 4096 + 0.1 * tile + 20.0;
     if (tile >= kTailLeast && w.all <= kTailRounds * w.tile && us < best.us)
-        best = {0, 1, us, {(int)std::min(100.0 * tile, 1.0e6), (int)std::min<int64_t>(deepest, kTailParts)}};
+        best = {0, 1, us, {(int)std::min(100.0 * tile, 1.0e6), (int)std::min<int64_t>(deepest, kTailParts),
+                           (int)std::min<int64_t>(kTailUnits, blocks_most(R, E, 256) * ceil_div(cols, 256) * kTailParts)}};
     return best;
 }
 
 // Workgroups of a launch, and the bytes of its parts.
-static int64_t experts_grid(const ExpertsPlan& p, int64_t nc) { return p.tiles * nc + (p.tail.us ? kTailUnits : 0); }
+static int64_t experts_grid(const ExpertsPlan& p, int64_t nc) { return p.tiles * nc + p.tail.units; }
 static size_t experts_part_bytes(const ExpertsPlan& p, int64_t R, int64_t cols)
 {
-    if (p.tail.us)
-        return align_up((size_t)std::min<int64_t>(kTailUnits, p.tiles * ceil_div(cols, 256) * kTailParts) * 65536 * 4);
+    if (p.tail.us) return align_up((size_t)p.tail.units * 65536 * 4);
     return p.splits > 1 ? align_up((size_t)p.splits * R * cols * 4) : 0;
 }
 
