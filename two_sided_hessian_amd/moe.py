@@ -424,21 +424,18 @@ class _Experts(torch.autograd.Function):
     """q4_experts and q4_experts_grad, each the other's derivative."""
 
     @staticmethod
-    def forward(ctx, v, w, offsets, call, back, ws, stream):
+    def forward(ctx, v, w, offsets, call, back, ws, stream, gradient):
         ctx.w, ctx.call, ctx.back = w, call, back
         ctx.save_for_backward(offsets)
-        return call(v.detach(), w, offsets, ws=ws, stream=stream)
+        v, out = v.detach(), None
+        if gradient:   # zeros in the rows that no expert has
+            out = v.new_zeros((v.shape[0], w.n if call is q4_experts_grad else w.m))
+        return call(v, w, offsets, out=out, ws=ws, stream=stream)
 
     @staticmethod
     def backward(ctx, g):
         offsets, = ctx.saved_tensors
-        g = g.contiguous()
-        if g.requires_grad and _grad_on():
-            r = _Experts.apply(g, ctx.w, offsets, ctx.back, ctx.call, None, None)
-        else:
-            cols = ctx.w.n if ctx.back is q4_experts_grad else ctx.w.m
-            r = ctx.back(g, ctx.w, offsets, out=g.new_zeros((g.shape[0], cols)))
-        return r, None, None, None, None, None, None
+        return (_Experts.apply(g.contiguous(), ctx.w, offsets, ctx.back, ctx.call, None, None, True),) + 7 * (None,)
 
 
 def _experts(call, size, name, x, w, offsets, out, ws, stream):
@@ -457,7 +454,7 @@ def _experts(call, size, name, x, w, offsets, out, ws, stream):
     if x.requires_grad and _grad_on():
         _without_out(out, name)
         both = (q4_experts, q4_experts_grad) if name == "x" else (q4_experts_grad, q4_experts)
-        return _Experts.apply(x, w, offsets, *both, ws, stream)
+        return _Experts.apply(x, w, offsets, *both, ws, stream, False)
     if out is None:
         out, ldo = _made(stream, lambda: (x.new_empty((R, out_cols)),))[0], out_cols
     else:
