@@ -42,3 +42,67 @@ def test_gradients_of_rows_that_no_expert_has_are_zeros_in_a_kept_graph():
             stale((R, cin), (R, cout))
             dg, = torch.autograd.grad(dv, g, v.detach())
             assert torch.equal(dg, dx)
+
+
+def kept(call, inputs, out_grad=None):
+    """The gradients of a call's result, or of its sum, in a kept graph."""
+    y = call(*inputs)
+    return torch.autograd.grad(y.sum() if out_grad is None else y, inputs, out_grad, create_graph=True)
+
+
+def single_calls():
+    """Each call that has a first derivative only, its inputs, and the gradients of its sum."""
+    T, E, k, n = 40, 8, 2, 96
+    logits = torch.randn((T, E), generator=torch.Generator().manual_seed(1)).to(DEV)
+    r = B.moe_route(logits, k)
+    a, b, ys = (tokens(T * k, n, BF16, i) for i in (1, 2, 3))
+    ones, rows = torch.ones((T, k), device=DEV), torch.ones((T, n), dtype=BF16, device=DEV)
+    out = {"dys": torch.zeros_like(ys), "dweights": torch.empty_like(r["weights"])}
+    yield "moe_route", lambda l: B.moe_route(l, k)["weights"], [logits], [B.moe_route_grad(ones, r["weights"], r["ids"], E)]
+    yield ("moe_combine", lambda y, w: B.moe_combine(y, r["place"], w), [ys, r["weights"]],
+           list(B.moe_combine_grad(rows, ys, r["place"], r["weights"], out=out).values()))
+    yield "gated_act", lambda a, b: B.gated_act(a, b), [a, b], list(B.gated_act_grad(torch.ones_like(a), *B.gated_act(a, b, checkpoint=True)[1:]))
+    w = [pack(*make_layer(*v, 64, i, lead=(E,)), 64) for i, v in enumerate(((64, n), (64, n), (n, 64)))]
+    x = tokens(T, n, BF16, 4)
+    p = [x.clone().requires_grad_(), logits.clone().requires_grad_()]
+    B.q4_moe_layer(*p, *w, k).sum().backward()
+    yield "q4_moe_layer", lambda x, l: B.q4_moe_layer(x, l, *w, k), [x, logits], [v.grad for v in p]
+
+
+def test_second_derivatives_are_refused_where_the_graph_is_kept():
+    """A loss that is linear in the result brings a gradient that requires none itself,
+    and the call's gradients depend on its inputs all the same."""
+    for name, call, plain, want in single_calls():
+        inputs = [v.clone().requires_grad_() for v in plain]
+        got = kept(call, inputs)
+        for a, b in zip(got, want):                               # the first derivative is what it is without the graph
+            assert torch.equal(a.detach(), b), name
+        other = sum(v.float().square().sum() for v in inputs)     # a term that has its own way to every input
+        for i, v in enumerate(got):
+            assert v.requires_grad, (name, i)
+            for x in inputs:
+                with pytest.raises(RuntimeError, match=f"{name}.* no second derivative"):
+                    torch.autograd.grad(v.float().square().sum() + other, x, retain_graph=True)
+            with pytest.raises(RuntimeError, match="no second derivative"):
+                (v.float().square().sum() + other).backward(retain_graph=True)
+        other.backward()                                          # what does not go through them is there
+        for x in inputs:
+            assert torch.equal(x.grad, 2 * x.detach())
+
+
+def test_second_derivatives_are_refused_where_the_gradient_requires_one():
+    for name, call, plain, want in single_calls():
+        inputs = [v.clone().requires_grad_() for v in plain]
+        y = call(*inputs)
+        g = torch.ones_like(y).requires_grad_()
+        with pytest.raises(RuntimeError, match="second derivative"):
+            got = torch.autograd.grad(y, inputs, g, create_graph=True)
+            torch.autograd.grad(sum(v.float().sum() for v in got), g)
+
+
+def test_gradients_that_are_not_needed_are_none_in_a_kept_graph():
+    for name, call, plain, want in single_calls():
+        for i in range(len(plain)):
+            inputs = [v.clone().requires_grad_(i == j) for j, v in enumerate(plain)]
+            got, = torch.autograd.grad(call(*inputs).sum(), inputs[i], create_graph=True)
+            assert torch.equal(got.detach(), want[i]), name

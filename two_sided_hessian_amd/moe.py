@@ -164,6 +164,33 @@ def _top_k(top_k):
     return int(top_k)
 
 
+class _Refusing(torch.autograd.Function):
+    """Gradients as they are, whose own derivative is refused."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tuple(t.detach() for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has no second derivative")
+
+
+def _once(name, gradients, *causes):
+    """The gradients that a backward pass of ``name`` made, None among them.  In a kept
+    graph (create_graph) they depend on ``causes``, and a derivative that reaches them
+    raises: without that they would count as constants."""
+    if not _grad_on() or not any(t.requires_grad for t in causes):
+        return gradients
+    made = [t for t in gradients if t is not None]
+    refusing = iter(_Refusing.apply(name, len(made), *made, *causes))
+    return tuple(None if t is None else next(refusing) for t in gradients)
+
+
+# A function whose backward pass keeps no tensor that leads to its inputs in the graph
+# returns an empty one beside its results (`lead`), and gives that to _once.
+
 # -------------------------------------------------------------------- route
 
 def moe_route_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
@@ -189,10 +216,11 @@ class _Route(torch.autograd.Function):
         return tuple(r[name] for name in _ROUTE)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, _ids, dweights, *_):
         weights, ids = ctx.saved_tensors
-        return moe_route_grad(dweights.contiguous(), weights, ids, ctx.experts, dtype=ctx.dtype), None, None, None
+        with torch.no_grad():
+            dlogits = moe_route_grad(dweights.contiguous(), weights, ids, ctx.experts, dtype=ctx.dtype)
+        return _once("moe_route", (dlogits, None, None, None), dweights, weights)
 
 
 def moe_route(logits, top_k, *, out=None, ws=None, stream=None):
@@ -347,10 +375,10 @@ class _Spread(torch.autograd.Function):
 def _combine_back(g, ys, place, weights):
     if g.requires_grad and _grad_on():
         raise RuntimeError("moe_combine with weights has no second derivative")
-    ys, weights = ys.detach(), weights.detach()
-    out = {"dys": torch.zeros(ys.shape, dtype=ys.dtype, device=ys.device), "dweights": torch.empty_like(weights)}
-    r = moe_combine_grad(g, ys, place, weights, out=out)
-    return r["dys"], None, r["dweights"]
+    with torch.no_grad():
+        out = {"dys": torch.zeros(ys.shape, dtype=ys.dtype, device=ys.device), "dweights": torch.empty_like(weights)}
+        r = moe_combine_grad(g, ys, place, weights, out=out)
+    return _once("moe_combine with weights", (r["dys"], None, r["dweights"]), ys, weights)
 
 
 def moe_combine(ys, place, weights=None, *, out=None, stream=None):
@@ -587,19 +615,20 @@ class _Gated(torch.autograd.Function):
     @staticmethod
     def forward(ctx, a, b, act, count, stream):
         h, ca, cb = gated_act(a.detach(), b.detach(), act=act, checkpoint=True, count=count, stream=stream)
+        lead = h.new_empty(0)
         ctx.act, ctx.like = act, (ca.rows, ca.cols, ca.dtype)
-        ctx.save_for_backward(ca.data, cb.data, count)
-        return h
+        ctx.save_for_backward(ca.data, cb.data, count, lead)
+        return h, lead
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g):
-        ca, cb, count = ctx.saved_tensors
-        g = g.contiguous()
-        out = None if count is None else (torch.zeros_like(g), torch.zeros_like(g))
-        da, db = gated_act_grad(g, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
-                                count=count, out=out)
-        return da, db, None, None, None
+    def backward(ctx, dh, _):
+        ca, cb, count, lead = ctx.saved_tensors
+        with torch.no_grad():
+            g = dh.contiguous()
+            out = None if count is None else (torch.zeros_like(g), torch.zeros_like(g))
+            da, db = gated_act_grad(g, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
+                                    count=count, out=out)
+        return _once("gated_act", (da, db, None, None, None), dh, lead)
 
 
 def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, stream=None):
@@ -626,7 +655,7 @@ def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, strea
         _without_out(out, "a or b")
         if checkpoint is not False:
             raise ValueError("checkpoint cannot be given where a or b requires a gradient: autograd keeps its own")
-        return _Gated.apply(a, b, act, count, stream)
+        return _Gated.apply(a, b, act, count, stream)[0]
     if out is None:
         out, ldo = _made(stream, lambda: (a.new_empty((rows, n)),))[0], n
     else:
@@ -701,34 +730,41 @@ class _Layer(torch.autograd.Function):
         y, r, ys, (ca, cb) = _forward(x.detach(), logits.detach(), w_gate, w_up, w_down, k, act, True)
         ctx.layers, ctx.act, ctx.like = (w_gate, w_up, w_down), act, (ca.rows, ca.cols, ca.dtype)
         ctx.logits = logits.shape[1], logits.dtype
-        ctx.save_for_backward(r["ids"], r["weights"], r["place"], r["offsets"], ys, ca.data, cb.data)
-        return y
+        lead = y.new_empty(0)
+        ctx.save_for_backward(r["ids"], r["weights"], r["place"], r["offsets"], ys, ca.data, cb.data, lead)
+        return y, lead
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy):
-        ids, weights, place, offsets, ys, ca, cb = ctx.saved_tensors
-        w_gate, w_up, w_down = ctx.layers
-        (R, n), f, e = ys.shape, w_gate.m, ys.new_empty
-        back = moe_combine_grad(dy.contiguous(), ys, place, weights,
-                                out={"dys": e((R, n)), "dweights": torch.empty_like(weights)})
-        dlogits = dx = None
-        if ctx.needs_input_grad[1]:
-            E, dtype = ctx.logits
-            dlogits = moe_route_grad(back["dweights"], weights, ids, E, out=e((weights.shape[0], E), dtype=dtype))
-        if ctx.needs_input_grad[0]:
-            ws = _shared((q4_experts_grad_workspace_bytes(R, w_down), q4_experts_grad_workspace_bytes(R, w_gate)), ys)
-            dh = q4_experts_grad(back["dys"], w_down, offsets, out=e((R, f)), ws=ws)
-            da, db = gated_act_grad(dh, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
-                                    count=offsets[-1:], out=(e((R, f)), e((R, f))))
-            # both halves of the rows' gradient in one sum: a token's places in
-            # the first and in the second
-            dxs = e((2 * R, n))
-            q4_experts_grad(da, w_gate, offsets, out=dxs[:R], ws=ws)
-            q4_experts_grad(db, w_up, offsets, out=dxs[R:], ws=ws)
-            both = torch.cat((place, torch.where(place < 0, place, place + R)), 1)
-            dx = moe_combine(dxs, both, out=e((place.shape[0], n)))
-        return dx, dlogits, None, None, None, None, None
+    def backward(ctx, dy, _):
+        with torch.no_grad():
+            gradients = _layer_back(ctx, dy)
+        return _once("q4_moe_layer", gradients + 5 * (None,), dy, ctx.saved_tensors[-1])
+
+
+def _layer_back(ctx, dy):
+    """The gradients of x and of the logits, None where one is not needed."""
+    ids, weights, place, offsets, ys, ca, cb, _ = ctx.saved_tensors
+    w_gate, w_up, w_down = ctx.layers
+    (R, n), f, e = ys.shape, w_gate.m, ys.new_empty
+    back = moe_combine_grad(dy.contiguous(), ys, place, weights,
+                            out={"dys": e((R, n)), "dweights": torch.empty_like(weights)})
+    dlogits = dx = None
+    if ctx.needs_input_grad[1]:
+        E, dtype = ctx.logits
+        dlogits = moe_route_grad(back["dweights"], weights, ids, E, out=e((weights.shape[0], E), dtype=dtype))
+    if ctx.needs_input_grad[0]:
+        ws = _shared((q4_experts_grad_workspace_bytes(R, w_down), q4_experts_grad_workspace_bytes(R, w_gate)), ys)
+        dh = q4_experts_grad(back["dys"], w_down, offsets, out=e((R, f)), ws=ws)
+        da, db = gated_act_grad(dh, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
+                                count=offsets[-1:], out=(e((R, f)), e((R, f))))
+        # both halves of the rows' gradient in one sum: a token's places in the first
+        # and in the second
+        dxs = e((2 * R, n))
+        q4_experts_grad(da, w_gate, offsets, out=dxs[:R], ws=ws)
+        q4_experts_grad(db, w_up, offsets, out=dxs[R:], ws=ws)
+        both = torch.cat((place, torch.where(place < 0, place, place + R)), 1)
+        dx = moe_combine(dxs, both, out=e((place.shape[0], n)))
+    return dx, dlogits
 
 
 def q4_moe_layer(x, logits, w_gate, w_up, w_down, top_k, *, act="silu"):
@@ -758,5 +794,5 @@ def q4_moe_layer(x, logits, w_gate, w_up, w_down, top_k, *, act="silu"):
         raise ValueError(f"top_k must be {E} at most, the number of experts")
     _act(act)
     if (x.requires_grad or logits.requires_grad) and _grad_on():
-        return _Layer.apply(x, logits, w_gate, w_up, w_down, k, act)
+        return _Layer.apply(x, logits, w_gate, w_up, w_down, k, act)[0]
     return _forward(x, logits, w_gate, w_up, w_down, k, act, False)[0]
