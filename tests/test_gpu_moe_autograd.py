@@ -106,3 +106,28 @@ def test_gradients_that_are_not_needed_are_none_in_a_kept_graph():
             inputs = [v.clone().requires_grad_(i == j) for j, v in enumerate(plain)]
             got, = torch.autograd.grad(call(*inputs).sum(), inputs[i], create_graph=True)
             assert torch.equal(got.detach(), want[i]), name
+
+
+def test_calls_without_a_gradient_refuse_tensors_that_require_one():
+    """New results and given ones (the native way), every floating input in turn."""
+    T, E, k, n = 40, 8, 2, 96
+    r = B.moe_route(torch.randn((T, E), generator=torch.Generator().manual_seed(1)).to(DEV), k)
+    x, ys, dy, g = tokens(T * k, n, BF16, 1), tokens(T * k, n, BF16, 2), tokens(T, n, BF16, 3), torch.rand((T, k), device=DEV)
+    ck = B.ck8_pack(x)
+    e = torch.empty_like
+    calls = [
+        (lambda v, out: B.moe_route_grad(*v, r["ids"], E, out=out), [g, r["weights"]], lambda: torch.empty((T, E), device=DEV)),
+        (lambda v, out: B.moe_combine_grad(v[0], v[1], r["place"], v[2], out=out), [dy, ys, r["weights"]],
+         lambda: {"dys": e(ys), "dweights": e(g)}),
+        (lambda v, out: B.gated_act_grad(v[0], ck, ck, out=out), [x], lambda: (e(x), e(x))),
+        (lambda v, out: B.ck8_pack(v[0], out=out), [x], lambda: B.Checkpoint8.empty(T * k, n, BF16, DEV)),
+    ]
+    for call, inputs, out in calls:
+        for given in (lambda: None, out):
+            call(inputs, given())
+            for i in range(len(inputs)):
+                v = [t.clone().requires_grad_(i == j) for j, t in enumerate(inputs)]
+                with pytest.raises(ValueError, match="has no gradient"):
+                    call(v, given())
+                with torch.no_grad():
+                    call(v, given())

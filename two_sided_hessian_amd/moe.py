@@ -158,6 +158,12 @@ def _without_out(out, what):
         raise ValueError(f"out cannot be given where {what} requires a gradient")
 
 
+def _no_gradient(call, *tensors):
+    """For calls whose results are not differentiable."""
+    if _grad_on() and any(t.requires_grad for t in tensors):
+        raise ValueError(f"{call} has no gradient: call it under torch.no_grad() or with detached tensors")
+
+
 def _top_k(top_k):
     if not 1 <= top_k <= BAKRON_MOE_MAX_TOP_K:
         raise ValueError(f"top_k must be 1 .. {BAKRON_MOE_MAX_TOP_K}")
@@ -260,7 +266,8 @@ def moe_route(logits, top_k, *, out=None, ws=None, stream=None):
 def moe_route_grad(dweights, weights, ids, experts, *, dtype=torch.float32, out=None, stream=None):
     """bakron_moe_route_grad: the gradient of moe_route's weights with respect to
     the logits, tokens x experts of ``dtype`` (or of out's), zero where an expert
-    was not chosen."""
+    was not chosen.  It has no gradient itself: tensors that require one are refused
+    unless under torch.no_grad()."""
     if out is not None and stream is None and _route_grad_at(dweights, weights, ids, experts, out):
         return out
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda or ids.dim() != 2:
@@ -271,6 +278,7 @@ def moe_route_grad(dweights, weights, ids, experts, *, dtype=torch.float32, out=
           _flat("ids", ids, torch.int32, (T, k), index)]
     if not k <= E <= BAKRON_MOE_MAX_EXPERTS:
         raise ValueError(f"experts must be {k} .. {BAKRON_MOE_MAX_EXPERTS}")
+    _no_gradient("moe_route_grad", dweights, weights)
     if _device() != index:
         with torch.cuda.device(index):
             return moe_route_grad(dweights, weights, ids, experts, dtype=dtype, out=out, stream=stream)
@@ -414,7 +422,8 @@ def moe_combine_grad(dy, ys, place, weights, *, out=None, stream=None):
     """bakron_moe_combine_grad: moe_combine's gradients, dict(dys, dweights):
     dys[place[t, j]] = weights[t, j] dy[t] and dweights[t, j] = dy[t] . ys[place[t, j]].
     ``out``: a dict of the two to write to.  Rows of dys that no choice has stay as
-    they are (in a new result: undefined)."""
+    they are (in a new result: undefined).  It has no gradient itself: tensors that
+    require one are refused unless under torch.no_grad()."""
     if out is not None and stream is None and _combine_grad_at(dy, ys, place, weights, out):
         return out
     if not isinstance(ys, torch.Tensor) or ys.dim() != 2:
@@ -424,6 +433,7 @@ def moe_combine_grad(dy, ys, place, weights, *, out=None, stream=None):
     T, k, at = _places(place, index)
     lddy = _output("dy", dy, T, n, ys.dtype, index)
     wp = _flat("weights", weights, torch.float32, (T, k), index)
+    _no_gradient("moe_combine_grad", dy, ys, weights)
     if _device() != index:
         with torch.cuda.device(index):
             return moe_combine_grad(dy, ys, place, weights, out=out, stream=stream)
@@ -559,13 +569,15 @@ def _checkpoint(name, ck, rows, cols, dtype, index):
 
 def ck8_pack(x, *, out=None, stream=None):
     """bakron_ck8_pack: the 8-bit checkpoint of a matrix in bfloat16 or float16
-    (rows contiguous).  ``out``: a Checkpoint8 of its size and type to write to."""
+    (rows contiguous).  ``out``: a Checkpoint8 of its size and type to write to.  It has
+    no gradient: x that requires one is refused unless under torch.no_grad()."""
     if out is not None and stream is None and _pack_at(x, out):
         return out
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a CUDA (HIP) tensor, rows x columns")
     rows, n = x.shape
     ldx, index = _rows("x", x, n), x.get_device()
+    _no_gradient("ck8_pack", x)
     if _device() != index:
         with torch.cuda.device(index):
             return ck8_pack(x, out=out, stream=stream)
@@ -674,7 +686,8 @@ def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, strea
 
 def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=None):
     """bakron_gated_act_grad: (da, db), the gradients of gated_act from the
-    checkpoints of a and b.  ``out``: a pair to write to; ``count``: as there."""
+    checkpoints of a and b.  ``out``: a pair to write to; ``count``: as there.  It has no
+    gradient itself: dh that requires one is refused unless under torch.no_grad()."""
     if out is not None and stream is None and _gated_grad_at(dh, ck_a, ck_b, _ACTS.get(act, -1), count, *out):
         return tuple(out)
     if not isinstance(dh, torch.Tensor) or dh.dim() != 2:
@@ -683,6 +696,7 @@ def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=N
     lddh, index, kind = _rows("dh", dh, n), dh.get_device(), _act(act)
     pa, pb = _checkpoint("ck_a", ck_a, rows, n, dh.dtype, index), _checkpoint("ck_b", ck_b, rows, n, dh.dtype, index)
     cp = None if count is None else _flat("count", count, torch.int32, (1,), index)
+    _no_gradient("gated_act_grad", dh)
     if _device() != index:
         with torch.cuda.device(index):
             return gated_act_grad(dh, ck_a, ck_b, act=act, count=count, out=out, stream=stream)
