@@ -43,8 +43,8 @@ struct Names {
 } names;
 PyObject *layer_type = nullptr, *checkpoint_type = nullptr;
 
-// A tensor that is a plain one on the current device, without a gradient to
-// take; -1 in `device` is set by the first of a call's tensors.
+// A tensor that is a plain one on the current device, without a gradient or a tangent
+// to take; -1 in `device` is set by the first of a call's tensors.
 const at::Tensor* plain(PyObject* o, int& device)
 {
     if (!THPVariable_CheckExact(o)) return nullptr;
@@ -57,6 +57,7 @@ const at::Tensor* plain(PyObject* o, int& device)
         return nullptr;
     }
     if (t.requires_grad() && c10::GradMode::is_enabled()) return nullptr;
+    if (t._fw_grad(0).defined()) return nullptr;   // (a dual tensor of forward mode)
     return &t;
 }
 

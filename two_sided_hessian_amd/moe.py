@@ -97,6 +97,8 @@ def _matrix(name, t, cols=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     _type_of(name, t.dtype)
+    if _q._forward._current_level >= 0:
+        _q._no_tangent(name, t)
     if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must have shape (rows, {'columns' if cols is None else cols}), got {tuple(t.shape)}")
     rows, cols = t.shape
@@ -116,6 +118,8 @@ def _flat(name, t, dtype, shape, index):
             t.get_device() == index):
         _b._check_dev(name, t, dtype, shape)
         _one_device(index, None, **{name: t})
+    if _q._forward._current_level >= 0:
+        _q._no_tangent(name, t)
     return t.data_ptr()
 
 

@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from . import _binding as _b
 
@@ -129,10 +130,18 @@ def q4_moe_workspace_bytes(tokens: int, w_gate: Q4Weight, top_k: int) -> int:
     return _b.lib().bakron_q4_moe_workspace_bytes(tokens, w_gate.n, w_gate.m, w_gate.count, top_k, w_gate._group)
 
 
+def _no_tangent(name, t):
+    """Refuses a dual tensor of forward-mode autograd, whose tangent the calls would drop."""
+    if _forward.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} has a forward-mode tangent, and the call has no derivative in forward mode")
+
+
 def _rows(name, t, cols, like=None):
     """Leading dimension of a tokens x cols matrix whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if _forward._current_level >= 0:   # (inside a dual_level)
+        _no_tangent(name, t)
     if t.dtype not in _TYPES or (like is not None and t.dtype != like):
         raise TypeError(f"{name} must be {like or 'torch.bfloat16 or torch.float16'}, got {t.dtype}")
     shape = t.shape
@@ -330,6 +339,8 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
             router.shape == (E, h) and router.is_contiguous()):
         _b._check_dev("router", router, dtype, (E, h))
         _one_device(index, None, router=router)
+    if _forward._current_level >= 0:
+        _no_tangent("router", router)
     if _device() != index:
         with torch.cuda.device(index):
             return q4_moe(x, router, w_gate, w_up, w_down, top_k, out=out, ws=ws, stream=stream)
