@@ -4,9 +4,9 @@
 // One decoding token's calls take 3 us on the GPU; checking their arguments from
 // Python took 3 us more on the host, and passing them through ctypes 1.5.  Each
 // function here looks at the same things as its namesake in moe.py and enqueues
-// the call where all of them are in order (True); in any other case it does
-// nothing (False), and moe.py takes the call, raises what there is to raise, or
-// hands it to autograd.  Tensors on another device than the current one, other
+// the call where all of them are in order (True, or the exception of a launch that
+// failed); in any other case it does nothing (False), and moe.py takes the call, raises
+// what there is to raise, or hands it to autograd.  Tensors on another device than the current one, other
 // streams than the current one, and subclasses of Tensor are its too.
 #include <Python.h>
 #include <dlfcn.h>
@@ -41,7 +41,7 @@ struct Names {
     NAMES(X)
 #undef X
 } names;
-PyObject *layer_type = nullptr, *checkpoint_type = nullptr;
+PyObject *layer_type = nullptr, *checkpoint_type = nullptr, *error_type = nullptr;
 
 // A tensor that is a plain one on the current device, without a gradient or a tangent
 // to take; -1 in `device` is set by the first of a call's tensors.
@@ -192,7 +192,19 @@ const int32_t* count_of(PyObject* o, int& device, bool& ok)
 }
 
 hipStream_t stream(int device) { return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream(); }
-PyObject* answer(int rc) { return PyBool_FromLong(rc == BAKRON_SUCCESS); }
+// What the library says to a call: refusals, which come before anything is enqueued, are
+// moe.py's to raise (or to mend, where a workspace is what is missing).  An error of a launch
+// is raised here: what the call enqueued before it must not be enqueued again.
+PyObject* answer(const char* call, int rc)
+{
+    if (rc == BAKRON_SUCCESS) Py_RETURN_TRUE;
+    if (rc == BAKRON_ERR_NULL_POINTER || rc == BAKRON_ERR_BAD_SIZE || rc == BAKRON_ERR_WORKSPACE || rc == BAKRON_ERR_BAD_ARG)
+        Py_RETURN_FALSE;
+    PyObject* e = PyObject_CallFunction(error_type, "is", rc, call);
+    if (e) PyErr_SetObject(error_type, e);
+    Py_XDECREF(e);
+    return nullptr;
+}
 PyObject* entry(PyObject* d, PyObject* name)
 {
     return PyDict_CheckExact(d) ? PyDict_GetItemWithError(d, name) : nullptr;
@@ -203,6 +215,7 @@ PyObject* entry(PyObject* d, PyObject* name)
     int dev = -1;
 #define NEED(cond) \
     if (!(cond)) Py_RETURN_FALSE
+#define CALL(call, ...) answer(#call, lib.call(__VA_ARGS__))
 
 // logits, top_k, out, ws
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
@@ -220,8 +233,8 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* ws;
     size_t bytes;
     NEED(T && ids && weights && place && order && offsets && workspace(a[3], dev, ws, bytes));
-    return answer(lib.bakron_moe_route(l.p, l.ld, T, l.type, E, (int32_t)k, ids, weights, place, order, offsets, ws, bytes,
-                                       stream(dev)));
+    return CALL(bakron_moe_route, l.p, l.ld, T, l.type, E, (int32_t)k, ids, weights, place, order, offsets, ws, bytes,
+                stream(dev));
 }
 
 // dweights, weights, ids, experts, out
@@ -237,7 +250,7 @@ PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     const float *g = (const float*)flat(a[0], dev, at::kFloat, d.rows, k), *w = (const float*)flat(a[1], dev, at::kFloat, d.rows, k);
     const int32_t* ids = (const int32_t*)flat(a[2], dev, at::kInt, d.rows, k);
     NEED(k >= 1 && k <= BAKRON_MOE_MAX_TOP_K && g && w && ids);
-    return answer(lib.bakron_moe_route_grad(g, w, ids, d.rows, E, (int32_t)k, d.p, d.ld, d.type, stream(dev)));
+    return CALL(bakron_moe_route_grad, g, w, ids, d.rows, E, (int32_t)k, d.p, d.ld, d.type, stream(dev));
 }
 
 // x, place, out
@@ -249,7 +262,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int32_t* place;
     NEED(matrix(a[0], dev, x) && places(a[1], dev, T, k, place) && x.rows == T && matrix(a[2], dev, xs) && xs.cols == x.cols &&
          xs.type == x.type);
-    return answer(lib.bakron_moe_gather(x.p, x.ld, T, x.type, x.cols, (int32_t)k, place, xs.p, xs.ld, xs.rows, stream(dev)));
+    return CALL(bakron_moe_gather, x.p, x.ld, T, x.type, x.cols, (int32_t)k, place, xs.p, xs.ld, xs.rows, stream(dev));
 }
 
 // ys, place, weights, out
@@ -262,7 +275,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
     const float* w = nullptr;
     NEED(matrix(a[0], dev, ys) && places(a[1], dev, T, k, place) && matrix_like(a[3], dev, y, T, ys.cols, ys.type));
     NEED(a[2] == Py_None || (w = (const float*)flat(a[2], dev, at::kFloat, T, k)));
-    return answer(lib.bakron_moe_combine(ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, y.p, y.ld, stream(dev)));
+    return CALL(bakron_moe_combine, ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, y.p, y.ld, stream(dev));
 }
 
 // dy, ys, place, weights, out
@@ -277,8 +290,8 @@ PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     float* dw = (float*)flat(entry(a[4], names.dweights), dev, at::kFloat, T, k);
     PyObject* o = entry(a[4], names.dys);
     NEED(w && dw && o && matrix_like(o, dev, dys, ys.rows, ys.cols, ys.type));
-    return answer(lib.bakron_moe_combine_grad(dy.p, dy.ld, ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, dys.p,
-                                              dys.ld, dw, stream(dev)));
+    return CALL(bakron_moe_combine_grad, dy.p, dy.ld, ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, dys.p,
+                dys.ld, dw, stream(dev));
 }
 
 // x, w, offsets, out, ws
@@ -293,7 +306,8 @@ PyObject* experts_of(bool grad, PyObject* const* a, Py_ssize_t n)
          matrix_like(a[3], dev, y, x.rows, grad ? w.n : w.m, x.type) && workspace(a[4], dev, ws, bytes));
     const int32_t* offsets = (const int32_t*)flat(a[2], dev, at::kInt, w.count + 1);
     NEED(offsets);
-    return answer((grad ? lib.bakron_q4_experts_grad : lib.bakron_q4_experts)(x.p, x.ld, x.rows, x.type, w.p, w.count, w.m, w.n, w.group,
+    return answer(grad ? "bakron_q4_experts_grad" : "bakron_q4_experts",
+                  (grad ? lib.bakron_q4_experts_grad : lib.bakron_q4_experts)(x.p, x.ld, x.rows, x.type, w.p, w.count, w.m, w.n, w.group,
                                                                              offsets, y.p, y.ld, ws, bytes, stream(dev)));
 }
 PyObject* experts(PyObject*, PyObject* const* a, Py_ssize_t n) { return experts_of(false, a, n); }
@@ -306,7 +320,7 @@ PyObject* pack(PyObject*, PyObject* const* a, Py_ssize_t n)
     Matrix x;
     void* ck;
     NEED(matrix(a[0], dev, x) && (ck = checkpoint(a[1], dev, x.rows, x.cols, x.type)));
-    return answer(lib.bakron_ck8_pack(x.p, x.ld, x.rows, x.type, x.cols, ck, stream(dev)));
+    return CALL(bakron_ck8_pack, x.p, x.ld, x.rows, x.type, x.cols, ck, stream(dev));
 }
 
 // a, b, kind, checkpoints (None or a pair), count, out
@@ -325,8 +339,8 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
              (ca = checkpoint(PyTuple_GET_ITEM(a[3], 0), dev, x.rows, x.cols, x.type)) &&
              (cb = checkpoint(PyTuple_GET_ITEM(a[3], 1), dev, x.rows, x.cols, x.type));
     NEED(ok);
-    return answer(lib.bakron_gated_act(x.p, x.ld, y.p, y.ld, x.rows, x.type, x.cols, (int32_t)kind, count, h.p, h.ld, ca, cb,
-                                       stream(dev)));
+    return CALL(bakron_gated_act, x.p, x.ld, y.p, y.ld, x.rows, x.type, x.cols, (int32_t)kind, count, h.p, h.ld, ca, cb,
+                stream(dev));
 }
 
 // dh, ck_a, ck_b, kind, count, da, db
@@ -341,14 +355,14 @@ PyObject* gated_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int32_t* count = count_of(a[4], dev, ok);
     void *ca = checkpoint(a[1], dev, d.rows, d.cols, d.type), *cb = checkpoint(a[2], dev, d.rows, d.cols, d.type);
     NEED(ok && ca && cb);
-    return answer(lib.bakron_gated_act_grad(d.p, d.ld, ca, cb, d.rows, d.type, d.cols, (int32_t)kind, count, da.p, da.ld, db.p, db.ld,
-                                            stream(dev)));
+    return CALL(bakron_gated_act_grad, d.p, d.ld, ca, cb, d.rows, d.type, d.cols, (int32_t)kind, count, da.p, da.ld, db.p, db.ld,
+                stream(dev));
 }
 
-// path of the library, Q4Weight, Checkpoint8
+// path of the library, Q4Weight, Checkpoint8, BakronError
 PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    const char* path = n == 3 ? PyUnicode_AsUTF8(a[0]) : nullptr;
+    const char* path = n == 4 ? PyUnicode_AsUTF8(a[0]) : nullptr;
     void* h = path ? dlopen(path, RTLD_NOW | RTLD_LOCAL) : nullptr;
     if (PyErr_Occurred()) return nullptr;
     if (!h) return PyErr_SetString(PyExc_RuntimeError, "the library cannot be loaded"), nullptr;
@@ -363,10 +377,10 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (!names.name) return nullptr;
     NAMES(X)
 #undef X
-    Py_INCREF(a[1]);
-    Py_INCREF(a[2]);
+    for (int i = 1; i < 4; ++i) Py_INCREF(a[i]);
     Py_XSETREF(layer_type, a[1]);
     Py_XSETREF(checkpoint_type, a[2]);
+    Py_XSETREF(error_type, a[3]);
     lib = l;
     Py_RETURN_NONE;
 }

@@ -81,7 +81,7 @@ def _get_ready():
     """The library's functions for _fast, which declines every call until then."""
     global _ready
     _b.lib()
-    _fast.load(_b.LIB_PATH, Q4Weight, Checkpoint8)
+    _fast.load(_b.LIB_PATH, Q4Weight, Checkpoint8, _b.BakronError)
     _ready = True
 
 
