@@ -5,9 +5,12 @@
 //
 // With few rows of dy the codes are what is read, and a weight formed for each code
 // would take most of the time: the step goes to dy's side instead, once per row of dy
-// and group, and the codes enter the MFMAs as the exact numbers u.  a is kept as two
-// bfloat16 terms (16 bits of mantissa), the second sum, one number per row of dy and
-// group, in float32; it comes off after at most 256 rows of W of a wave, since the first
+// and group, and the codes enter the MFMAs as the exact numbers u.  a is rounded to 16
+// bits, which two bfloat16 terms hold exactly, and both sums are of that number: what the
+// rounding leaves (2^-16 of a at most) is weighted by c - z then.  With a itself in the
+// second sum it is weighted by 16 + c, which rows of W that are alike do not average out
+// (14336 of them: 0.77 of a float16 result's rounding).  The second sum, one number per row of dy and
+// group, is float32; it comes off after at most 256 rows of W of a wave, since the first
 // one grows with the mean of a where the result does not.
 //
 // The sum runs over W's rows, and a packed dword holds eight columns of one row.  A lane
@@ -21,7 +24,7 @@
 // different banks.  The LDS is a wave's own: no barrier is involved.
 //
 // HBM bounds it up to some 16 rows of dy (16 tokens, 2 of 8 experts of 14336 x 4096: 55 us,
-// 4.7 TB/s), then the vector instructions that split a: 64 tokens, 103 us.  A weight formed
+// 4.7 TB/s), then the vector instructions that split a: 64 tokens, 106 us.  A weight formed
 // for every code, as with many rows, took 117 us of 16 tokens.
 #pragma once
 
@@ -42,6 +45,9 @@ __device__ __forceinline__ void wait_loads()
 {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
 }
+
+// What two bfloat16 terms hold of a value: its first 16 bits, rounded to nearest.
+__device__ __forceinline__ uint32_t two_terms(float v) { return (__float_as_uint(v) + 0x80u) & 0xFFFFFF00u; }
 
 // 16 SETS rows of dy, the 128 columns of block kb of W.  HALF: the block's halves have
 // grids of their own.  acc[.][.][e]: columns 64 (d >> 1) + 16 q + 8 (d & 1) + e, q = lane / 4
@@ -133,10 +139,13 @@ struct GradFew {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float a = f[t][2 * i] * sz[i].x, b = f[t][2 * i + 1] * sz[i].z;
-                    off[t][h] = fmaf(a, sz[i].y + kQ4Offset, off[t][h]);
-                    off[t][h] = fmaf(b, sz[i].w + kQ4Offset, off[t][h]);
-                    hi[i] = Bf16::down2(a, b);
-                    lo[i] = Bf16::down2(a - Bf16::up((uint16_t)hi[i]), b - __uint_as_float(hi[i] & 0xFFFF0000u));
+                    const uint32_t a16 = two_terms(a), b16 = two_terms(b);
+                    const float ha = __uint_as_float(a16 & 0xFFFF0000u), hb = __uint_as_float(b16 & 0xFFFF0000u);
+                    const float la = __uint_as_float(a16) - ha, lb = __uint_as_float(b16) - hb;   // (8 bits each)
+                    hi[i] = __builtin_amdgcn_perm(b16, a16, 0x07060302u);   // the upper halves
+                    lo[i] = __builtin_amdgcn_perm(__float_as_uint(lb), __float_as_uint(la), 0x07060302u);
+                    off[t][h] = fmaf(__uint_as_float(a16), sz[i].y + kQ4Offset, off[t][h]);
+                    off[t][h] = fmaf(__uint_as_float(b16), sz[i].w + kQ4Offset, off[t][h]);
                 }
                 st.hi[t][h] = __builtin_bit_cast(bf16x8, hi);
                 st.lo[t][h] = __builtin_bit_cast(bf16x8, lo);
