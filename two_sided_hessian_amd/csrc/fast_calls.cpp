@@ -24,8 +24,8 @@ namespace {
 
 #define CALLS(X)                                                                                                          \
     X(bakron_moe_route) X(bakron_moe_route_grad) X(bakron_moe_gather) X(bakron_moe_combine) X(bakron_moe_combine_grad)    \
-    X(bakron_q4_experts) X(bakron_q4_experts_grad) X(bakron_ck8_pack) X(bakron_ck8_unpack) X(bakron_gated_act)            \
-    X(bakron_gated_act_grad) X(bakron_ck8_bytes)
+    X(bakron_q4_experts) X(bakron_q4_experts_grad) X(bakron_ck8_pack) X(bakron_gated_act) X(bakron_gated_act_grad)        \
+    X(bakron_ck8_bytes)
 struct Library {
 #define X(name) decltype(&::name) name = nullptr;
     CALLS(X)

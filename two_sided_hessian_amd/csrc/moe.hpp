@@ -9,7 +9,6 @@ namespace bk {
 // A third activation type beside Bf16 and Fp16 (q4.hpp), for logits and
 // unpacked checkpoints: raw 32-bit storage.
 struct Fp32 {
-    typedef uint32_t raw;
     static __device__ __forceinline__ float up(uint32_t v) { return __uint_as_float(v); }
     static __device__ __forceinline__ uint32_t down(float v) { return __float_as_uint(v); }
 };

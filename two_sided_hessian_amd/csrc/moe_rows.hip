@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256) void k_moe_combine_grad(const uint16_t* __rest
     }
 }
 
-// rows x cols zeros
+// n zeros
 __global__ __launch_bounds__(256) void k_moe_zero(float* __restrict__ v, int64_t n)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) v[i] = 0.f;

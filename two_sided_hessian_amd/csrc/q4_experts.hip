@@ -665,7 +665,7 @@ static void experts_run(const ExpertsCall& c)
                 (int)c.rows, w.n, w.gb, p.pieces, reinterpret_cast<float*>(c.ws), p.lds_, copy, p.ldc);
     if (!direct) x = copy, ldx = p.ldc;
     if (p.TA == 4) experts_launch<X, 4, 4, false>(c, p, w, x, ldx);
-    else if (p.TA == 2) (own ? experts_launch<X, 2, 2, true> : experts_launch<X, 2, 2, false>)(c, p, w, x, ldx);
+    else if (p.TA == 2) experts_launch<X, 2, 2, false>(c, p, w, x, ldx);
     else (own ? experts_launch<X, 1, 2, true> : experts_launch<X, 1, 2, false>)(c, p, w, x, ldx);
     experts_parts<X>(c, p, w.m);
 }

@@ -95,13 +95,13 @@ struct TileShape {
 struct TileChoice {
     int shape, splits;
 };
-template <int N, class Tiles>   // tiles(tokens): how many blocks of so many tokens there are
-inline TileChoice tile_choose_of(const TileShape (&shapes)[N], Tiles tiles_of, int64_t T, int64_t cols, int64_t depth, int64_t most)
+template <int N>
+inline TileChoice tile_choose(const TileShape (&shapes)[N], int64_t T, int64_t cols, int64_t depth, int64_t most)
 {
     TileChoice best = {0, 1};
     double least = 0.0;
     for (int i = 0; i < N; ++i) {
-        const int64_t tiles = tiles_of(shapes[i].tokens) * ceil_div(cols, shapes[i].cols);
+        const int64_t tiles = ceil_div(T, shapes[i].tokens) * ceil_div(cols, shapes[i].cols);
         for (int s = 1; s == 1 || (s <= most && tiles * s <= 1024); ++s) {
             const double us = ceil_div(tiles * s, 256) * shapes[i].us * depth / (4096.0 * s) +
                               (s > 1 ? 2.0 + 8.0e-6 / 4 * s * T * cols : 0.0);
@@ -109,11 +109,6 @@ inline TileChoice tile_choose_of(const TileShape (&shapes)[N], Tiles tiles_of, i
         }
     }
     return best;
-}
-template <int N>
-inline TileChoice tile_choose(const TileShape (&shapes)[N], int64_t T, int64_t cols, int64_t depth, int64_t most)
-{
-    return tile_choose_of(shapes, [T](int tokens) { return ceil_div(T, tokens); }, T, cols, depth, most);
 }
 
 // A padded copy of x (T x n, n rounded up to 64 columns, zeros beyond n).
