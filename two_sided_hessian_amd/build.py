@@ -3,7 +3,8 @@
 Each .hip file under csrc/ is compiled separately (in parallel) into
 _build/ and linked into two_sided_hessian_amd/libbakron.so.  fast_calls.cpp
 becomes two_sided_hessian_amd/_fast.so beside it, a Python module that calls
-the library (host code only, torch's headers).
+the library (host code only, torch's headers).  The library needs neither torch nor
+that module: where it cannot be built, the build says so and goes on without it.
 """
 from __future__ import annotations
 
@@ -49,8 +50,6 @@ def fast_command(out: str) -> list:
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     procs = []
-    fast = FAST + ".tmp%d" % os.getpid()
-    procs.append(("fast_calls.cpp", subprocess.Popen(fast_command(fast), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     objs = []
     for s in SOURCES:
         obj = os.path.join(BUILD, s.replace(".hip", ".o"))
@@ -59,6 +58,11 @@ def build(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((s, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    fast, fast_proc, why = FAST + ".tmp%d" % os.getpid(), None, ""
+    try:
+        fast_proc = subprocess.Popen(fast_command(fast), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except (ImportError, OSError) as e:   # no torch, or no host compiler
+        why = str(e)
     failed = []
     for s, p in procs:
         out = p.communicate()[0].decode(errors="replace")
@@ -67,13 +71,23 @@ def build(verbose: bool = False) -> str:
             failed.append((s, out))
         elif verbose and out.strip():
             print(out)
+    if fast_proc is not None:
+        why = fast_proc.communicate()[0].decode(errors="replace")
     if failed:
+        if os.path.exists(fast):
+            os.remove(fast)
         raise RuntimeError("hipcc failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
-    os.replace(fast, FAST)
+    if fast_proc is not None and fast_proc.returncode == 0:
+        os.replace(fast, FAST)
+    else:
+        for left in (fast, FAST):   # one of another build's might not fit this library
+            if os.path.exists(left):
+                os.remove(left)
+        print(f"{os.path.basename(FAST)} is not built, its calls go through ctypes:\n{why}", file=sys.stderr)
     return LIB
 
 
