@@ -192,12 +192,28 @@ const int32_t* count_of(PyObject* o, int& device, bool& ok)
 }
 
 hipStream_t stream(int device) { return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream(); }
+
+// A given output, or an object that keeps one as its `data`, counts as changed in place
+// (moe.py's _written); null: none.
+void written(PyObject* o)
+{
+    PyObject* t = !o ? nullptr : THPVariable_CheckExact(o) ? Py_NewRef(o) : PyObject_GetAttr(o, names.data);
+    if (!t) return PyErr_Clear();
+    const at::Tensor& v = THPVariable_Unpack(t);   // (checked before the call)
+    if (!v.is_inference()) v.unsafeGetTensorImpl()->bump_version();
+    Py_DECREF(t);
+}
+
 // What the library says to a call: refusals, which come before anything is enqueued, are
 // moe.py's to raise (or to mend, where a workspace is what is missing).  An error of a launch
 // is raised here: what the call enqueued before it must not be enqueued again.
-PyObject* answer(const char* call, int rc)
+template <class... Outputs>
+PyObject* answer(const char* call, int rc, Outputs... outputs)
 {
-    if (rc == BAKRON_SUCCESS) Py_RETURN_TRUE;
+    if (rc == BAKRON_SUCCESS) {
+        (written(outputs), ...);
+        Py_RETURN_TRUE;
+    }
     if (rc == BAKRON_ERR_NULL_POINTER || rc == BAKRON_ERR_BAD_SIZE || rc == BAKRON_ERR_WORKSPACE || rc == BAKRON_ERR_BAD_ARG)
         Py_RETURN_FALSE;
     PyObject* e = PyObject_CallFunction(error_type, "is", rc, call);
@@ -215,7 +231,7 @@ PyObject* entry(PyObject* d, PyObject* name)
     int dev = -1;
 #define NEED(cond) \
     if (!(cond)) Py_RETURN_FALSE
-#define CALL(call, ...) answer(#call, lib.call(__VA_ARGS__))
+#define CALL(call, args, ...) answer(#call, lib.call args, __VA_ARGS__)
 
 // logits, top_k, out, ws
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
@@ -233,8 +249,10 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* ws;
     size_t bytes;
     NEED(T && ids && weights && place && order && offsets && workspace(a[3], dev, ws, bytes));
-    return CALL(bakron_moe_route, l.p, l.ld, T, l.type, E, (int32_t)k, ids, weights, place, order, offsets, ws, bytes,
-                stream(dev));
+    return CALL(bakron_moe_route, (l.p, l.ld, T, l.type, E, (int32_t)k, ids, weights, place, order, offsets, ws, bytes,
+                stream(dev)),
+                entry(a[2], names.ids), entry(a[2], names.weights), entry(a[2], names.place), entry(a[2], names.order),
+                entry(a[2], names.offsets));
 }
 
 // dweights, weights, ids, experts, out
@@ -250,7 +268,7 @@ PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     const float *g = (const float*)flat(a[0], dev, at::kFloat, d.rows, k), *w = (const float*)flat(a[1], dev, at::kFloat, d.rows, k);
     const int32_t* ids = (const int32_t*)flat(a[2], dev, at::kInt, d.rows, k);
     NEED(k >= 1 && k <= BAKRON_MOE_MAX_TOP_K && g && w && ids);
-    return CALL(bakron_moe_route_grad, g, w, ids, d.rows, E, (int32_t)k, d.p, d.ld, d.type, stream(dev));
+    return CALL(bakron_moe_route_grad, (g, w, ids, d.rows, E, (int32_t)k, d.p, d.ld, d.type, stream(dev)), a[4]);
 }
 
 // x, place, out
@@ -262,7 +280,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int32_t* place;
     NEED(matrix(a[0], dev, x) && places(a[1], dev, T, k, place) && x.rows == T && matrix(a[2], dev, xs) && xs.cols == x.cols &&
          xs.type == x.type);
-    return CALL(bakron_moe_gather, x.p, x.ld, T, x.type, x.cols, (int32_t)k, place, xs.p, xs.ld, xs.rows, stream(dev));
+    return CALL(bakron_moe_gather, (x.p, x.ld, T, x.type, x.cols, (int32_t)k, place, xs.p, xs.ld, xs.rows, stream(dev)), a[2]);
 }
 
 // ys, place, weights, out
@@ -275,7 +293,8 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
     const float* w = nullptr;
     NEED(matrix(a[0], dev, ys) && places(a[1], dev, T, k, place) && matrix_like(a[3], dev, y, T, ys.cols, ys.type));
     NEED(a[2] == Py_None || (w = (const float*)flat(a[2], dev, at::kFloat, T, k)));
-    return CALL(bakron_moe_combine, ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, y.p, y.ld, stream(dev));
+    return CALL(bakron_moe_combine, (ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, y.p, y.ld, stream(dev)),
+                a[3]);
 }
 
 // dy, ys, place, weights, out
@@ -290,8 +309,8 @@ PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     float* dw = (float*)flat(entry(a[4], names.dweights), dev, at::kFloat, T, k);
     PyObject* o = entry(a[4], names.dys);
     NEED(w && dw && o && matrix_like(o, dev, dys, ys.rows, ys.cols, ys.type));
-    return CALL(bakron_moe_combine_grad, dy.p, dy.ld, ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, dys.p,
-                dys.ld, dw, stream(dev));
+    return CALL(bakron_moe_combine_grad, (dy.p, dy.ld, ys.p, ys.ld, ys.rows, ys.type, ys.cols, (int32_t)k, place, w, T, dys.p,
+                dys.ld, dw, stream(dev)), o, entry(a[4], names.dweights));
 }
 
 // x, w, offsets, out, ws
@@ -306,9 +325,9 @@ PyObject* experts_of(bool grad, PyObject* const* a, Py_ssize_t n)
          matrix_like(a[3], dev, y, x.rows, grad ? w.n : w.m, x.type) && workspace(a[4], dev, ws, bytes));
     const int32_t* offsets = (const int32_t*)flat(a[2], dev, at::kInt, w.count + 1);
     NEED(offsets);
-    return answer(grad ? "bakron_q4_experts_grad" : "bakron_q4_experts",
-                  (grad ? lib.bakron_q4_experts_grad : lib.bakron_q4_experts)(x.p, x.ld, x.rows, x.type, w.p, w.count, w.m, w.n, w.group,
-                                                                             offsets, y.p, y.ld, ws, bytes, stream(dev)));
+    const auto run = grad ? lib.bakron_q4_experts_grad : lib.bakron_q4_experts;
+    const int rc = run(x.p, x.ld, x.rows, x.type, w.p, w.count, w.m, w.n, w.group, offsets, y.p, y.ld, ws, bytes, stream(dev));
+    return answer(grad ? "bakron_q4_experts_grad" : "bakron_q4_experts", rc, a[3]);
 }
 PyObject* experts(PyObject*, PyObject* const* a, Py_ssize_t n) { return experts_of(false, a, n); }
 PyObject* experts_grad(PyObject*, PyObject* const* a, Py_ssize_t n) { return experts_of(true, a, n); }
@@ -320,7 +339,7 @@ PyObject* pack(PyObject*, PyObject* const* a, Py_ssize_t n)
     Matrix x;
     void* ck;
     NEED(matrix(a[0], dev, x) && (ck = checkpoint(a[1], dev, x.rows, x.cols, x.type)));
-    return CALL(bakron_ck8_pack, x.p, x.ld, x.rows, x.type, x.cols, ck, stream(dev));
+    return CALL(bakron_ck8_pack, (x.p, x.ld, x.rows, x.type, x.cols, ck, stream(dev)), a[1]);
 }
 
 // a, b, kind, checkpoints (None or a pair), count, out
@@ -339,8 +358,8 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
              (ca = checkpoint(PyTuple_GET_ITEM(a[3], 0), dev, x.rows, x.cols, x.type)) &&
              (cb = checkpoint(PyTuple_GET_ITEM(a[3], 1), dev, x.rows, x.cols, x.type));
     NEED(ok);
-    return CALL(bakron_gated_act, x.p, x.ld, y.p, y.ld, x.rows, x.type, x.cols, (int32_t)kind, count, h.p, h.ld, ca, cb,
-                stream(dev));
+    return CALL(bakron_gated_act, (x.p, x.ld, y.p, y.ld, x.rows, x.type, x.cols, (int32_t)kind, count, h.p, h.ld, ca, cb,
+                stream(dev)), a[5], ca ? PyTuple_GET_ITEM(a[3], 0) : nullptr, cb ? PyTuple_GET_ITEM(a[3], 1) : nullptr);
 }
 
 // dh, ck_a, ck_b, kind, count, da, db
@@ -355,8 +374,8 @@ PyObject* gated_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int32_t* count = count_of(a[4], dev, ok);
     void *ca = checkpoint(a[1], dev, d.rows, d.cols, d.type), *cb = checkpoint(a[2], dev, d.rows, d.cols, d.type);
     NEED(ok && ca && cb);
-    return CALL(bakron_gated_act_grad, d.p, d.ld, ca, cb, d.rows, d.type, d.cols, (int32_t)kind, count, da.p, da.ld, db.p, db.ld,
-                stream(dev));
+    return CALL(bakron_gated_act_grad, (d.p, d.ld, ca, cb, d.rows, d.type, d.cols, (int32_t)kind, count, da.p, da.ld, db.p,
+                db.ld, stream(dev)), a[5], a[6]);
 }
 
 // path of the library, Q4Weight, Checkpoint8, BakronError

@@ -9,6 +9,8 @@ outputs are given (decoding steps, captured or not) are tried by _fast first,
 which checks and enqueues them in native code (csrc/fast_calls.cpp) and leaves
 everything else, refusals among it, to the code here.
 
+Given outputs count as changed in place, as torch's own do.
+
 Autograd: moe_route (weights), moe_gather, moe_combine, q4_experts, gated_act
 and q4_moe_layer take part in it where an input requires a gradient and ``out``
 is not given.  Gradients with respect to sorted rows that no choice has are
@@ -22,7 +24,7 @@ import torch
 
 from . import _binding as _b
 from . import q4 as _q
-from .q4 import Q4Weight, _calls, _check, _device, _grad_on, _made, _on, _one_device, _raw_stream, _rows
+from .q4 import Q4Weight, _calls, _check, _device, _grad_on, _made, _on, _one_device, _raw_stream, _rows, _written
 
 BAKRON_MOE_F32 = 2
 BAKRON_MOE_SILU = 0
@@ -264,6 +266,7 @@ def moe_route(logits, top_k, *, out=None, ws=None, stream=None):
     ws = _space(ws, moe_route_workspace_bytes(T, E, k), logits.device, index, stream)
     wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     _run("bakron_moe_route", logits.data_ptr(), ld, T, _TYPES3[logits.dtype], E, k, *at, wp, wn, s)
+    _written(*(out[name] for name in _ROUTE))
     return out
 
 
@@ -294,6 +297,7 @@ def moe_route_grad(dweights, weights, ids, experts, *, dtype=torch.float32, out=
     if out.shape[0] != T or out.get_device() != index:
         raise ValueError(f"out must be a ({T}, {E}) tensor on cuda:{index}")
     _run("bakron_moe_route_grad", *at, T, E, k, out.data_ptr(), ld, _TYPES3[out.dtype], s)
+    _written(out)
     return out
 
 
@@ -345,6 +349,7 @@ def moe_gather(x, place, *, out=None, stream=None):
         out = _made(stream, lambda: (x.new_empty((T * k, n)),))[0]
     ldo = _output("out", out, out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else 0, n, x.dtype, index)
     _run("bakron_moe_gather", x.data_ptr(), ldx, T, _TYPES[x.dtype], n, k, at, out.data_ptr(), ldo, out.shape[0], s)
+    _written(out)
     return out
 
 
@@ -419,6 +424,7 @@ def moe_combine(ys, place, weights=None, *, out=None, stream=None):
     else:
         ldo = _output("out", out, T, n, ys.dtype, index)
     _run("bakron_moe_combine", ys.data_ptr(), ldys, rows, _TYPES[ys.dtype], n, k, at, wp, T, out.data_ptr(), ldo, s)
+    _written(out)
     return out
 
 
@@ -449,6 +455,7 @@ def moe_combine_grad(dy, ys, place, weights, *, out=None, stream=None):
     ldo, dw = _output("out['dys']", dys, rows, n, ys.dtype, index), _flat("out['dweights']", out["dweights"], torch.float32, (T, k), index)
     _run("bakron_moe_combine_grad", dy.data_ptr(), lddy, ys.data_ptr(), ldys, rows, _TYPES[ys.dtype], n, k, at, wp, T,
          dys.data_ptr(), ldo, dw, s)
+    _written(out["dys"], out["dweights"])
     return out
 
 
@@ -505,6 +512,7 @@ def _experts(call, size, name, x, w, offsets, out, ws, stream):
     wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     _run(call, x.data_ptr(), ldx, R, _TYPES[x.dtype], data.data_ptr(), w.count, w.m, w.n, w._group, at, out.data_ptr(), ldo,
          wp, wn, s)
+    _written(out)
     return out
 
 
@@ -591,6 +599,7 @@ def ck8_pack(x, *, out=None, stream=None):
         out = Checkpoint8(data, rows, n, x.dtype)
     at = _checkpoint("out", out, rows, n, x.dtype, index)
     _run("bakron_ck8_pack", x.data_ptr(), ldx, rows, _TYPES[x.dtype], n, at, s)
+    _written(out.data)
     return out
 
 
@@ -616,6 +625,7 @@ def ck8_unpack(ck, *, dtype=None, out=None, stream=None):
     if out.shape[0] != ck.rows or out.get_device() != index:
         raise ValueError(f"out must be a ({ck.rows}, {ck.cols}) tensor on cuda:{index}")
     _run("bakron_ck8_unpack", at, ck.rows, ck.cols, _TYPES3[out.dtype], out.data_ptr(), ld, s)
+    _written(out)
     return out
 
 
@@ -685,7 +695,11 @@ def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, strea
         ca, cb = (_checkpoint("checkpoint", c, rows, n, a.dtype, index) for c in checkpoint)
     _run("bakron_gated_act", a.data_ptr(), lda, b.data_ptr(), ldb, rows, _TYPES[a.dtype], n, kind, cp, out.data_ptr(), ldo,
          ca, cb, s)
-    return out if ca is None and checkpoint is False else (out, *checkpoint)
+    if checkpoint is False:
+        _written(out)
+        return out
+    _written(out, *(c.data for c in checkpoint))
+    return (out, *checkpoint)
 
 
 def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=None):
@@ -711,6 +725,7 @@ def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=N
     lda, ldb = _output("out[0]", da, rows, n, dh.dtype, index), _output("out[1]", db, rows, n, dh.dtype, index)
     _run("bakron_gated_act_grad", dh.data_ptr(), lddh, pa, pb, rows, _TYPES[dh.dtype], n, kind, cp, da.data_ptr(), lda,
          db.data_ptr(), ldb, s)
+    _written(da, db)
     return da, db
 
 

@@ -227,6 +227,14 @@ def _made(stream, make):
     return results
 
 
+def _written(*tensors):
+    """Given outputs count as changed in place, as torch's own do: autograd then refuses
+    a backward pass that would read what was saved there before."""
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 class _Calls(dict):
     """The library's functions by name (an attribute of it is looked up anew
     each time)."""
@@ -262,7 +270,8 @@ def _linear(call, size, name, x, w, out, ws, stream):
             raise ValueError(f"out cannot be given where {name} requires a gradient")
         both = (q4_linear, q4_linear_grad) if name == "x" else (q4_linear_grad, q4_linear)
         return _Differentiable.apply(x, w, *both, ws, stream)
-    if out is None:
+    given = out is not None
+    if not given:
         out = x.new_empty((T, out_cols)) if stream is None else _made(stream, lambda: (x.new_empty((T, out_cols)),))[0]
         ldo = out_cols
     else:
@@ -277,6 +286,8 @@ def _linear(call, size, name, x, w, out, ws, stream):
     rc = _calls[call](x.data_ptr(), ldx, T, _TYPES[x.dtype], data.data_ptr(), w.m, w.n, w._group, out.data_ptr(), ldo, wp, wn, s)
     if rc:
         _check(rc, call)
+    if given:
+        _written(out)
     return out
 
 
@@ -374,4 +385,5 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
                       weights.data_ptr(), wp, wn, s)
     if rc:
         _check(rc, call)
+    _written(y, ids, weights)
     return out
