@@ -90,3 +90,37 @@ def test_a_choice_written_over_before_its_backward_pass_is_refused():
         B.moe_route(first, k, out=r, **kw)
         got, = torch.autograd.grad(B.moe_gather(x, r["place"]), x, dxs)
         assert torch.equal(got, want)
+
+
+def test_outputs_that_require_a_gradient_are_refused(monkeypatch):
+    from test_moe_binding import Calls, checkpoint, on
+    from test_q4_binding import Calls as LinearCalls, layer
+    calls, linear = Calls(monkeypatch), LinearCalls(monkeypatch)
+    T, E, k, n, m = 3, 8, 2, 128, 64
+    place, p = on(0, T, k, dtype=I32), on(0, T, k, dtype=F32)
+    x, ys, dm, w, w1 = on(0, T, n), on(0, T * k, n), on(0, T * k, m), layer(0, m, n, E), layer(0, m, n)
+    offsets, ws = on(0, E + 1, dtype=I32), on(0, 1 << 20, dtype=torch.uint8)
+    ck = checkpoint(0, T * k, n)
+
+    def five(weights):
+        return {"ids": on(0, T, k, dtype=I32), "weights": weights, "place": place, "order": on(0, T * k, dtype=I32), "offsets": offsets}
+    for shape, dtype, call in (
+            ((T, k), F32, lambda o: B.moe_route(on(0, T, E), k, out=five(o), ws=ws)),
+            ((T, E), BF16, lambda o: B.moe_route_grad(p, p, place, E, out=o)),
+            ((T * k, n), BF16, lambda o: B.moe_gather(x, place, out=o)), ((T, n), BF16, lambda o: B.moe_combine(ys, place, p, out=o)),
+            ((T * k, n), BF16, lambda o: B.moe_combine_grad(x, ys, place, p, out={"dys": o, "dweights": on(0, T, k, dtype=F32)})),
+            ((T, k), F32, lambda o: B.moe_combine_grad(x, ys, place, p, out={"dys": on(0, T * k, n), "dweights": o})),
+            ((T * k, m), BF16, lambda o: B.q4_experts(ys, w, offsets, out=o, ws=ws)),
+            ((T * k, n), BF16, lambda o: B.q4_experts_grad(dm, w, offsets, out=o, ws=ws)),
+            ((T * k, n), BF16, lambda o: B.ck8_unpack(ck, out=o)), ((T * k, n), BF16, lambda o: B.gated_act(ys, ys, out=o)),
+            ((T * k, n), BF16, lambda o: B.gated_act_grad(ys, ck, ck, out=(o, on(0, T * k, n)))),
+            ((T * k, n), BF16, lambda o: B.gated_act_grad(ys, ck, ck, out=(on(0, T * k, n), o))),
+            ((T, m), BF16, lambda o: B.q4_linear(x, w1, out=o)),
+            ((T, n), BF16, lambda o: B.q4_moe(x, on(0, E, n), w, w, layer(0, n, m, E), k, ws=ws, out={"y": o, "ids": place, "weights": p}))):
+        out = on(0, *shape, dtype=dtype).requires_grad_()
+        with pytest.raises(ValueError, match="out must not require a gradient"):
+            call(out)
+        assert not calls.made and not linear.made
+        with torch.no_grad():
+            call(out)
+        calls.made.clear(), linear.made.clear()

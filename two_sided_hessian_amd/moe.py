@@ -24,7 +24,8 @@ import torch
 
 from . import _binding as _b
 from . import q4 as _q
-from .q4 import Q4Weight, _calls, _check, _device, _grad_on, _made, _on, _one_device, _raw_stream, _rows, _written
+from .q4 import Q4Weight, _calls, _check, _device, _grad_on, _made, _on, _one_device, _plain_outputs, _raw_stream, _rows, \
+    _written
 
 BAKRON_MOE_F32 = 2
 BAKRON_MOE_SILU = 0
@@ -263,6 +264,7 @@ def moe_route(logits, top_k, *, out=None, ws=None, stream=None):
         out = dict(zip(_ROUTE, _made(stream, lambda: _route_results(logits, k))))
     at = [_flat(f"out['{name}']", out[name], torch.float32 if name == "weights" else i32,
                 (T * k,) if name == "order" else (E + 1,) if name == "offsets" else (T, k), index) for name in _ROUTE]
+    _plain_outputs(out["weights"])
     ws = _space(ws, moe_route_workspace_bytes(T, E, k), logits.device, index, stream)
     wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     _run("bakron_moe_route", logits.data_ptr(), ld, T, _TYPES3[logits.dtype], E, k, *at, wp, wn, s)
@@ -296,6 +298,7 @@ def moe_route_grad(dweights, weights, ids, experts, *, dtype=torch.float32, out=
     ld = _matrix("out", out, E)
     if out.shape[0] != T or out.get_device() != index:
         raise ValueError(f"out must be a ({T}, {E}) tensor on cuda:{index}")
+    _plain_outputs(out)
     _run("bakron_moe_route_grad", *at, T, E, k, out.data_ptr(), ld, _TYPES3[out.dtype], s)
     _written(out)
     return out
@@ -348,6 +351,7 @@ def moe_gather(x, place, *, out=None, stream=None):
     if out is None:
         out = _made(stream, lambda: (x.new_empty((T * k, n)),))[0]
     ldo = _output("out", out, out.shape[0] if isinstance(out, torch.Tensor) and out.dim() else 0, n, x.dtype, index)
+    _plain_outputs(out)
     _run("bakron_moe_gather", x.data_ptr(), ldx, T, _TYPES[x.dtype], n, k, at, out.data_ptr(), ldo, out.shape[0], s)
     _written(out)
     return out
@@ -423,6 +427,7 @@ def moe_combine(ys, place, weights=None, *, out=None, stream=None):
         out, ldo = _made(stream, lambda: (ys.new_empty((T, n)),))[0], n
     else:
         ldo = _output("out", out, T, n, ys.dtype, index)
+    _plain_outputs(out)
     _run("bakron_moe_combine", ys.data_ptr(), ldys, rows, _TYPES[ys.dtype], n, k, at, wp, T, out.data_ptr(), ldo, s)
     _written(out)
     return out
@@ -453,6 +458,7 @@ def moe_combine_grad(dy, ys, place, weights, *, out=None, stream=None):
         out = {"dys": dys, "dweights": dw}
     dys = out["dys"]
     ldo, dw = _output("out['dys']", dys, rows, n, ys.dtype, index), _flat("out['dweights']", out["dweights"], torch.float32, (T, k), index)
+    _plain_outputs(dys, out["dweights"])
     _run("bakron_moe_combine_grad", dy.data_ptr(), lddy, ys.data_ptr(), ldys, rows, _TYPES[ys.dtype], n, k, at, wp, T,
          dys.data_ptr(), ldo, dw, s)
     _written(out["dys"], out["dweights"])
@@ -508,6 +514,7 @@ def _experts(call, size, name, x, w, offsets, out, ws, stream):
         out, ldo = _made(stream, lambda: (x.new_empty((R, out_cols)),))[0], out_cols
     else:
         ldo = _output("out", out, R, out_cols, x.dtype, index)
+    _plain_outputs(out)
     ws = _space(ws, size(R, w), x.device, index, stream)
     wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
     _run(call, x.data_ptr(), ldx, R, _TYPES[x.dtype], data.data_ptr(), w.count, w.m, w.n, w._group, at, out.data_ptr(), ldo,
@@ -624,6 +631,7 @@ def ck8_unpack(ck, *, dtype=None, out=None, stream=None):
     ld = _matrix("out", out, ck.cols)
     if out.shape[0] != ck.rows or out.get_device() != index:
         raise ValueError(f"out must be a ({ck.rows}, {ck.cols}) tensor on cuda:{index}")
+    _plain_outputs(out)
     _run("bakron_ck8_unpack", at, ck.rows, ck.cols, _TYPES3[out.dtype], out.data_ptr(), ld, s)
     _written(out)
     return out
@@ -693,6 +701,7 @@ def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, strea
             checkpoint = [Checkpoint8(data, rows, n, a.dtype) for data in
                           _made(stream, lambda: [Checkpoint8.empty(rows, n, a.dtype, a.device).data for _ in range(2)])]
         ca, cb = (_checkpoint("checkpoint", c, rows, n, a.dtype, index) for c in checkpoint)
+    _plain_outputs(out)
     _run("bakron_gated_act", a.data_ptr(), lda, b.data_ptr(), ldb, rows, _TYPES[a.dtype], n, kind, cp, out.data_ptr(), ldo,
          ca, cb, s)
     if checkpoint is False:
@@ -723,6 +732,7 @@ def gated_act_grad(dh, ck_a, ck_b, *, act="silu", count=None, out=None, stream=N
         out = tuple(_made(stream, lambda: (dh.new_empty((rows, n)), dh.new_empty((rows, n)))))
     da, db = out
     lda, ldb = _output("out[0]", da, rows, n, dh.dtype, index), _output("out[1]", db, rows, n, dh.dtype, index)
+    _plain_outputs(da, db)
     _run("bakron_gated_act_grad", dh.data_ptr(), lddh, pa, pb, rows, _TYPES[dh.dtype], n, kind, cp, da.data_ptr(), lda,
          db.data_ptr(), ldb, s)
     _written(da, db)

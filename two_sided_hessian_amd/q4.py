@@ -227,6 +227,12 @@ def _made(stream, make):
     return results
 
 
+def _plain_outputs(*tensors):
+    """Given outputs that require a gradient would keep the one of what they held before."""
+    if _grad_on() and any(t.requires_grad for t in tensors):
+        raise ValueError("out must not require a gradient")
+
+
 def _written(*tensors):
     """Given outputs count as changed in place, as torch's own do: autograd then refuses
     a backward pass that would read what was saved there before."""
@@ -278,6 +284,7 @@ def _linear(call, size, name, x, w, out, ws, stream):
         ldo = _rows("out", out, out_cols, x.dtype)
         if out.shape[0] != T or out.get_device() != index:
             raise ValueError(f"out must be a ({T}, {out_cols}) tensor on {x.device}")
+        _plain_outputs(out)
     if ws is None:
         ws = _workspace(size(T, w), x.device, stream)
     elif ws.get_device() != index or not ws.is_contiguous():
@@ -374,6 +381,7 @@ def q4_moe(x, router, w_gate, w_up, w_down, top_k, *, out=None, ws=None, stream=
         _b._check_dev("out['ids']", ids, torch.int32, (T, top_k))
         _b._check_dev("out['weights']", weights, torch.float32, (T, top_k))
         _one_device(index, None, **{"out['y']": y, "out['ids']": ids, "out['weights']": weights})
+        _plain_outputs(y, weights)
     if ws is None:
         ws = _workspace(q4_moe_workspace_bytes(T, w_gate, top_k), x.device, stream)
     elif ws.get_device() != index or not ws.is_contiguous():
