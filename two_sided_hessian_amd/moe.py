@@ -190,6 +190,14 @@ class _Refusing(torch.autograd.Function):
         raise RuntimeError(f"{ctx.name} has no second derivative")
 
 
+def _plainly(back, *args):
+    """A backward pass whose calls are not recorded in a kept graph."""
+    if not _grad_on():
+        return back(*args)
+    with torch.no_grad():
+        return back(*args)
+
+
 def _once(name, gradients, *causes):
     """The gradients that a backward pass of ``name`` made, None among them.  In a kept
     graph (create_graph) they depend on ``causes``, and a derivative that reaches them
@@ -231,8 +239,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def backward(ctx, _ids, dweights, *_):
         weights, ids = ctx.saved_tensors
-        with torch.no_grad():
-            dlogits = moe_route_grad(dweights.contiguous(), weights, ids, ctx.experts, dtype=ctx.dtype)
+        dlogits = _plainly(lambda: moe_route_grad(dweights.contiguous(), weights, ids, ctx.experts, dtype=ctx.dtype))
         return _once("moe_route", (dlogits, None, None, None), dweights, weights)
 
 
@@ -396,9 +403,11 @@ class _Spread(torch.autograd.Function):
 def _combine_back(g, ys, place, weights):
     if g.requires_grad and _grad_on():
         raise RuntimeError("moe_combine with weights has no second derivative")
-    with torch.no_grad():
+
+    def back():
         out = {"dys": torch.zeros(ys.shape, dtype=ys.dtype, device=ys.device), "dweights": torch.empty_like(weights)}
-        r = moe_combine_grad(g, ys, place, weights, out=out)
+        return moe_combine_grad(g, ys, place, weights, out=out)
+    r = _plainly(back)
     return _once("moe_combine with weights", (r["dys"], None, r["dweights"]), ys, weights)
 
 
@@ -652,17 +661,19 @@ class _Gated(torch.autograd.Function):
         lead = h.new_empty(0)
         ctx.act, ctx.like = act, (ca.rows, ca.cols, ca.dtype)
         ctx.save_for_backward(ca.data, cb.data, count, lead)
+        ctx.set_materialize_grads(False)   # (lead has no gradient)
         return h, lead
 
     @staticmethod
     def backward(ctx, dh, _):
         ca, cb, count, lead = ctx.saved_tensors
-        with torch.no_grad():
+
+        def back():
             g = dh.contiguous()
             out = None if count is None else (torch.zeros_like(g), torch.zeros_like(g))
-            da, db = gated_act_grad(g, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
-                                    count=count, out=out)
-        return _once("gated_act", (da, db, None, None, None), dh, lead)
+            return gated_act_grad(g, Checkpoint8(ca, *ctx.like), Checkpoint8(cb, *ctx.like), act=ctx.act,
+                                  count=count, out=out)
+        return _once("gated_act", (*_plainly(back), None, None, None), dh, lead)
 
 
 def gated_act(a, b, *, act="silu", checkpoint=False, count=None, out=None, stream=None):
@@ -775,18 +786,17 @@ class _Layer(torch.autograd.Function):
         ctx.logits = logits.shape[1], logits.dtype
         lead = y.new_empty(0)
         ctx.save_for_backward(r["ids"], r["weights"], r["place"], r["offsets"], ys, ca.data, cb.data, lead)
+        ctx.set_materialize_grads(False)   # (lead has no gradient)
         return y, lead
 
     @staticmethod
     def backward(ctx, dy, _):
-        with torch.no_grad():
-            gradients = _layer_back(ctx, dy)
-        return _once("q4_moe_layer", gradients + 5 * (None,), dy, ctx.saved_tensors[-1])
+        *saved, lead = ctx.saved_tensors
+        return _once("q4_moe_layer", _plainly(_layer_back, ctx, dy, *saved) + 5 * (None,), dy, lead)
 
 
-def _layer_back(ctx, dy):
+def _layer_back(ctx, dy, ids, weights, place, offsets, ys, ca, cb):
     """The gradients of x and of the logits, None where one is not needed."""
-    ids, weights, place, offsets, ys, ca, cb, _ = ctx.saved_tensors
     w_gate, w_up, w_down = ctx.layers
     (R, n), f, e = ys.shape, w_gate.m, ys.new_empty
     back = moe_combine_grad(dy.contiguous(), ys, place, weights,

@@ -227,18 +227,23 @@ def _made(stream, make):
     return results
 
 
+_increment = torch._C._increment_version
+
+
 def _plain_outputs(*tensors):
     """Given outputs that require a gradient would keep the one of what they held before."""
-    if _grad_on() and any(t.requires_grad for t in tensors):
-        raise ValueError("out must not require a gradient")
+    for t in tensors:
+        if t.requires_grad and _grad_on():
+            raise ValueError("out must not require a gradient")
 
 
 def _written(*tensors):
     """Given outputs count as changed in place, as torch's own do: autograd then refuses
     a backward pass that would read what was saved there before."""
-    for t in tensors:
-        if not t.is_inference():
-            torch.autograd.graph.increment_version(t)
+    try:
+        _increment(tensors)
+    except RuntimeError:                     # (inference tensors, which have no version, among them)
+        _increment([t for t in tensors if not t.is_inference()])
 
 
 class _Calls(dict):
