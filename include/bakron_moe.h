@@ -55,6 +55,7 @@ extern "C" {
 /* Activations of bakron_gated_act. */
 #define BAKRON_MOE_SILU 0  /* act(v) = v sigmoid(v) */
 #define BAKRON_MOE_GELU 1  /* act(v) = v sigmoid(2 sqrt(2 / pi) (v + 0.044715 v^3)), the tanh form */
+/* (a sigmoid below 2^-126, of arguments under -87.3, counts as 0) */
 
 #define BAKRON_MOE_MAX_ROWS 16777216   /* tokens, and tokens top_k, of one call */
 #define BAKRON_MOE_MAX_TOP_K 16        /* experts chosen per token */
@@ -149,7 +150,9 @@ size_t bakron_q4_experts_grad_workspace_bytes(int64_t rows, int64_t experts, int
  *                  may hold anything.
  * rows       [in]  0 <= rows <= BAKRON_MOE_MAX_ROWS: the room that x and y
  *                  have.  The kernel and its tiles are chosen for rows / experts
- *                  rows per expert; any distribution is served.
+ *                  rows per expert; any distribution is served, but at the
+ *                  price of that form (few rows on average: an expert's
+ *                  codes are read again for every 32 of its rows).
  * packed, experts, m, n, group_size [in] a stack packed by bakron_q4_pack,
  *                  1 <= experts <= BAKRON_MOE_MAX_EXPERTS.
  * offsets    [in]  experts + 1 int32 on the device.
@@ -163,8 +166,10 @@ int bakron_q4_experts(const void* x, int64_t ldx, int64_t rows, int32_t type, co
 /*
  * bakron_q4_experts_grad -- the gradient of bakron_q4_experts with respect to
  * its rows, dx[p] = dy[p] W_e.  Experts with many rows: each weight is rounded
- * once to dy's type, as bakron_q4_linear_grad does it.  With few: dy times a
- * step is kept in two bfloat16 terms (2^-16 relative) and the codes are exact.
+ * once to dy's type, as bakron_q4_linear_grad does it, so that a result is off by
+ * two roundings of its type instead of one (1.41 times in the mean square).  With
+ * few: dy times a step is rounded to 16 bits (2^-16 relative), and the codes are
+ * exact.  Which of the two it is goes by rows, experts and the layer's size.
  *
  * dy         [in]  rows x m; dx [out] rows x n.  m == 0 writes zeros.
  *                  Everything else as in bakron_q4_experts.

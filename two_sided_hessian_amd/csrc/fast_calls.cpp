@@ -1,8 +1,8 @@
 // fast_calls.cpp -- the calls of moe.py whose outputs are given, without Python
 // between their arguments and the library.
 //
-// One decoding token's calls take 3 us on the GPU; checking their arguments from
-// Python took 3 us more on the host, and passing them through ctypes 1.5.  Each
+// One decoding token's calls take 3 us on the GPU.  Without the launch, a call through
+// moe.py's checks and ctypes takes 4 us on the host, and 0.25 through here.  Each
 // function here looks at the same things as its namesake in moe.py and enqueues
 // the call where all of them are in order (True, or the exception of a launch that
 // failed); in any other case it does nothing (False), and moe.py takes the call, raises

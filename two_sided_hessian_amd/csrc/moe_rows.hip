@@ -161,8 +161,9 @@ static void combine_grad_enqueue(const void* dy, int64_t lddy, const void* ys, i
                                  float* dweights, hipStream_t s)
 {
     // Four waves share a token wherever a wave's 512 columns do not take a row whole:
-    // what is in flight lies together (8192 tokens of 2 x 4096: 65 us, and 79 with a wave
-    // per token).
+    // what is in flight lies together (calls of 8192 tokens of 2 x 4096: 62 us, and 76 with a
+    // wave per token; 6 x 2048: 85 and 99; narrow rows would rather have the wave, 2 x 1024: 16
+    // and 14, 2 x 640: 14 and 10).
     const bool wide = n > 512;
     enqueue(wide ? k_moe_combine_grad<X, K, 4> : k_moe_combine_grad<X, K, 1>,
             dim3((unsigned)std::min(kUnitBlocks, wide ? T : ceil_div(T, 4))), dim3(256), s,

@@ -10,11 +10,12 @@
 // of every expert, and takes its own by a prefix sum over the 64 lanes; what is
 // past the last block ends there.  A block never holds two experts' rows.
 //
-//   * few rows per expert (decoding): codes are what is read, and HBM bounds it.
+//   * few rows per expert (decoding): codes are what is read, and HBM bounds the product.
 //     k_q4_experts_few has blocks of up to 32 rows and row tiles of W over workgroups: 16
 //     tokens, 6 of 64 experts of 1024 x 2048 in groups of 64: 13.0 us a call, 5.2 TB/s of
 //     what has to move, a large copy's rate.  k_q4_experts_grad_few has blocks of 32 rows
-//     (16) and 128 columns: 16 tokens, 2 of 8 of 14336 x 4096: 55 us (floor 50); tiles of 64
+//     (16) and 128 columns, and vector instructions bound it: 16 tokens, 2 of 8 of 14336 x 4096:
+//     53 us with seven experts in use, 75 - 83 with all eight (floors 44 and 51); tiles of 64
 //     rows took 117.  Blocks of 64 rows, two waves a SIMD: 92 us for 103 at 64 tokens, but
 //     162 for 139 at 128 and 63 for 54 at 512 tokens, 6 of 64 of 2048 x 1024.
 //   * many: k_q4_experts and k_q4_experts_grad, tiles of 64 .. 256 rows, MFMAs.  8192
@@ -333,9 +334,11 @@ __global__ __launch_bounds__(256) void k_q4_experts_zero(uint16_t* __restrict__ 
 // the columns of a pair and are joined in wave order.
 
 constexpr int kFewRows = 32;   // of a block
-// Up to so many rows per expert on average (6 of 64 experts of 1024 x 2048, 39 rows each:
-// 36.6 us, and 43.6 in tiles of 64 rows; 48: 40.8 and 44.8; 60: 49.0 and 49.7; 2 of 8 of
-// 14336 x 4096, 50 each: 117 and 102).
+// Up to so many rows per expert on average.  One number for layers of every size is a
+// compromise: an expert of more than 32 rows has two blocks, which read its codes twice.
+// 2 of 8 of 14336 x 4096, 33 rows each: 100 us, and 106 in tiles of 64 rows; 40: 108 and
+// 105; 48: 121 and 106; of 4096 x 4096, 48: 38 and 48.  6 of 64 of 1024 x 2048, 38 uneven
+// ones: 52 and 47, 39 nearly even ones: 37 and 44, 48: 41 and 45.
 constexpr int kFewMean = 48;
 constexpr int kFewLds = 8 * std::max(few_lds(kFewRows / 4), 16 * 64 * 4);   // staged rows, then the joining sums
 

@@ -23,9 +23,12 @@
 // in which the eight dwords of a lane are 256 bytes apart and the 64 lanes' lie in
 // different banks.  The LDS is a wave's own: no barrier is involved.
 //
-// HBM bounds it up to some 16 rows of dy (16 tokens, 2 of 8 experts of 14336 x 4096: 55 us,
-// 4.7 TB/s), then the vector instructions that split a: 64 tokens, 106 us.  A weight formed
-// for every code, as with many rows, took 117 us of 16 tokens.
+// Vector instructions bound it (0.82 of the busy cycles), those that expand codes for the
+// fewest rows and those that split a for more; HBM is next.  Groups of 128, 2 of 8 experts
+// of 14336 x 4096: 16 tokens 53 us while at most seven experts have rows (4.4 TB/s of codes
+// and grids, partly from the Infinity Cache), 75 - 83 where all eight have (3.2 - 3.5); 64 tokens
+// 82 - 88 with 16 rows each, 109 with 4 to 30.  A weight formed for every code, as with many
+// rows, took 117 us of 16 tokens.
 #pragma once
 
 #include "moe.hpp"

@@ -3,8 +3,9 @@
 order, rows there and back, the experts' products, their inner activation with
 8-bit checkpoints, and the whole layer.
 
-Arguments are checked as in q4.py: no tensor is looked into, every arithmetic
-step runs in the library's HIP kernels, and there is no fallback.  Calls whose
+Arguments are checked as in q4.py: no tensor is looked into, the calls' arithmetic runs
+in the library's HIP kernels, and there is no fallback (q4_moe_layer's backward pass makes
+a second set of places with three of torch's operators).  Calls whose
 outputs are given (decoding steps, captured or not) are tried by _fast first,
 which checks and enqueues them in native code (csrc/fast_calls.cpp) and leaves
 everything else, refusals among it, to the code here.
@@ -14,7 +15,9 @@ Given outputs count as changed in place, as torch's own do.
 Autograd: moe_route (weights), moe_gather, moe_combine, q4_experts, gated_act
 and q4_moe_layer take part in it where an input requires a gradient and ``out``
 is not given.  Gradients with respect to sorted rows that no choice has are
-zeros.
+zeros.  moe_gather, q4_experts and moe_combine without weights are linear and can be
+differentiated again; the others have first derivatives only, and a second one that
+reaches them raises.  There are no derivatives in forward mode: dual tensors are refused.
 """
 from __future__ import annotations
 
@@ -62,7 +65,7 @@ _ACTS = {"silu": BAKRON_MOE_SILU, "gelu": BAKRON_MOE_GELU}
 
 try:
     from . import _fast
-except ImportError:                      # not built: the same calls through ctypes, 3 us more each on the host
+except ImportError:                      # not built: the same calls through ctypes, 4 us each on the host
     _fast = None
 
 

@@ -43,7 +43,8 @@ _TYPES = {torch.bfloat16: BAKRON_Q4_BF16, torch.float16: BAKRON_Q4_FP16}
 class Q4Weight:
     """One layer (count 1) or a stack of ``count`` layers of m x n in the
     packed layout, with group_size columns per grid (None: one grid per row).
-    ``data`` is the device buffer (uint8) that holds it.  ``w[e]`` is layer e of
+    ``data`` is the device buffer (uint8) that holds it, as q4_pack makes it (its size is
+    not checked again by every call).  ``w[e]`` is layer e of
     a stack alone, on the same memory: what q4_linear takes (q4_experts takes the
     stack as it is)."""
 
