@@ -131,3 +131,24 @@ def test_calls_without_a_gradient_refuse_tensors_that_require_one():
                     call(v, given())
                 with torch.no_grad():
                     call(v, given())
+
+
+class Cut(torch.autograd.Function):
+    """Its input as it is, and no gradient for it."""
+
+    @staticmethod
+    def forward(ctx, x):
+        return x.clone()
+
+    @staticmethod
+    def backward(ctx, g):
+        return None
+
+
+def test_a_result_without_a_gradient():
+    for name, call, plain, _ in single_calls():
+        inputs = [v.clone().requires_grad_() for v in plain]
+        other = sum(v.float().square().sum() for v in inputs)
+        (Cut.apply(call(*inputs)).sum() + other).backward()
+        for x in inputs:
+            assert torch.equal(x.grad, 2 * x.detach()), name

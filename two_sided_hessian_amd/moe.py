@@ -670,6 +670,8 @@ class _Gated(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dh, _):
         ca, cb, count, lead = ctx.saved_tensors
+        if dh is None:
+            return 5 * (None,)
 
         def back():
             g = dh.contiguous()
@@ -795,6 +797,8 @@ class _Layer(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, _):
         *saved, lead = ctx.saved_tensors
+        if dy is None:
+            return 7 * (None,)
         return _once("q4_moe_layer", _plainly(_layer_back, ctx, dy, *saved) + 5 * (None,), dy, lead)
 
 
