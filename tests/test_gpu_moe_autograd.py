@@ -152,3 +152,25 @@ def test_a_result_without_a_gradient():
         (Cut.apply(call(*inputs)).sum() + other).backward()
         for x in inputs:
             assert torch.equal(x.grad, 2 * x.detach()), name
+
+
+def test_saved_tensors_kept_elsewhere_or_made_again():
+    """Under activation checkpointing, with saved tensors moved to the host, and for a graph
+    that is gone through twice."""
+    from torch.utils.checkpoint import checkpoint
+    for name, call, plain, want in single_calls():
+        def gradients(run, times=1):
+            inputs = [v.clone().requires_grad_() for v in plain]
+            loss = run(*inputs).sum()
+            for i in range(times):
+                got = torch.autograd.grad(loss, inputs, retain_graph=i + 1 < times)
+                for a, b in zip(got, want):
+                    assert torch.equal(a, b), name
+        gradients(lambda *v: checkpoint(call, *v, use_reentrant=False))
+        gradients(call, 2)
+        with torch.autograd.graph.save_on_cpu():
+            gradients(call)
+            inputs = [v.clone().requires_grad_() for v in plain]
+            got = torch.autograd.grad(call(*inputs).sum(), inputs, create_graph=True)
+        with pytest.raises(RuntimeError, match="no second derivative"):
+            torch.autograd.grad(got[0].float().square().sum(), inputs[0])

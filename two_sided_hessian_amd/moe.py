@@ -341,7 +341,7 @@ def moe_gather(x, place, *, out=None, stream=None):
     x[t].  x: tokens x columns in bfloat16 or float16; place: int32 tokens x top_k
     (moe_route).  Returns tokens * top_k x columns; ``out``: where to write it (any
     number of rows).  Rows that no choice has stay as they are (in a new result:
-    undefined).  Autograd: its gradient is moe_combine without weights."""
+    undefined); a row that two choices share ends as some mixture of theirs.  Autograd: its gradient is moe_combine without weights."""
     if out is not None and stream is None and _gather_at(x, place, out):
         return out
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
@@ -419,7 +419,9 @@ def moe_combine(ys, place, weights=None, *, out=None, stream=None):
     weights[t, j] ys[place[t, j]] (weights None: all 1; a choice without a row adds
     nothing).  ys: rows x columns in bfloat16 or float16; weights: float32 tokens x
     top_k.  ``out``: where to write y.  Autograd: the gradients are those of
-    moe_combine_grad (without weights: moe_gather)."""
+    moe_combine_grad (without weights: moe_gather), for places that name each row once at
+    most, as moe_route's do (of a row that two choices share, the gradient ends as some
+    mixture of theirs and not as their sum)."""
     if out is not None and stream is None and _combine_at(ys, place, weights, out):
         return out
     if not isinstance(ys, torch.Tensor) or ys.dim() != 2:
