@@ -341,7 +341,8 @@ def moe_gather(x, place, *, out=None, stream=None):
     x[t].  x: tokens x columns in bfloat16 or float16; place: int32 tokens x top_k
     (moe_route).  Returns tokens * top_k x columns; ``out``: where to write it (any
     number of rows).  Rows that no choice has stay as they are (in a new result:
-    undefined); a row that two choices share ends as some mixture of theirs.  Autograd: its gradient is moe_combine without weights."""
+    undefined); a row that two choices share ends as some mixture of theirs.  Autograd:
+    its gradient is moe_combine without weights."""
     if out is not None and stream is None and _gather_at(x, place, out):
         return out
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
